@@ -242,6 +242,105 @@ DPLR_API dplr_status dplr_gdp_forward(const dplr_desc* desc, const void* q, cons
                              void* workspace, size_t ws_bytes, void* stream);
 DPLR_API const char* dplr_gdp_path(const dplr_desc* desc);
 
+/* ---------------------------------------------------------------------------------------------------------------
+ * Linear attention with one decay per head (no low-rank term): per batch b and value head h,
+ *
+ *     S_t = exp(g_t) S_{t-1} + k_t v_t^T,        o_t = S_t^T q_t
+ *
+ * the constant-decay and scalar-gate members of the decay taxonomy (HDLA page, research background: none, constant,
+ * diagonal; "Log-Linear Attention" page, framework: O = (Q K^T . M) V with a 1-semiseparable M). Query/key heads may be
+ * shared: value head h reads query/key head h / (H / Hq). The readout uses the state after token t's update; there
+ * is no 1/sqrt(dk) factor.
+ *
+ * Tensors are given with their element strides along batch, head and token; the feature axis is contiguous. Strides of
+ * axes of length 1 are not looked at. q, k [B,Hq,T,dk]; v, o [B,H,T,dv], all of desc->in_dtype: o has the inputs' type.
+ * Their data must be 16-byte aligned and their strides positive multiples of 16 bytes. Log-gates g <= 0 are fp32:
+ * [B,H,T] with any non-negative strides, or with desc->per_head [H], contiguous (the strides are not looked at); -inf
+ * forgets the state. States are fp32, contiguous [dk][dv] per (batch, head) or (slot, head), 16-byte aligned.
+ * dk, dv in {32, 64, 128}; H a multiple of Hq; B*H < 2^24; T >= 0 with B*H*T < 2^31. Outputs must not overlap inputs;
+ * S_T may be S0. A non-finite value of a token reaches the outputs of the tokens after it and may reach those of the
+ * up to 127 tokens before it (the chunk that is computed together), never another batch entry, head or request.
+ * Results do not depend on timing (fixed orders of summation, no atomics on values). Workspaces are 256-byte aligned
+ * device memory of the caller, not shared by calls that overlap; the first 256 bytes hold a status word as described
+ * for dplr_la_workspace_size (zero it once; read it with dplr_la_read_status). Nothing is allocated. */
+typedef struct {
+    void* data;          /* first element; inputs are only read */
+    int64_t sb, sh, st;  /* element strides of batch, head, token */
+} dplr_hd_tensor;
+
+typedef struct {
+    int32_t in_dtype;         /* dplr_dtype of q, k, v, o */
+    int32_t B, H, Hq, T;      /* batch, value heads, query/key heads, tokens */
+    int32_t dk, dv;
+    int32_t per_head;         /* 1: one log-gate per head, [H]; 0: one per token, [B,H,T] */
+} dplr_hd_desc;
+
+/* DPLR_OK if the shape is supported. */
+DPLR_API dplr_status dplr_hd_check(const dplr_hd_desc* desc);
+
+/* The kernels a descriptor takes: "hd_tcgen05" (bf16, dk and dv in {64, 128}: tensor cores) or "hd_fp32" (everything
+ * else: fp32 on the CUDA cores), "" if it is invalid. */
+DPLR_API const char* dplr_hd_path(const dplr_hd_desc* desc);
+
+/* The prompt: o, and S_T (nullable) from S0 (nullable: zero). Few heads and a long sequence: the sequence is cut into
+ * segments whose states are formed first, in parallel, into the workspace. */
+DPLR_API size_t dplr_hd_workspace_size(const dplr_hd_desc* desc);
+DPLR_API dplr_status dplr_hd_forward(const dplr_hd_desc* desc, const dplr_hd_tensor* q, const dplr_hd_tensor* k,
+                                     const dplr_hd_tensor* v, const dplr_hd_tensor* decay, const float* S0,
+                                     const dplr_hd_tensor* o, float* S_T, void* workspace, size_t ws_bytes,
+                                     void* stream);
+
+/* The gradients of dplr_hd_forward's inputs given dO (in_dtype, like o) and dST (fp32, nullable: zero): dq, dk, dv of
+ * in_dtype with strides of their own; shared query/key heads get the sum over their value heads; ddecay fp32,
+ * contiguous [B,H,T] or with per_head [H] (summed over batch and tokens), nullable; dS0 fp32, nullable. */
+DPLR_API size_t dplr_hd_backward_workspace_size(const dplr_hd_desc* desc);
+DPLR_API dplr_status dplr_hd_backward(const dplr_hd_desc* desc, const dplr_hd_tensor* q, const dplr_hd_tensor* k,
+                                      const dplr_hd_tensor* v, const dplr_hd_tensor* decay, const float* S0,
+                                      const dplr_hd_tensor* dO, const float* dST, const dplr_hd_tensor* dq,
+                                      const dplr_hd_tensor* dk, const dplr_hd_tensor* dv, float* ddecay, float* dS0,
+                                      void* workspace, size_t ws_bytes, void* stream);
+
+/* Tables of a ragged batch of R requests, built on the GPU from their lengths (one launch; capturable, so that a graph
+ * replays with other lengths). Inputs, int32 on the device: lengths [R] (tokens of this step, >= 0), slots [R] (where
+ * each request's state lives, 0 <= slot < n_slots, different for requests that have tokens; not looked at for those
+ * that have none), context [R] (tokens that the state already holds, >= 0). Request r's tokens are the rows starts[r] ..
+ * starts[r+1] - 1 of the packed tensors, which have `capacity` rows. Outputs, int32:
+ *   starts       [R+1]
+ *   blocks       [capacity / block + R][4]: (request, first row, rows, index within the request) of each block of up to
+ *                `block` tokens, request by request; -1 behind the last
+ *   block_starts [R+1]: each request's first block
+ *   token_slot   [capacity]: each row's slot; -1 behind the last token
+ *   token_pos    [capacity]: each row's position in its request, context included; -1 behind the last token
+ *   status       [1]: DPLR_OK, or DPLR_ERR_INVALID_ARG for a negative length or context, a slot out of range or given to
+ *                two requests with tokens, positions beyond 2^31 - 1 or more than `capacity` tokens; the tables are then
+ *                those of a batch without tokens.
+ * 1 <= R <= 8192, 0 <= capacity < 2^30, block a multiple of 32, 1 <= n_slots <= 2^20. */
+DPLR_API dplr_status dplr_hd_plan(int32_t R, int32_t capacity, int32_t block, int32_t n_slots, const int32_t* lengths,
+                                  const int32_t* slots, const int32_t* context, int32_t* starts, int32_t* blocks,
+                                  int32_t* block_starts, int32_t* token_slot, int32_t* token_pos, int32_t* status,
+                                  void* stream);
+
+/* The prompts of a ragged batch, on a pool of states S [n_slots][H][dk][dv] updated in place: a request with context > 0
+ * starts from its slot's state, one with context 0 from zero; requests without tokens leave theirs as it was. desc: B = 1
+ * and T = the capacity; q, k, v, o, decay have one row per token (the batch stride is not looked at). The tables are
+ * those of dplr_hd_plan with the same R, T and `block`; context and slots the arrays given to it. Rows of o behind the
+ * last token are left as they were. */
+DPLR_API size_t dplr_hd_packed_workspace_size(const dplr_hd_desc* desc, int32_t R, int32_t block);
+DPLR_API dplr_status dplr_hd_forward_packed(const dplr_hd_desc* desc, int32_t R, int32_t block, int32_t n_slots,
+                                            const int32_t* blocks, const int32_t* block_starts, const int32_t* slots,
+                                            const int32_t* context, const dplr_hd_tensor* q, const dplr_hd_tensor* k,
+                                            const dplr_hd_tensor* v, const dplr_hd_tensor* decay, float* S,
+                                            const dplr_hd_tensor* o, void* workspace, size_t ws_bytes, void* stream);
+
+/* One token for each of desc->B rows (desc->T = 1) on a pool of states S [n_slots][H][dk][dv], updated in place: row i
+ * works on the state in slots[i] (int32, on the device), or on none if slots[i] is -1: its o is then zero. Arithmetic
+ * in fp32. A row whose slot is out of range or that an earlier row has is treated as one without a state, and
+ * `status` (int32 on the device, nullable; never cleared here) gets DPLR_ERR_INVALID_ARG. No workspace. */
+DPLR_API dplr_status dplr_hd_decode_step(const dplr_hd_desc* desc, int32_t n_slots, const int32_t* slots,
+                                         const dplr_hd_tensor* q, const dplr_hd_tensor* k, const dplr_hd_tensor* v,
+                                         const dplr_hd_tensor* decay, float* S, const dplr_hd_tensor* o,
+                                         int32_t* status, void* stream);
+
 /* Name of the kernel path that dplr_la_forward runs for `desc` (no counterpart in the
  * paper; static storage): "gdn_fused_tcgen05" (GDN, bf16, dk = dv = 128: one fused
  * per-head kernel on the tensor cores), "hdla_tcgen05" (HDLA, bf16, dk = dv = 128: the

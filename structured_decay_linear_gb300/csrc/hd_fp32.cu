@@ -1,0 +1,318 @@
+// Linear attention with one decay per head in fp32 on the CUDA cores: every type and size, both directions of time,
+// dense and ragged batches (hd_internal.h has the operator). It runs what the tensor-core kernel does not take: fp32
+// inputs, and bf16 with a head size of 32.
+//
+// A CTA owns one segment of one (batch, head) and a block of up to 64 columns of the state, which it keeps in shared
+// memory, and walks the segment in chunks of 32 tokens (G: inclusive cumulative log-gates of the chunk):
+//   forward    P_rc = (x_r . y_c) e^{G_r - G_c}, c <= r;  o_r = P z + e^{G_r} R^T x_r;      R <- e^{G_n} R + sum e^{G_n - G_c} y_c z_c^T
+//   backward   P_rc = (x_r . y_c) e^{G_c - G_r}, c >= r;  o_r = P z + e^{G_n - G_r} R^T x_r;  R <- e^{G_n} R + sum e^{G_c} y_c z_c^T
+// Columns of the state evolve independently, so the column blocks share nothing but the product x y^T, which each
+// forms again. Exponents are differences of cumulative gates and never positive: nothing overflows for any gate.
+#include <cuda_bf16.h>
+
+#include "hd_internal.h"
+
+namespace dplr {
+namespace hd {
+namespace {
+
+constexpr int TH = 256;   // threads
+constexpr int C = 32;     // tokens of a chunk
+constexpr int LDP = C + 4;
+
+template <class T> struct Vec;
+template <> struct Vec<float> {
+    static constexpr int N = 4;
+    static __device__ __forceinline__ void load(const float* p, float* d) {
+        const float4 v = *reinterpret_cast<const float4*>(p);
+        d[0] = v.x; d[1] = v.y; d[2] = v.z; d[3] = v.w;
+    }
+};
+template <> struct Vec<__nv_bfloat16> {
+    static constexpr int N = 8;
+    static __device__ __forceinline__ void load(const __nv_bfloat16* p, float* d) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            d[2 * i] = __uint_as_float(u[i] << 16);
+            d[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+        }
+    }
+};
+
+__device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+
+// Rows t0 .. t0 + C - 1 of a row sequence (features c0 .. c0 + D - 1) as fp32 into shared memory; rows from n on are 0.
+template <class IT, int D, int LD>
+__device__ __forceinline__ void load_rows(float* dst, const View& v, int b, int h, long long t0, int n, int c0) {
+    constexpr int N = Vec<IT>::N, PER = D / N;
+    const IT* base = static_cast<const IT*>(v.p) + b * v.sb + (h / v.div) * v.sh + t0 * v.st + c0;
+    for (int i = threadIdx.x; i < C * PER; i += TH) {
+        const int r = i / PER, c = (i % PER) * N;
+        float d[N];
+        if (r < n) {
+            Vec<IT>::load(base + r * v.st + c, d);
+        } else {
+#pragma unroll
+            for (int e = 0; e < N; ++e) d[e] = 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < N; e += 4)
+            *reinterpret_cast<float4*>(dst + r * LD + c + e) = make_float4(d[e], d[e + 1], d[e + 2], d[e + 3]);
+    }
+}
+
+template <class IT>
+__device__ __forceinline__ void store4(void* p, long long at, const float (&v)[4], bool f32) {
+    if (f32 || sizeof(IT) == 4) {
+        *reinterpret_cast<float4*>(static_cast<float*>(p) + at) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+        __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), c = __floats2bfloat162_rn(v[2], v[3]);
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p) + at) =
+            make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&c));
+    }
+}
+
+template <class IT, int DX, int NZ>
+__device__ __forceinline__ void segment_pass(const Pass& p, const Geometry& geo, const Segment& sg, int zb, long long bh, float* sm) {
+    constexpr int LDX = DX + 4, LDZ = NZ + 4;
+    constexpr int CG = NZ / 4, RG = TH / CG;        // column groups of 4, row groups
+    constexpr int OR = C / RG, SR = DX / RG;        // rows of o and of the state per thread
+    float* X = sm;
+    float* Y = X + C * LDX;
+    float* Z = Y + C * LDX;
+    float* S = Z + C * LDZ;
+    float* P = S + DX * LDZ;
+    float* G = P + C * LDP;                         // [C] cumulative gates and [C] what their rounding left,
+    float* GL = G + C;                              // [C] weights of the update, [C] of the readout
+    float* W = GL + C;
+    float* CX = W + C;
+    float* tot = CX + C;                            // [1] the chunk's total
+    const int tid = threadIdx.x, cg = tid % CG, rg = tid / CG, c0 = 4 * cg, z0 = zb * NZ;
+    const bool rev = p.reverse;
+    const bool so = p.states_only;
+
+    // ---- the starting state
+    {
+        const float* src = nullptr;
+        if (!so) {
+            if (p.bound && !sg.alone) src = p.bound + (rev ? sg.entry + sg.step : sg.entry) * (long long)DX * p.DZ;
+            else if (p.ext_in && !sg.fresh) src = p.ext_in + sg.ext * (long long)DX * p.DZ;
+        }
+        for (int i = tid; i < DX * NZ; i += TH) {
+            // walk the state along its contiguous axis
+            const int r = p.siz == 1 ? i / NZ : i % DX, c = p.siz == 1 ? i % NZ : i / DX;
+            S[r * LDZ + c] = src ? src[r * p.six + (z0 + c) * p.siz] : 0.f;
+        }
+    }
+    float gsum = 0.f;
+    const float* gp = p.g + sg.b * p.gb + sg.h * p.gh;
+    const int nchunk = (sg.n + C - 1) / C;
+    for (int jj = 0; jj < nchunk; ++jj) {
+        const int j = rev ? nchunk - 1 - jj : jj;
+        const long long t0 = (long long)sg.t0 + j * C;
+        const int n = min(C, sg.n - j * C);
+        __syncthreads();
+        if (!so) load_rows<IT, DX, LDX>(X, p.x, sg.b, sg.h, t0, n, 0);
+        load_rows<IT, DX, LDX>(Y, p.y, sg.b, sg.h, t0, n, 0);
+        load_rows<IT, NZ, LDZ>(Z, p.z, sg.b, sg.h, t0, n, z0);
+        if (tid < 32) {
+            float g0 = tid < n ? gp[(t0 + tid) * p.gt] : 0.f;
+            g0 = g0 < kMinGate ? kMinGate : g0;
+            double g = g0;      // sums in 64 bits: after a gate of -100 those between later tokens still count
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const double y = __shfl_up_sync(0xffffffffu, g, off);
+                if (tid >= off) g += y;
+            }
+            const double gn = __shfl_sync(0xffffffffu, g, 31);
+            const float all = (float)gn, rest = (float)(gn - g);
+            G[tid] = (float)g;
+            GL[tid] = (float)(g - (double)(float)g);
+            W[tid] = __expf(rev ? (float)g : rest);
+            CX[tid] = __expf(rev ? rest : (float)g);
+            if (tid == 0) tot[0] = all;
+        }
+        __syncthreads();
+        const float all = tot[0];
+        gsum += all;
+        if (!so) {
+            // ---- P: rows r, r + 16 x columns c, c + 16
+            const int r = tid >> 4, c = tid & 15;
+            float a[2][2] = {};
+#pragma unroll 8
+            for (int i = 0; i < DX; i += 4) {
+                const float4 x0 = ld4(X + r * LDX + i), x1 = ld4(X + (r + 16) * LDX + i);
+                const float4 y0 = ld4(Y + c * LDX + i), y1 = ld4(Y + (c + 16) * LDX + i);
+                a[0][0] = fmaf(x0.x, y0.x, fmaf(x0.y, y0.y, fmaf(x0.z, y0.z, fmaf(x0.w, y0.w, a[0][0]))));
+                a[0][1] = fmaf(x0.x, y1.x, fmaf(x0.y, y1.y, fmaf(x0.z, y1.z, fmaf(x0.w, y1.w, a[0][1]))));
+                a[1][0] = fmaf(x1.x, y0.x, fmaf(x1.y, y0.y, fmaf(x1.z, y0.z, fmaf(x1.w, y0.w, a[1][0]))));
+                a[1][1] = fmaf(x1.x, y1.x, fmaf(x1.y, y1.y, fmaf(x1.z, y1.z, fmaf(x1.w, y1.w, a[1][1]))));
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                    const int rr = r + 16 * e, cc = c + 16 * f;
+                    const bool in = rev ? cc >= rr : cc <= rr;
+                    const float d = (G[rr] - G[cc]) + (GL[rr] - GL[cc]);
+                    P[rr * LDP + cc] = in ? a[e][f] * __expf(rev ? -d : d) : 0.f;
+                }
+            __syncthreads();
+            // ---- o: rows OR rg .. of 4 columns
+            float o[OR][4] = {};
+#pragma unroll 4
+            for (int i = 0; i < DX; i += 4) {
+                float4 s[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[e] = ld4(S + (i + e) * LDZ + c0);
+#pragma unroll
+                for (int q = 0; q < OR; ++q) {
+                    const float4 x = ld4(X + (OR * rg + q) * LDX + i);
+                    const float xv[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        o[q][0] = fmaf(xv[e], s[e].x, o[q][0]);
+                        o[q][1] = fmaf(xv[e], s[e].y, o[q][1]);
+                        o[q][2] = fmaf(xv[e], s[e].z, o[q][2]);
+                        o[q][3] = fmaf(xv[e], s[e].w, o[q][3]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < OR; ++q) {
+                const float cx = CX[OR * rg + q];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[q][e] *= cx;
+            }
+#pragma unroll 4
+            for (int u = 0; u < C; ++u) {
+                const float4 z = ld4(Z + u * LDZ + c0);
+#pragma unroll
+                for (int q = 0; q < OR; ++q) {
+                    const int rr = OR * rg + q;
+                    if (rev ? u >= rr : u <= rr) {      // a token that is not seen may hold anything
+                        const float w = P[rr * LDP + u];
+                        o[q][0] = fmaf(w, z.x, o[q][0]);
+                        o[q][1] = fmaf(w, z.y, o[q][1]);
+                        o[q][2] = fmaf(w, z.z, o[q][2]);
+                        o[q][3] = fmaf(w, z.w, o[q][3]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < OR; ++q) {
+                const int rr = OR * rg + q;
+                const long long t = t0 + rr;
+                if (rr < n) store4<IT>(p.o, sg.b * p.ob + sg.h * p.oh + t * p.ot + z0 + c0, o[q], p.o_f32);
+                if (p.dots) {
+                    float d = 0.f;
+                    if (rr < n) {
+                        const IT* w = static_cast<const IT*>(p.w.p) + sg.b * p.w.sb + (sg.h / p.w.div) * p.w.sh + t * p.w.st + z0 + c0;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) d = fmaf(o[q][e], static_cast<float>(w[e]), d);
+                    }
+#pragma unroll
+                    for (int off = CG / 2; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
+                    if (cg == 0 && rr < n)
+                        p.dots[(zb * bh + sg.b * geo.H + sg.h) * geo.T + t] = d;
+                }
+            }
+            __syncthreads();   // S was read
+        }
+        // ---- the state: rows SR rg .. of 4 columns
+        {
+            float a[SR][4];
+            const float e = __expf(all);
+#pragma unroll
+            for (int q = 0; q < SR; ++q) {
+                const float4 s = ld4(S + (SR * rg + q) * LDZ + c0);
+                a[q][0] = e * s.x; a[q][1] = e * s.y; a[q][2] = e * s.z; a[q][3] = e * s.w;
+            }
+            for (int u = 0; u < n; ++u) {
+                const float w = W[u];
+                float4 z = ld4(Z + u * LDZ + c0);
+                z.x *= w; z.y *= w; z.z *= w; z.w *= w;
+#pragma unroll
+                for (int q = 0; q < SR; ++q) {
+                    const float y = Y[u * LDX + SR * rg + q];
+                    a[q][0] = fmaf(y, z.x, a[q][0]);
+                    a[q][1] = fmaf(y, z.y, a[q][1]);
+                    a[q][2] = fmaf(y, z.z, a[q][2]);
+                    a[q][3] = fmaf(y, z.w, a[q][3]);
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < SR; ++q)
+                *reinterpret_cast<float4*>(S + (SR * rg + q) * LDZ + c0) = make_float4(a[q][0], a[q][1], a[q][2], a[q][3]);
+        }
+    }
+    __syncthreads();
+    // ---- the state it ends with
+    float* dst = nullptr;
+    if (so) dst = p.bound + (rev ? sg.entry : sg.entry + sg.step) * (long long)DX * p.DZ;
+    else if (p.ext_out && (rev ? sg.first : sg.last)) dst = p.ext_out + sg.ext * (long long)DX * p.DZ;
+    if (dst)
+        for (int i = tid; i < DX * NZ; i += TH) {
+            const int r = i / NZ, c = i % NZ;
+            dst[r * p.six + (z0 + c) * p.siz] = S[r * LDZ + c];
+        }
+    if (so && p.gsum && zb == 0 && tid == 0) p.gsum[sg.entry] = gsum;
+}
+
+template <class IT, int DX>
+__device__ __forceinline__ void pass_nz(const Pass& p, const Geometry& geo, const Segment& sg, int zb, long long bh, float* sm) {
+    if (p.DZ == 32) segment_pass<IT, DX, 32>(p, geo, sg, zb, bh, sm);
+    else segment_pass<IT, DX, 64>(p, geo, sg, zb, bh, sm);
+}
+
+// grid: x = unit * (column blocks of the widest pass) + column block, y = pass
+template <class IT>
+__global__ void __launch_bounds__(TH) hd_fp32_kernel(const __grid_constant__ Launch a, int zmax, long long bh) {
+    extern __shared__ __align__(16) float sm[];
+    const Pass& p = a.pass[blockIdx.y];
+    const int zb = blockIdx.x % zmax;
+    if (zb * (p.DZ == 32 ? 32 : 64) >= p.DZ) return;
+    Segment sg;
+    if (!locate(a.geo, blockIdx.x / zmax, sg)) return;
+    if (p.states_only == 1 && (p.reverse ? sg.first : sg.last)) return;
+    switch (p.DX) {
+        case 32: pass_nz<IT, 32>(p, a.geo, sg, zb, bh, sm); break;
+        case 64: pass_nz<IT, 64>(p, a.geo, sg, zb, bh, sm); break;
+        default: pass_nz<IT, 128>(p, a.geo, sg, zb, bh, sm); break;
+    }
+}
+
+std::atomic<uint64_t> g_set_f32{0}, g_set_bf16{0};
+
+}  // namespace
+
+int fp32_zblock(int DZ) { return DZ == 32 ? 32 : 64; }
+
+cudaError_t launch_fp32(const Launch& a, cudaStream_t s) {
+    int zmax = 1;
+    size_t bytes = 0;
+    for (int i = 0; i < a.npass; ++i) {
+        const Pass& p = a.pass[i];
+        const int nz = fp32_zblock(p.DZ);
+        zmax = max(zmax, p.DZ / nz);
+        const size_t need = sizeof(float) * ((size_t)2 * C * (p.DX + 4) + (size_t)(C + p.DX) * (nz + 4) + C * LDP + 4 * C + 4);
+        bytes = need > bytes ? need : bytes;
+    }
+    const long long n = units(a.geo, a.B, a.max_blocks) * zmax;
+    if (n == 0) return cudaSuccess;
+    if (n >= (1LL << 31)) return cudaErrorInvalidValue;
+    const void* f = a.bf16 ? (const void*)hd_fp32_kernel<__nv_bfloat16> : (const void*)hd_fp32_kernel<float>;
+    const int most = (int)(sizeof(float) * (2 * C * 132 + (C + 128) * 68 + C * LDP + 4 * C + 4));
+    cudaError_t e = set_smem_limit_once(f, most, a.bf16 ? g_set_bf16 : g_set_f32);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)n, (unsigned)a.npass);
+    const long long bh = (long long)a.B * a.geo.H;
+    if (a.bf16) hd_fp32_kernel<__nv_bfloat16><<<grid, TH, bytes, s>>>(a, zmax, bh);
+    else hd_fp32_kernel<float><<<grid, TH, bytes, s>>>(a, zmax, bh);
+    return cudaGetLastError();
+}
+
+}  // namespace hd
+}  // namespace dplr

@@ -1,0 +1,163 @@
+// Linear attention with one decay per head: what its translation units share (not part of the ABI).
+//
+// Everything, gradients included, is one operator on three row sequences x, y (DX features) and z (DZ features):
+//
+//   forward in time    o_t = R_t^T x_t,  R_t = e^{g_t} R_{t-1} + y_t z_t^T
+//   backward in time   o_t = R_t^T x_t,  R_t = e^{g_{t+1}} R_{t+1} + y_t z_t^T
+//
+// The prompt is (x, y, z) = (q, k, v) forward. With dS_t the gradient of the state after token t, dq_t = S_t dO_t is
+// (dO, v, k) forward (its state is S^T), dk_t = dS_t v_t is (v, dO, q) backward (state dS^T) and dv_t = dS_t^T k_t is
+// (k, q, dO) backward (state dS), because dS_t = e^{g_{t+1}} dS_{t+1} + q_t dO_t^T.
+//
+// A sequence is cut into segments. Segment i starts (forward) from the boundary state i and ends at boundary i + 1;
+// backward it starts from boundary i + 1. "States" passes form each segment's own contribution, a scan turns these
+// into the boundary states, and "outputs" passes compute every segment from its boundary state.
+#pragma once
+
+#include "dplr_internal.h"
+
+namespace dplr {
+namespace hd {
+
+constexpr int kChunk = 128;           // tokens that the tensor-core kernels compute together
+constexpr float kMinGate = -128.f;    // log-gates below this act like it: e^-128 is zero in fp32
+
+// One row sequence: element (b, h, t, i) at p + b sb + (h / div) sh + t st + i.
+struct View {
+    const void* p;
+    long long sb, sh, st;
+    int div;
+};
+
+// Which (batch, head, segment) a CTA works on.
+struct Geometry {
+    int H;
+    int T;                  // tokens of a sequence (dense)
+    int nseg, L;            // dense: segments of a sequence, tokens of a segment
+    const int* blocks;      // packed: [.][4] request, first row, rows, index in the request; null: dense
+    const int* block_starts;
+    const int* slots;
+    const int* context;
+    int n_slots;
+};
+
+struct Segment {
+    int b, h, t0, n;
+    bool alone;             // the sequence has one segment: its boundary states are the caller's
+    bool first, last;
+    bool fresh;             // packed: the request starts from zero
+    long long ext;          // index of the sequence's state in the caller's arrays
+    long long entry;        // index of boundary state "segment start" in the boundary array; the next is entry + step
+    long long step;
+};
+
+__host__ __device__ inline long long units(const Geometry& g, int B, int max_blocks) {
+    return g.blocks ? (long long)max_blocks * g.H : (long long)B * g.H * g.nseg;
+}
+
+// False: nothing to do (a block behind the last).
+__device__ __forceinline__ bool locate(const Geometry& g, long long unit, Segment& s) {
+    if (g.blocks) {
+        const int blk = (int)(unit / g.H);
+        s.h = (int)(unit % g.H);
+        const int4 e = *reinterpret_cast<const int4*>(g.blocks + 4 * (long long)blk);
+        if (e.x < 0) return false;
+        const int nb = g.block_starts[e.x + 1] - g.block_starts[e.x];
+        s.b = 0; s.t0 = e.y; s.n = e.z;
+        s.alone = nb == 1; s.first = e.w == 0; s.last = e.w == nb - 1;
+        s.fresh = g.context[e.x] == 0;
+        const int slot = g.slots[e.x];
+        if (slot < 0 || slot >= g.n_slots) return false;
+        s.ext = (long long)slot * g.H + s.h;
+        s.entry = (long long)blk * g.H + s.h;
+        s.step = g.H;
+        return true;
+    }
+    const long long bh = unit / g.nseg;
+    const int seg = (int)(unit % g.nseg);
+    s.b = (int)(bh / g.H); s.h = (int)(bh % g.H);
+    s.t0 = seg * g.L;
+    s.n = min(g.L, g.T - s.t0);
+    s.alone = g.nseg == 1; s.first = seg == 0; s.last = seg == g.nseg - 1;
+    s.fresh = false;
+    s.ext = bh;
+    s.entry = bh * (g.nseg + 1) + seg;
+    s.step = 1;
+    return true;
+}
+
+// One pass over the segments. States are [DX][DZ] of the pass: element (i, j) of the state with index e of an array of
+// [dk][dv] states at e * dk * dv + i * six + j * siz (six, siz = dv, 1 or, for a pass on transposed states, 1, dv).
+struct Pass {
+    View x, y, z;
+    const float* g; long long gb, gh, gt;   // log-gates (0 strides: one per head)
+    int reverse;
+    int DX, DZ;
+    long long six, siz;
+    const float* ext_in;     // the caller's initial (backward in time: final) states, nullable
+    float* ext_out;          // outputs pass: where the last segment leaves its state (plain orientation), nullable
+    float* bound;            // boundary states (null: every sequence has one segment)
+    float* gsum;             // states pass: sum of the segment's gates, at the segment's entry
+    // outputs
+    void* o; long long ob, oh, ot; int o_f32;
+    // dots: per token sum_j o_j w_j with w like z, at dots[zb * B * H * T + (b * H + h) * T + t]; null: none
+    View w; float* dots;
+    int states_only;         // 1: states pass without the segment whose contribution no boundary needs; 2: with it
+};
+
+struct Launch {
+    Geometry geo;
+    int B, bf16;
+    int max_blocks;          // packed
+    int npass;
+    Pass pass[3];
+    int* status;
+    long long wait_cycles;
+};
+
+cudaError_t launch_decode(const View& q, const View& k, const View& v, const float* g, long long gb, long long gh,
+                          float* S, const int* slots, int nslots, int B, int H, int dk, int dv, bool bf16, void* o,
+                          long long ob, long long oh, int* status, cudaStream_t s);
+
+// CUDA-core kernels (any type and size), 64-column (or 32) blocks of the state per CTA.
+int fp32_zblock(int DZ);
+cudaError_t launch_fp32(const Launch& a, cudaStream_t s);
+
+// Turns segments' own contributions into boundary states, in place. Forward: the contribution of segment i lies at
+// boundary i + 1, and boundary 0 is ext (or zero); backward: that of segment i at boundary i, boundary nseg is ext.
+// Both arrays may be given (the gradient's two scans in one launch). `upto_end`: forward goes on to boundary nseg.
+struct Scan {
+    Geometry geo;
+    int B, R, dk, dv;
+    float* fwd; const float* fwd_ext; int upto_end;
+    float* bwd; const float* bwd_ext;
+    const float* gsum;
+};
+cudaError_t launch_scan(const Scan& a, cudaStream_t s);
+
+// ddecay from the per-token dots and the boundary states: with a_t = q_t . dq_t - k_t . dk_t and e the end of t's segment,
+//   ddecay_t = sum_{s=t..e} a_s + <S_e, dS_e>
+// (the contributions of pairs of tokens on the same side of t cancel in the sum; segments keep what cancels short).
+struct GateGrad {
+    int B, H, T, nseg, L, dk, dv;
+    const float* dq_dots; int nq;          // [nq][B*H*T]: partial sums over column blocks
+    const float* dk_dots; int nk;
+    const float* fwd; const float* bwd;    // boundary states; null: one segment
+    int last_end;                          // whether <S_T, dS_T> counts (dST given)
+    const float* S_T; const float* dST;    // one segment with last_end: the two states
+    float* dg_token;                       // [B,H,T], null with per_head
+    double* seg_sum;                       // [B*H*nseg] with per_head
+    float* dg_head;                        // [H] with per_head
+};
+cudaError_t launch_gate_grad(const GateGrad& a, cudaStream_t s);
+
+// Gradients of shared query/key heads: out[b, hq, t] = sum over hq's value heads of part [B,H,T,D] (fp32), in head order.
+struct GroupSum {
+    int B, H, Hq, T, D, bf16;
+    const float* part;
+    void* out; long long ob, oh, ot;
+};
+cudaError_t launch_group_sum(const GroupSum& a, cudaStream_t s);
+
+}  // namespace hd
+}  // namespace dplr

@@ -1,0 +1,153 @@
+// Tables of a ragged batch from its requests' lengths: starts, blocks of rows, each row's slot and position.
+//
+// One launch without waits between CTAs: every CTA scans the lengths itself (R x 12 bytes, from L2 after the first) and
+// then fills its share of the tables, finding a row's request by bisection of the starts in shared memory. The floor
+// is a launch and the scan's latency for few requests, and for many the bytes of the tables (8 a row of the batch).
+#include "dplr_internal.h"
+
+namespace dplr {
+namespace hd {
+namespace {
+
+constexpr int TH = 512;
+constexpr int kMaxRequests = 8192, kMaxSlots = 1 << 20;
+constexpr int kRows = 2 * TH;     // rows of the batch that a CTA fills in one turn
+
+struct PlanArgs {
+    int R, cap, block, nslots, nblocks;
+    const int* lengths; const int* slots; const int* context;
+    int* starts; int4* blocks; int* block_starts; int* token_slot; int* token_pos; int* status;
+};
+
+// Exclusive prefix sums of two values over the CTA; the totals too. 64 bits: lengths that are refused may be anything.
+__device__ __forceinline__ void scan2(long long a, long long b, long long* sh, long long& ea, long long& eb,
+                                      long long& ta, long long& tb) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    long long xa = a, xb = b;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long ya = __shfl_up_sync(0xffffffffu, xa, off), yb = __shfl_up_sync(0xffffffffu, xb, off);
+        if (lane >= off) { xa += ya; xb += yb; }
+    }
+    __syncthreads();
+    if (lane == 31) { sh[2 * w] = xa; sh[2 * w + 1] = xb; }
+    __syncthreads();
+    long long pa = 0, pb = 0;
+    ta = 0; tb = 0;
+#pragma unroll
+    for (int i = 0; i < TH / 32; ++i) {
+        if (i < w) { pa += sh[2 * i]; pb += sh[2 * i + 1]; }
+        ta += sh[2 * i]; tb += sh[2 * i + 1];
+    }
+    ea = pa + xa - a;
+    eb = pb + xb - b;
+}
+
+// The last r with s[r] <= t among s[0 .. n - 1], s ascending, s[0] <= t.
+__device__ __forceinline__ int find(const int* s, int n, int t) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s[mid] <= t) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(TH) hd_plan_kernel(PlanArgs a) {
+    extern __shared__ int sm[];
+    int* st = sm;                        // [R + 1] starts
+    int* bs = st + a.R + 1;              // [R + 1] first blocks
+    unsigned* seen = reinterpret_cast<unsigned*>(bs + a.R + 1);   // one bit per slot
+    __shared__ long long sh[2 * TH / 32];
+    const int tid = threadIdx.x;
+    for (int i = tid; i < (a.nslots + 31) / 32; i += TH) seen[i] = 0;
+    __syncthreads();
+    bool bad = false;
+    long long rows = 0, blocks = 0;
+    for (int r0 = 0; r0 < a.R; r0 += TH) {
+        const int r = r0 + tid;
+        int n = 0;
+        if (r < a.R) {
+            n = a.lengths[r];
+            const int c = a.context[r];
+            if (n < 0 || n > a.cap || c < 0 || (long long)c + n > 2147483647LL) { bad = true; n = 0; }
+            if (n > 0) {
+                const int s = a.slots[r];
+                if (s < 0 || s >= a.nslots) bad = true;
+                else if (atomicOr(&seen[s >> 5], 1u << (s & 31)) & (1u << (s & 31))) bad = true;
+            }
+        }
+        long long en, eb, tn, tb;
+        scan2(n, (n + a.block - 1) / a.block, sh, en, eb, tn, tb);
+        if (r < a.R) {
+            st[r] = (int)min(rows + en, (long long)a.cap);
+            bs[r] = (int)min(blocks + eb, (long long)a.nblocks);
+        }
+        rows += tn;
+        blocks += tb;
+    }
+    bad = __syncthreads_or(bad) || rows > a.cap;
+    if (bad) {      // the tables of a batch without tokens
+        rows = 0; blocks = 0;
+        for (int r = tid; r < a.R; r += TH) { st[r] = 0; bs[r] = 0; }
+    }
+    if (tid == 0) { st[a.R] = (int)rows; bs[a.R] = (int)blocks; }
+    __syncthreads();
+    if (blockIdx.x == 0) {
+        for (int r = tid; r <= a.R; r += TH) { a.starts[r] = st[r]; a.block_starts[r] = bs[r]; }
+        if (tid == 0) *a.status = bad ? (int)DPLR_ERR_INVALID_ARG : (int)DPLR_OK;
+    }
+    const int stride = gridDim.x * TH;
+    for (int i = blockIdx.x * TH + tid; i < a.nblocks; i += stride) {
+        int4 e = make_int4(-1, -1, -1, -1);
+        if (i < blocks) {
+            const int r = find(bs, a.R, i), k = i - bs[r];
+            const int first = st[r] + k * a.block;
+            e = make_int4(r, first, min(a.block, st[r + 1] - first), k);
+        }
+        a.blocks[i] = e;
+    }
+    for (int t = blockIdx.x * TH + tid; t < a.cap; t += stride) {
+        int slot = -1, pos = -1;
+        if (t < rows) {
+            const int r = find(st, a.R, t);
+            slot = a.slots[r];
+            pos = a.context[r] + (t - st[r]);
+        }
+        a.token_slot[t] = slot;
+        a.token_pos[t] = pos;
+    }
+}
+
+std::atomic<uint64_t> g_set{0};
+
+}  // namespace
+}  // namespace hd
+}  // namespace dplr
+
+using namespace dplr;
+using namespace dplr::hd;
+
+extern "C" dplr_status dplr_hd_plan(int32_t R, int32_t capacity, int32_t block, int32_t n_slots, const int32_t* lengths,
+                                    const int32_t* slots, const int32_t* context, int32_t* starts, int32_t* blocks,
+                                    int32_t* block_starts, int32_t* token_slot, int32_t* token_pos, int32_t* status,
+                                    void* stream) {
+    if (R < 1 || capacity < 0 || block < 1 || n_slots < 1) return DPLR_ERR_INVALID_ARG;
+    if (R > kMaxRequests || capacity >= (1 << 30) || block % 32 != 0 || n_slots > kMaxSlots) return DPLR_ERR_UNSUPPORTED;
+    auto ok = [](const void* p, unsigned al) { return p && (reinterpret_cast<uintptr_t>(p) & (al - 1)) == 0; };
+    if (!ok(lengths, 4) || !ok(slots, 4) || !ok(context, 4) || !ok(starts, 4) || !ok(blocks, 16) || !ok(block_starts, 4) ||
+        !ok(status, 4) || (capacity > 0 && (!ok(token_slot, 4) || !ok(token_pos, 4))))
+        return DPLR_ERR_INVALID_ARG;
+    PlanArgs a{R, capacity, block, n_slots, capacity / block + R, lengths, slots, context, starts,
+               reinterpret_cast<int4*>(blocks), block_starts, token_slot, token_pos, status};
+    const int bytes = 4 * (2 * (R + 1) + (n_slots + 31) / 32);
+    const int most = 4 * (2 * (kMaxRequests + 1) + kMaxSlots / 32);
+    static_assert(4 * (2 * (kMaxRequests + 1) + kMaxSlots / 32) < 227 * 1024 - 1024, "shared memory budget");
+    cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(hd_plan_kernel), most, g_set);
+    if (e != cudaSuccess) return DPLR_ERR_CUDA;
+    const long long items = capacity > a.nblocks ? capacity : a.nblocks;
+    const long long want = (items + kRows - 1) / kRows, sms = sm_count();
+    const unsigned grid = (unsigned)(want < 1 ? 1 : (want < sms ? want : sms));
+    hd_plan_kernel<<<grid, TH, bytes, static_cast<cudaStream_t>(stream)>>>(a);
+    return cudaGetLastError() == cudaSuccess ? DPLR_OK : DPLR_ERR_CUDA;
+}

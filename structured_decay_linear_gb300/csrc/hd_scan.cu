@@ -1,0 +1,212 @@
+// The small steps between the passes of the per-head-decay operator: boundary states from segments' own contributions,
+// the gradient of the log-gates, and the sums over value heads that share a query/key head. All are bound by the
+// bytes that they move; none uses atomics, so their results do not depend on timing.
+#include <cuda_bf16.h>
+
+#include "hd_internal.h"
+
+namespace dplr {
+namespace hd {
+namespace {
+
+// ---- boundary states: one thread per four elements of one (sequence, head)'s state, walking its segments. The loads
+// of the contributions do not depend on the chain, so four are in flight at a time.
+constexpr int kAhead = 4;
+
+__global__ void __launch_bounds__(256) hd_scan_kernel(const __grid_constant__ Scan a) {
+    const long long size = (long long)a.dk * a.dv;
+    const int at = (blockIdx.y * 256 + threadIdx.x) * 4;
+    if (at >= size) return;
+    const bool back = a.fwd == nullptr || blockIdx.z == 1;
+    float* W = back ? a.bwd : a.fwd;
+    const float* ext = back ? a.bwd_ext : a.fwd_ext;
+    long long base, step, eidx;
+    int nseg;
+    bool fresh = false;
+    if (a.geo.blocks) {
+        const int r = blockIdx.x / a.geo.H, h = blockIdx.x % a.geo.H;
+        const int b0 = a.geo.block_starts[r];
+        nseg = a.geo.block_starts[r + 1] - b0;
+        if (nseg < 2) return;
+        base = (long long)b0 * a.geo.H + h;
+        step = a.geo.H;
+        const int slot = a.geo.slots[r];
+        if (slot < 0 || slot >= a.geo.n_slots) return;
+        eidx = (long long)slot * a.geo.H + h;
+        fresh = a.geo.context[r] == 0;
+    } else {
+        nseg = a.geo.nseg;
+        base = (long long)blockIdx.x * (nseg + 1);
+        step = 1;
+        eidx = blockIdx.x;
+    }
+    float4 cur = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (ext && !fresh) cur = *reinterpret_cast<const float4*>(ext + eidx * size + at);
+    // step i (0 ..): the contribution lies at boundary first + i dir, its gates at segment gfirst + i dir
+    const int n = back ? nseg - 1 : (a.upto_end ? nseg : nseg - 1);
+    const long long dir = back ? -step : step;
+    const long long start = base + (back ? (long long)nseg * step : 0);
+    const long long gfirst = base + (back ? (long long)(nseg - 1) * step : 0);
+    *reinterpret_cast<float4*>(W + start * size + at) = cur;
+    for (int i = 0; i < n; i += kAhead) {
+        float4 v[kAhead];
+        float e[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (i + u < n) {
+                v[u] = *reinterpret_cast<const float4*>(W + (start + (i + u + 1) * dir) * size + at);
+                e[u] = __expf(a.gsum[gfirst + (i + u) * dir]);
+            }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (i + u < n) {
+                cur.x = fmaf(e[u], cur.x, v[u].x);
+                cur.y = fmaf(e[u], cur.y, v[u].y);
+                cur.z = fmaf(e[u], cur.z, v[u].z);
+                cur.w = fmaf(e[u], cur.w, v[u].w);
+                *reinterpret_cast<float4*>(W + (start + (i + u + 1) * dir) * size + at) = cur;
+            }
+    }
+}
+
+// ---- the gradient of the log-gates: one CTA per segment of one (batch, head)
+__global__ void __launch_bounds__(256) hd_gate_grad_kernel(const __grid_constant__ GateGrad a) {
+    __shared__ double part[8];
+    __shared__ double carry_s;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const long long bh = blockIdx.x / a.nseg;
+    const int seg = blockIdx.x % a.nseg;
+    const int t0 = seg * a.L, n = min(a.L, a.T - t0);
+    const long long size = (long long)a.dk * a.dv, all = (long long)a.B * a.H * a.T;
+    const bool last = seg == a.nseg - 1;
+    // <S, dS> at the segment's end
+    double d = 0.0;
+    if (!last || a.last_end) {
+        const float *S, *R;
+        if (a.fwd) {
+            S = a.fwd + (bh * (a.nseg + 1) + seg + 1) * size;
+            R = a.bwd + (bh * (a.nseg + 1) + seg + 1) * size;
+        } else {
+            S = a.S_T + bh * size;
+            R = a.dST + bh * size;
+        }
+        for (int i = 4 * tid; i < size; i += 1024) {
+            const float4 x = *reinterpret_cast<const float4*>(S + i), y = *reinterpret_cast<const float4*>(R + i);
+            d += (double)(x.x * y.x + x.y * y.y) + (double)(x.z * y.z + x.w * y.w);
+        }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
+    if (lane == 0) part[warp] = d;
+    __syncthreads();
+    double carry = 0.0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) carry += part[w];
+    // suffix sums, 256 tokens at a time from the end
+    double total = 0.0;
+    for (int hi = n; hi > 0; hi -= 256) {
+        const int i = hi - 1 - tid;            // thread 0 takes the last token
+        double x = 0.0;
+        const long long t = bh * a.T + t0 + i;
+        if (i >= 0) {
+            for (int z = 0; z < a.nq; ++z) x += (double)a.dq_dots[z * all + t];
+            for (int z = 0; z < a.nk; ++z) x -= (double)a.dk_dots[z * all + t];
+        }
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const double y = __shfl_up_sync(0xffffffffu, x, off);
+            if (lane >= off) x += y;
+        }
+        __syncthreads();
+        if (lane == 31) part[warp] = x;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) x += part[w];
+        x += carry;
+        if (i >= 0) {
+            if (a.dg_token) a.dg_token[t] = (float)x;
+            total += x;
+        }
+        if (tid == 255) carry_s = x;
+        __syncthreads();
+        carry = carry_s;
+    }
+    if (a.seg_sum) {
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+        __syncthreads();
+        if (lane == 0) part[warp] = total;
+        __syncthreads();
+        if (tid == 0) {
+            double s = 0.0;
+            for (int w = 0; w < 8; ++w) s += part[w];
+            a.seg_sum[blockIdx.x] = s;
+        }
+    }
+}
+
+// one warp per head: the sum of its segments, batch by batch
+__global__ void __launch_bounds__(32) hd_head_grad_kernel(const __grid_constant__ GateGrad a) {
+    const int h = blockIdx.x, lane = threadIdx.x;
+    double s = 0.0;
+    for (int i = lane; i < a.B * a.nseg; i += 32)
+        s += a.seg_sum[((long long)(i / a.nseg) * a.H + h) * a.nseg + i % a.nseg];
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    if (lane == 0) a.dg_head[h] = (float)s;
+}
+
+template <bool BF>
+__global__ void __launch_bounds__(256) hd_group_sum_kernel(const __grid_constant__ GroupSum a) {
+    const int per = a.D / 4, group = a.H / a.Hq;
+    const long long n = (long long)a.B * a.Hq * a.T * per;
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
+        const int c = (int)(i % per) * 4;
+        const long long row = i / per;
+        const long long t = row % a.T, hq = (row / a.T) % a.Hq, b = row / a.T / a.Hq;
+        const float* src = a.part + ((b * a.H + hq * group) * a.T + t) * a.D + c;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int j = 0; j < group; ++j) {
+            const float4 v = *reinterpret_cast<const float4*>(src + (long long)j * a.T * a.D);
+            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+        }
+        const long long at = b * a.ob + hq * a.oh + t * a.ot + c;
+        if (BF) {
+            __nv_bfloat162 x = __floats2bfloat162_rn(s.x, s.y), y = __floats2bfloat162_rn(s.z, s.w);
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) =
+                make_uint2(*reinterpret_cast<uint32_t*>(&x), *reinterpret_cast<uint32_t*>(&y));
+        } else {
+            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = s;
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_scan(const Scan& a, cudaStream_t s) {
+    const long long rows = a.geo.blocks ? (long long)a.R * a.geo.H : (long long)a.B * a.geo.H;
+    if (rows == 0) return cudaSuccess;
+    const unsigned gy = (unsigned)((a.dk * a.dv / 4 + 255) / 256), gz = a.fwd && a.bwd ? 2 : 1;
+    hd_scan_kernel<<<dim3((unsigned)rows, gy, gz), 256, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_gate_grad(const GateGrad& a, cudaStream_t s) {
+    const long long n = (long long)a.B * a.H * a.nseg;
+    if (n >= (1LL << 31)) return cudaErrorInvalidValue;
+    hd_gate_grad_kernel<<<(unsigned)n, 256, 0, s>>>(a);
+    if (a.dg_head) hd_head_grad_kernel<<<(unsigned)a.H, 32, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_group_sum(const GroupSum& a, cudaStream_t s) {
+    const long long n = (long long)a.B * a.Hq * a.T * (a.D / 4);
+    const long long most = (long long)sm_count() * 8;
+    const long long blocks = (n + 255) / 256;
+    const unsigned g = (unsigned)(blocks < most ? blocks : most);
+    if (a.bf16) hd_group_sum_kernel<true><<<g, 256, 0, s>>>(a);
+    else hd_group_sum_kernel<false><<<g, 256, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace hd
+}  // namespace dplr

@@ -29,6 +29,15 @@ class dplr_desc(ctypes.Structure):
                 ("r_ab", ctypes.c_int32), ("r_kv", ctypes.c_int32), ("chunk", ctypes.c_int32)]
 
 
+class dplr_hd_tensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("sb", ctypes.c_int64), ("sh", ctypes.c_int64), ("st", ctypes.c_int64)]
+
+
+class dplr_hd_desc(ctypes.Structure):
+    _fields_ = [("in_dtype", ctypes.c_int32), ("B", ctypes.c_int32), ("H", ctypes.c_int32), ("Hq", ctypes.c_int32),
+                ("T", ctypes.c_int32), ("dk", ctypes.c_int32), ("dv", ctypes.c_int32), ("per_head", ctypes.c_int32)]
+
+
 class DplrError(RuntimeError):
     def __init__(self, status: int, what: str):
         super().__init__(f"{what}: {status_string(status)}")
@@ -103,6 +112,29 @@ def library() -> ctypes.CDLL:
             lib.dplr_la_forward_host_seq.restype = ctypes.c_int
             lib.dplr_la_forward_host_seq.argtypes = [dp] + [_vp] * 12 + [_vp, ctypes.c_size_t, ctypes.c_int,
                                                                          ctypes.c_int, _vp]
+            hp, tp, i32 = ctypes.POINTER(dplr_hd_desc), ctypes.POINTER(dplr_hd_tensor), ctypes.c_int32
+            lib.dplr_hd_check.restype = ctypes.c_int
+            lib.dplr_hd_check.argtypes = [hp]
+            lib.dplr_hd_path.restype = ctypes.c_char_p
+            lib.dplr_hd_path.argtypes = [hp]
+            lib.dplr_hd_workspace_size.restype = ctypes.c_size_t
+            lib.dplr_hd_workspace_size.argtypes = [hp]
+            lib.dplr_hd_forward.restype = ctypes.c_int
+            lib.dplr_hd_forward.argtypes = [hp, tp, tp, tp, tp, _vp, tp, _vp, _vp, ctypes.c_size_t, _vp]
+            lib.dplr_hd_backward_workspace_size.restype = ctypes.c_size_t
+            lib.dplr_hd_backward_workspace_size.argtypes = [hp]
+            lib.dplr_hd_backward.restype = ctypes.c_int
+            lib.dplr_hd_backward.argtypes = [hp, tp, tp, tp, tp, _vp, tp, _vp, tp, tp, tp, _vp, _vp, _vp,
+                                             ctypes.c_size_t, _vp]
+            lib.dplr_hd_plan.restype = ctypes.c_int
+            lib.dplr_hd_plan.argtypes = [i32, i32, i32, i32] + [_vp] * 10
+            lib.dplr_hd_packed_workspace_size.restype = ctypes.c_size_t
+            lib.dplr_hd_packed_workspace_size.argtypes = [hp, i32, i32]
+            lib.dplr_hd_forward_packed.restype = ctypes.c_int
+            lib.dplr_hd_forward_packed.argtypes = [hp, i32, i32, i32, _vp, _vp, _vp, _vp, tp, tp, tp, tp, _vp, tp, _vp,
+                                                   ctypes.c_size_t, _vp]
+            lib.dplr_hd_decode_step.restype = ctypes.c_int
+            lib.dplr_hd_decode_step.argtypes = [hp, i32, _vp, tp, tp, tp, tp, _vp, tp, _vp, _vp]
             _lib = lib
     return _lib
 
@@ -603,3 +635,352 @@ class GDP:
         if st != DPLR_OK:
             raise DplrError(st, "dplr_gdp_forward")
         return self.o, self.S_T
+
+
+# ----------------------------------------------------------------------------
+# Linear attention with one decay per head (dplr_hd_*).
+# ----------------------------------------------------------------------------
+
+def make_hd_desc(in_dtype, B: int, H: int, T: int, dk: int, dv: int, q_heads: Optional[int] = None,
+                 per_head: bool = False) -> dplr_hd_desc:
+    if in_dtype in (torch.bfloat16, "bf16", DPLR_BF16):
+        dt = DPLR_BF16
+    elif in_dtype in (torch.float32, "f32", DPLR_F32):
+        dt = DPLR_F32
+    else:
+        raise ValueError(f"unsupported input dtype {in_dtype}")
+    return dplr_hd_desc(dt, B, H, H if q_heads is None else q_heads, T, dk, dv, int(bool(per_head)))
+
+
+def dplr_hd_check(desc: dplr_hd_desc) -> int:
+    return int(library().dplr_hd_check(ctypes.byref(desc)))
+
+
+def dplr_hd_path(desc: dplr_hd_desc) -> str:
+    return library().dplr_hd_path(ctypes.byref(desc)).decode()
+
+
+def dplr_hd_workspace_size(desc: dplr_hd_desc) -> int:
+    return int(library().dplr_hd_workspace_size(ctypes.byref(desc)))
+
+
+def dplr_hd_backward_workspace_size(desc: dplr_hd_desc) -> int:
+    return int(library().dplr_hd_backward_workspace_size(ctypes.byref(desc)))
+
+
+def dplr_hd_packed_workspace_size(desc: dplr_hd_desc, R: int, block: int) -> int:
+    return int(library().dplr_hd_packed_workspace_size(ctypes.byref(desc), int(R), int(block)))
+
+
+def _ref(t: Optional[dplr_hd_tensor]):
+    return None if t is None else ctypes.byref(t)
+
+
+def dplr_hd_forward(desc, q, k, v, decay, S0, o, S_T, workspace, ws_bytes, stream) -> int:
+    """q, k, v, decay, o: dplr_hd_tensor (or None); the states and the workspace: device pointers."""
+    return int(library().dplr_hd_forward(ctypes.byref(desc), _ref(q), _ref(k), _ref(v), _ref(decay), S0, _ref(o), S_T,
+                                         workspace, ctypes.c_size_t(ws_bytes), stream))
+
+
+def dplr_hd_backward(desc, q, k, v, decay, S0, dO, dST, dq, dk, dv, ddecay, dS0, workspace, ws_bytes, stream) -> int:
+    return int(library().dplr_hd_backward(ctypes.byref(desc), _ref(q), _ref(k), _ref(v), _ref(decay), S0, _ref(dO), dST,
+                                          _ref(dq), _ref(dk), _ref(dv), ddecay, dS0, workspace,
+                                          ctypes.c_size_t(ws_bytes), stream))
+
+
+def dplr_hd_plan(R, capacity, block, n_slots, lengths, slots, context, starts, blocks, block_starts, token_slot,
+                 token_pos, status, stream) -> int:
+    return int(library().dplr_hd_plan(R, capacity, block, n_slots, lengths, slots, context, starts, blocks,
+                                      block_starts, token_slot, token_pos, status, stream))
+
+
+def dplr_hd_forward_packed(desc, R, block, n_slots, blocks, block_starts, slots, context, q, k, v, decay, S, o,
+                           workspace, ws_bytes, stream) -> int:
+    return int(library().dplr_hd_forward_packed(ctypes.byref(desc), R, block, n_slots, blocks, block_starts, slots,
+                                                context, _ref(q), _ref(k), _ref(v), _ref(decay), S, _ref(o), workspace,
+                                                ctypes.c_size_t(ws_bytes), stream))
+
+
+def dplr_hd_decode_step(desc, n_slots, slots, q, k, v, decay, S, o, status, stream) -> int:
+    return int(library().dplr_hd_decode_step(ctypes.byref(desc), n_slots, slots, _ref(q), _ref(k), _ref(v), _ref(decay),
+                                             S, _ref(o), status, stream))
+
+
+def _hd(t: torch.Tensor) -> dplr_hd_tensor:
+    """A [B,H,T,d] (or [B,H,T] gates) tensor with its own strides."""
+    st = t.stride()
+    return dplr_hd_tensor(t.data_ptr(), st[0], st[1], st[2])
+
+
+def _hd_rows(t: torch.Tensor) -> dplr_hd_tensor:
+    """A [tokens,H,d] (or [tokens,H] gates) tensor as one batch entry."""
+    st = t.stride()
+    return dplr_hd_tensor(t.data_ptr(), 0, st[1], st[0])
+
+
+def _hd_step(t: torch.Tensor) -> dplr_hd_tensor:
+    """A [rows,H,d] (or [rows,H] gates) tensor whose rows are batch entries of one token."""
+    st = t.stride()
+    return dplr_hd_tensor(t.data_ptr(), st[0], st[1], 0)
+
+
+_HEAD_GATES = lambda t: dplr_hd_tensor(t.data_ptr(), 0, 0, 0)  # noqa: E731
+
+
+def _need_view(t, name, device, dtype, shape, features=True):
+    """Like _need, for a tensor that may be strided (its feature axis contiguous)."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if features and t.numel() > 0:
+        if t.stride(-1) != 1:
+            raise ValueError(f"{name} must be contiguous along its last axis")
+        if any(n > 1 and (s <= 0 or s * t.element_size() % 16) for n, s in zip(t.shape[:-1], t.stride()[:-1])):
+            raise ValueError(f"{name} needs strides that are positive multiples of 16 bytes")
+        if t.data_ptr() % 16:
+            raise ValueError(f"{name} must start on a 16-byte boundary")
+
+
+class _HeadDecayBase:
+    def _setup(self, in_dtype, B, H, T, dk, dv, q_heads, per_head, device):
+        self.desc = make_hd_desc(in_dtype, B, H, T, dk, dv, q_heads, per_head)
+        st = dplr_hd_check(self.desc)
+        if st != DPLR_OK:
+            raise DplrError(st, "dplr_hd_check")
+        self.B, self.H, self.Hq, self.T, self.dk, self.dv = B, H, self.desc.Hq, T, dk, dv
+        self.in_dtype = torch.bfloat16 if self.desc.in_dtype == DPLR_BF16 else torch.float32
+        self.per_head = bool(per_head)
+        self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        if self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        self.path = dplr_hd_path(self.desc)
+
+    def _workspace(self, nbytes, name):
+        if nbytes == 0:
+            raise DplrError(DPLR_ERR_INVALID_ARG, name)
+        self.ws_bytes = nbytes
+        self.workspace = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)   # status word zeroed once
+
+    def _rows(self, heads, d, token_major, dtype=None):
+        B, T = self.B, self.T
+        dt = self.in_dtype if dtype is None else dtype
+        if token_major:
+            return torch.zeros((B, T, heads, d), dtype=dt, device=self.device).transpose(1, 2)
+        return torch.zeros((B, heads, T, d), dtype=dt, device=self.device)
+
+    def _stream(self, stream):
+        return (stream if stream is not None else torch.cuda.current_stream(self.device)).cuda_stream
+
+    def _gates(self, decay, shape, wrap):
+        if self.per_head:
+            _need(decay, "decay", self.device, torch.float32, (self.H,))
+            return _HEAD_GATES(decay)
+        _need_view(decay, "decay", self.device, torch.float32, shape, features=False)
+        if any(s < 0 for s in decay.stride()):
+            raise ValueError("decay needs non-negative strides")
+        return wrap(decay)
+
+    def device_status(self, clear: bool = False) -> int:
+        """The workspace's device status word (0, or DPLR_ERR_TIMEOUT after a bounded wait gave up), read
+        synchronously through dplr_la_read_status."""
+        with torch.cuda.device(self.device):
+            s = torch.cuda.current_stream(self.device)
+            st, word = dplr_la_read_status(_ptr(self.workspace), self.workspace.numel(), clear, s.cuda_stream)
+        if st != DPLR_OK:
+            raise DplrError(st, "dplr_la_read_status")
+        return word
+
+
+class HeadDecay(_HeadDecayBase):
+    """Prepared forward of linear attention with one decay per head (dplr_hd_forward): S_t = exp(g_t) S_{t-1} + k_t v_t^T,
+    o_t = S_t^T q_t. Owns the outputs o [B,H,T,dv] (the inputs' type; stored with the tokens before the heads if
+    `token_major`), S_T [B,H,dk,dv] fp32, and the workspace, so that repeated calls allocate nothing."""
+
+    def __init__(self, in_dtype, B: int, H: int, T: int, dk: int, dv: int, q_heads: Optional[int] = None,
+                 per_head: bool = False, token_major: bool = False, device: Optional[torch.device] = None):
+        self._setup(in_dtype, B, H, T, dk, dv, q_heads, per_head, device)
+        with torch.cuda.device(self.device):
+            self._workspace(dplr_hd_workspace_size(self.desc), "dplr_hd_workspace_size")
+            self.o = self._rows(H, dv, token_major)
+            self.S_T = torch.empty((B, H, dk, dv), dtype=torch.float32, device=self.device)
+
+    def __call__(self, q, k, v, decay, S0=None,
+                 stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+        """q, k [B,Hq,T,dk], v [B,H,T,dv], strided as they are; decay [B,H,T] fp32, or [H] with per_head."""
+        B, H, Hq, T, dev, dt = self.B, self.H, self.Hq, self.T, self.device, self.in_dtype
+        _need_view(q, "q", dev, dt, (B, Hq, T, self.dk))
+        _need_view(k, "k", dev, dt, (B, Hq, T, self.dk))
+        _need_view(v, "v", dev, dt, (B, H, T, self.dv))
+        g = self._gates(decay, (B, H, T), _hd)
+        if S0 is not None:
+            _need(S0, "S0", dev, torch.float32, (B, H, self.dk, self.dv))
+        with torch.cuda.device(dev):
+            st = dplr_hd_forward(self.desc, _hd(q), _hd(k), _hd(v), g, _ptr(S0), _hd(self.o), _ptr(self.S_T),
+                                 _ptr(self.workspace), self.ws_bytes, self._stream(stream))
+        if st != DPLR_OK:
+            raise DplrError(st, "dplr_hd_forward")
+        return self.o, self.S_T
+
+
+class HeadDecayBackward(_HeadDecayBase):
+    """Prepared backward of HeadDecay (dplr_hd_backward): owns the workspace and the gradients, q, k, v in the inputs'
+    type (token-major if asked for), decay ([B,H,T], or [H] with per_head) and S0 in fp32."""
+
+    def __init__(self, in_dtype, B: int, H: int, T: int, dk: int, dv: int, q_heads: Optional[int] = None,
+                 per_head: bool = False, token_major: bool = False, device: Optional[torch.device] = None):
+        self._setup(in_dtype, B, H, T, dk, dv, q_heads, per_head, device)
+        with torch.cuda.device(self.device):
+            self._workspace(dplr_hd_backward_workspace_size(self.desc), "dplr_hd_backward_workspace_size")
+            f = lambda *shape: torch.zeros(shape, dtype=torch.float32, device=self.device)  # noqa: E731
+            self.grads = {"q": self._rows(self.Hq, dk, token_major), "k": self._rows(self.Hq, dk, token_major),
+                          "v": self._rows(H, dv, token_major), "decay": f(H) if per_head else f(B, H, T),
+                          "S0": f(B, H, dk, dv)}
+
+    def __call__(self, dO, dST, q, k, v, decay, S0=None, decay_grad: bool = True,
+                 stream: Optional[torch.cuda.Stream] = None) -> dict:
+        """Gradients of HeadDecay's inputs (a dict, also kept in .grads) given dO [B,H,T,dv] in the inputs' type and
+        dST (fp32 or None: zero). Without `decay_grad` the gradient of the gates is not computed (and not returned)."""
+        B, H, Hq, T, dev, dt = self.B, self.H, self.Hq, self.T, self.device, self.in_dtype
+        _need_view(dO, "dO", dev, dt, (B, H, T, self.dv))
+        _need_view(q, "q", dev, dt, (B, Hq, T, self.dk))
+        _need_view(k, "k", dev, dt, (B, Hq, T, self.dk))
+        _need_view(v, "v", dev, dt, (B, H, T, self.dv))
+        g = self._gates(decay, (B, H, T), _hd)
+        for name, t in (("S0", S0), ("dST", dST)):
+            if t is not None:
+                _need(t, name, dev, torch.float32, (B, H, self.dk, self.dv))
+        G = self.grads
+        with torch.cuda.device(dev):
+            st = dplr_hd_backward(self.desc, _hd(q), _hd(k), _hd(v), g, _ptr(S0), _hd(dO), _ptr(dST), _hd(G["q"]),
+                                  _hd(G["k"]), _hd(G["v"]), _ptr(G["decay"]) if decay_grad else None, _ptr(G["S0"]),
+                                  _ptr(self.workspace), self.ws_bytes, self._stream(stream))
+        if st != DPLR_OK:
+            raise DplrError(st, "dplr_hd_backward")
+        return G if decay_grad else {n: t for n, t in G.items() if n != "decay"}
+
+
+class RequestPlan:
+    """Tables of a ragged batch of `requests` requests with up to `capacity` tokens, built on the GPU from their lengths
+    (dplr_hd_plan). Owns the tables: starts [R+1], blocks [capacity // block + R, 4], block_starts [R+1], token_slot and
+    token_pos [capacity], all int32."""
+
+    def __init__(self, requests: int, capacity: int, slots: int, block: int = 128,
+                 device: Optional[torch.device] = None):
+        self.R, self.capacity, self.n_slots, self.block = int(requests), int(capacity), int(slots), int(block)
+        self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        if self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        if self.R < 1 or self.capacity < 0 or self.block < 32 or self.block % 32 or self.n_slots < 1:
+            raise ValueError("RequestPlan needs requests >= 1, capacity >= 0, slots >= 1 and a block that is a multiple of 32")
+        f = lambda *shape: torch.full(shape, -1, dtype=torch.int32, device=self.device)  # noqa: E731
+        self.starts, self.block_starts = f(self.R + 1), f(self.R + 1)
+        self.blocks = f(self.capacity // self.block + self.R, 4)
+        self.token_slot, self.token_pos = f(self.capacity), f(self.capacity)
+        self.status = f(1)
+
+    @property
+    def tables(self) -> dict:
+        return {"starts": self.starts, "blocks": self.blocks, "block_starts": self.block_starts,
+                "token_slot": self.token_slot, "token_pos": self.token_pos}
+
+    def __call__(self, lengths, slots, context, stream: Optional[torch.cuda.Stream] = None) -> dict:
+        """lengths, slots, context: int32 [R] on the device. Returns the tables (see device_status for refused input)."""
+        for name, t in (("lengths", lengths), ("slots", slots), ("context", context)):
+            _need(t, name, self.device, torch.int32, (self.R,))
+        with torch.cuda.device(self.device):
+            s = stream if stream is not None else torch.cuda.current_stream(self.device)
+            st = dplr_hd_plan(self.R, self.capacity, self.block, self.n_slots, _ptr(lengths), _ptr(slots),
+                              _ptr(context), _ptr(self.starts), _ptr(self.blocks), _ptr(self.block_starts),
+                              _ptr(self.token_slot), _ptr(self.token_pos), _ptr(self.status), s.cuda_stream)
+        if st != DPLR_OK:
+            raise DplrError(st, "dplr_hd_plan")
+        self.slots, self.context = slots, context     # the packed forward reads them
+        return self.tables
+
+    def device_status(self) -> int:
+        """The last call's status word (DPLR_OK or DPLR_ERR_INVALID_ARG), read synchronously."""
+        return int(self.status.item())
+
+
+class HeadDecayPacked(_HeadDecayBase):
+    """Prepared forward of a ragged batch (dplr_hd_forward_packed) on a pool of states: `plan` (a RequestPlan; one is made
+    if none is given) says which rows belong to which request. Owns the output o [capacity,H,dv] (rows behind the last
+    token stay as they were) and the workspace."""
+
+    def __init__(self, in_dtype, requests: int, capacity: int, slots: int, H: int, dk: int, dv: int,
+                 q_heads: Optional[int] = None, per_head: bool = False, plan: Optional[RequestPlan] = None,
+                 device: Optional[torch.device] = None):
+        self._setup(in_dtype, 1, H, capacity, dk, dv, q_heads, per_head, device)
+        if plan is None:
+            plan = RequestPlan(requests, capacity, slots, default_block(self.desc, requests), self.device)
+        elif (plan.R, plan.capacity, plan.n_slots, plan.device) != (requests, capacity, slots, self.device):
+            raise ValueError("the plan is for another number of requests, capacity, slots or device")
+        self.plan, self.n_slots = plan, int(slots)
+        with torch.cuda.device(self.device):
+            self._workspace(dplr_hd_packed_workspace_size(self.desc, plan.R, plan.block), "dplr_hd_packed_workspace_size")
+            self.o = torch.zeros((capacity, H, dv), dtype=self.in_dtype, device=self.device)
+
+    def __call__(self, q, k, v, decay, S, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+        """q, k [capacity,Hq,dk], v [capacity,H,dv], decay [capacity,H] fp32 or [H]; S [slots,H,dk,dv] fp32 is updated."""
+        p, n, dev, dt = self.plan, self.T, self.device, self.in_dtype
+        if not hasattr(p, "slots"):
+            raise ValueError("call the plan first: it makes the tables")
+        _need_view(q, "q", dev, dt, (n, self.Hq, self.dk))
+        _need_view(k, "k", dev, dt, (n, self.Hq, self.dk))
+        _need_view(v, "v", dev, dt, (n, self.H, self.dv))
+        g = self._gates(decay, (n, self.H), _hd_rows)
+        _need(S, "S", dev, torch.float32, (self.n_slots, self.H, self.dk, self.dv))
+        with torch.cuda.device(dev):
+            st = dplr_hd_forward_packed(self.desc, p.R, p.block, self.n_slots, _ptr(p.blocks), _ptr(p.block_starts),
+                                        _ptr(p.slots), _ptr(p.context), _hd_rows(q), _hd_rows(k), _hd_rows(v), g,
+                                        _ptr(S), _hd_rows(self.o), _ptr(self.workspace), self.ws_bytes,
+                                        self._stream(stream))
+        if st != DPLR_OK:
+            raise DplrError(st, "dplr_hd_forward_packed")
+        return self.o
+
+
+def default_block(desc: dplr_hd_desc, requests: int) -> int:
+    """Tokens per block of a ragged batch: long enough that few requests need the extra pass over their keys and values
+    which every block but a request's last costs."""
+    return 1024
+
+
+class HeadDecayDecode(_HeadDecayBase):
+    """Prepared one-token step for `rows` rows on a pool of states (dplr_hd_decode_step): owns the output o [rows,H,dv]."""
+
+    def __init__(self, in_dtype, rows: int, H: int, dk: int, dv: int, slots: int, q_heads: Optional[int] = None,
+                 per_head: bool = False, device: Optional[torch.device] = None):
+        self._setup(in_dtype, rows, H, 1, dk, dv, q_heads, per_head, device)
+        self.n_slots = int(slots)
+        self.o = torch.zeros((rows, H, dv), dtype=self.in_dtype, device=self.device)
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+
+    def device_status(self, clear: bool = False) -> int:
+        """DPLR_ERR_INVALID_ARG if a row's slot was out of range or an earlier row's since the word was cleared."""
+        word = int(self.status.item())
+        if clear:
+            self.status.zero_()
+        return word
+
+    def __call__(self, q, k, v, decay, S, slots, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+        """q, k [rows,Hq,dk], v [rows,H,dv], decay [rows,H] fp32 or [H]; S [slots,H,dk,dv] fp32 is updated in place;
+        slots [rows] int32: each row's state, -1 for a row without one."""
+        n, dev, dt = self.B, self.device, self.in_dtype
+        _need_view(q, "q", dev, dt, (n, self.Hq, self.dk))
+        _need_view(k, "k", dev, dt, (n, self.Hq, self.dk))
+        _need_view(v, "v", dev, dt, (n, self.H, self.dv))
+        g = self._gates(decay, (n, self.H), _hd_step)
+        _need(S, "S", dev, torch.float32, (self.n_slots, self.H, self.dk, self.dv))
+        _need(slots, "slots", dev, torch.int32, (n,))
+        with torch.cuda.device(dev):
+            st = dplr_hd_decode_step(self.desc, self.n_slots, _ptr(slots), _hd_step(q), _hd_step(k), _hd_step(v), g,
+                                     _ptr(S), _hd_step(self.o), _ptr(self.status), self._stream(stream))
+        if st != DPLR_OK:
+            raise DplrError(st, "dplr_hd_decode_step")
+        return self.o

@@ -1,0 +1,172 @@
+"""Linear attention with one decay per head: refusals of the C ABI (nothing is launched, no GPU), and the float64 reference
+of the GPU tests against the framework's own oracle and against differences."""
+
+import numpy as np
+import pytest
+
+import head_decay_reference as ref
+import oracle
+
+FAKE = 1 << 20   # aligned, never dereferenced: every check comes before the first launch
+
+
+@pytest.fixture(scope="module")
+def sdl():
+    from structured_decay_linear_gb300 import build as nvbuild
+    nvbuild.build()
+    import structured_decay_linear_gb300 as s
+    s.library()
+    return s
+
+
+def tensor(sdl, B, H, T, d, data=FAKE, **kw):
+    v = dict(sb=H * T * d, sh=T * d, st=d)
+    v.update(kw)
+    return sdl.dplr_hd_tensor(data, v["sb"], v["sh"], v["st"])
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(), 0), (dict(q_heads=2), 0), (dict(q_heads=3), 1), (dict(q_heads=0), 1), (dict(T=0), 0), (dict(T=-1), 1),
+    (dict(B=0), 1), (dict(dk=48), 2), (dict(dv=256), 2), (dict(dk=0), 1), (dict(B=1 << 14, H=1 << 10, T=1), 2),
+    (dict(B=1, H=4, T=1 << 29), 2), (dict(dt="f32", dk=32, dv=32), 0)])
+def test_descriptors(sdl, kw, expect):
+    v = dict(B=2, H=4, T=100, dk=64, dv=128, dt="bf16", q_heads=None)
+    v.update(kw)
+    d = sdl.make_hd_desc(v["dt"], v["B"], v["H"], v["T"], v["dk"], v["dv"], v["q_heads"])
+    assert sdl.dplr_hd_check(d) == expect
+    sizes = (sdl.dplr_hd_workspace_size(d), sdl.dplr_hd_backward_workspace_size(d))
+    assert all(n >= 256 and n % 256 == 0 for n in sizes) if expect == 0 else sizes == (0, 0)
+    assert (sdl.dplr_hd_path(d) != "") == (expect == 0)
+
+
+def test_bad_enums(sdl):
+    d = sdl.make_hd_desc("bf16", 1, 1, 8, 64, 64)
+    d.in_dtype = 7
+    assert sdl.dplr_hd_check(d) == 1
+    d = sdl.make_hd_desc("bf16", 1, 1, 8, 64, 64)
+    d.per_head = 2
+    assert sdl.dplr_hd_check(d) == 1
+    assert sdl.library().dplr_hd_check(None) == 1
+
+
+def forward(sdl, d, **kw):
+    B, H, Hq, T, dk, dv = d.B, d.H, d.Hq, d.T, d.dk, d.dv
+    a = dict(q=tensor(sdl, B, Hq, T, dk), k=tensor(sdl, B, Hq, T, dk), v=tensor(sdl, B, H, T, dv),
+             decay=sdl.dplr_hd_tensor(FAKE, H * T, T, 1), S0=FAKE, o=tensor(sdl, B, H, T, dv), S_T=FAKE, ws=FAKE,
+             nbytes=sdl.dplr_hd_workspace_size(d))
+    a.update(kw)
+    return sdl.dplr_hd_forward(d, a["q"], a["k"], a["v"], a["decay"], a["S0"], a["o"], a["S_T"], a["ws"], a["nbytes"],
+                               None)
+
+
+def test_forward_refuses(sdl):
+    d = sdl.make_hd_desc("bf16", 2, 4, 100, 64, 128, 2)
+    bad = lambda heads, dim: [  # noqa: E731
+        None, tensor(sdl, 2, heads, 100, dim, data=None), tensor(sdl, 2, heads, 100, dim, data=FAKE + 8),
+        tensor(sdl, 2, heads, 100, dim, sb=0), tensor(sdl, 2, heads, 100, dim, sh=-64),
+        tensor(sdl, 2, heads, 100, dim, st=dim + 4)]
+    for name, heads, dim in (("q", 2, 64), ("k", 2, 64), ("v", 4, 128), ("o", 4, 128)):
+        for t in bad(heads, dim):
+            assert forward(sdl, d, **{name: t}) == 1, name
+        assert forward(sdl, d, **{name: tensor(sdl, 2, heads, 100, dim, sb=1 << 42)}) == 2
+    assert forward(sdl, d, o=tensor(sdl, 2, 4, 100, 128, st=64)) == 1            # rows of o on top of each other
+    assert forward(sdl, d, o=tensor(sdl, 2, 4, 100, 128, sh=99 * 128)) == 1
+    for t in (None, sdl.dplr_hd_tensor(FAKE + 2, 400, 100, 1), sdl.dplr_hd_tensor(FAKE, 400, 100, -1),
+              sdl.dplr_hd_tensor(FAKE, -400, 100, 1)):
+        assert forward(sdl, d, decay=t) == 1
+    assert forward(sdl, d, S0=FAKE + 4) == 1 and forward(sdl, d, S_T=FAKE + 8) == 1
+    need = sdl.dplr_hd_workspace_size(d)
+    assert forward(sdl, d, nbytes=need - 1) == 3 and forward(sdl, d, ws=None) == 3 and forward(sdl, d, ws=FAKE + 16) == 3
+
+
+def test_backward_refuses(sdl):
+    d = sdl.make_hd_desc("bf16", 2, 4, 100, 64, 128, 2)
+    kq, vv = tensor(sdl, 2, 2, 100, 64), tensor(sdl, 2, 4, 100, 128)
+    names = ["q", "k", "v", "decay", "S0", "dO", "dST", "dq", "dk", "dv", "ddecay", "dS0", "ws", "nbytes"]
+    base = [kq, kq, vv, sdl.dplr_hd_tensor(FAKE, 400, 100, 1), FAKE, vv, FAKE, kq, kq, vv, FAKE, FAKE, FAKE,
+            sdl.dplr_hd_backward_workspace_size(d)]
+
+    def call(**kw):
+        return sdl.dplr_hd_backward(d, *[kw.get(n, b) for n, b in zip(names, base)], None)
+
+    for n in ("q", "k", "v", "decay", "dO", "dq", "dk", "dv"):
+        assert call(**{n: None}) == 1, n
+    for n in ("dq", "dk"):
+        assert call(**{n: tensor(sdl, 2, 2, 100, 64, sh=64)}) == 1               # overlapping rows
+    for n in ("S0", "dST", "dS0"):
+        assert call(**{n: FAKE + 4}) == 1
+    assert call(ddecay=FAKE + 2) == 1
+    assert call(nbytes=base[-1] - 1) == 3 and call(ws=None) == 3 and call(ws=FAKE + 32) == 3
+
+
+def test_plan_refuses(sdl):
+    def call(R=4, cap=100, block=128, slots=8, **kw):
+        names = ["lengths", "slots", "context", "starts", "blocks", "block_starts", "token_slot", "token_pos", "status"]
+        return sdl.dplr_hd_plan(R, cap, block, slots, *[kw.get("p_" + n, FAKE) for n in names], None)
+
+    assert call(R=0) == 1 and call(cap=-1) == 1 and call(block=0) == 1 and call(slots=0) == 1
+    assert call(R=8193) == 2 and call(cap=1 << 30) == 2 and call(block=100) == 2 and call(slots=(1 << 20) + 1) == 2
+    for n in ("lengths", "slots", "context", "starts", "blocks", "block_starts", "token_slot", "token_pos", "status"):
+        assert call(**{"p_" + n: None}) == 1 and call(**{"p_" + n: FAKE + 2}) == 1, n
+    assert call(p_blocks=FAKE + 4) == 1
+
+
+def test_packed_and_decode_refuse(sdl):
+    d = sdl.make_hd_desc("bf16", 1, 4, 100, 64, 128, 2)
+    kq, vv, g = tensor(sdl, 1, 2, 100, 64), tensor(sdl, 1, 4, 100, 128), sdl.dplr_hd_tensor(FAKE, 0, 100, 1)
+    assert sdl.dplr_hd_packed_workspace_size(d, 3, 100) == 0 and sdl.dplr_hd_packed_workspace_size(d, 0, 128) == 0
+    assert sdl.dplr_hd_packed_workspace_size(sdl.make_hd_desc("bf16", 2, 4, 100, 64, 128, 2), 3, 128) == 0
+    small, large = (sdl.dplr_hd_packed_workspace_size(d, 3, b) for b in (128, 64))
+    assert small == 256 and large > (1 + 3) * 4 * 64 * 128 * 4
+
+    def packed(R=3, block=64, slots=8, tables=(FAKE,) * 4, q=kq, k=kq, v=vv, decay=g, S=FAKE, o=vv, ws=FAKE, n=large):
+        return sdl.dplr_hd_forward_packed(d, R, block, slots, *tables, q, k, v, decay, S, o, ws, n, None)
+
+    for i in range(4):
+        assert packed(tables=[None if j == i else FAKE for j in range(4)]) == 1
+    assert packed(R=0) == 1 and packed(block=48) == 1 and packed(slots=0) == 1 and packed(S=None) == 1
+    assert packed(q=None) == 1 and packed(o=None) == 1 and packed(decay=None) == 1 and packed(n=large - 1) == 3
+    assert packed(S=FAKE + 4) == 1 and packed(ws=None) == 3
+
+    one = sdl.make_hd_desc("bf16", 5, 4, 1, 64, 128, 2)
+    kq, vv, g = tensor(sdl, 5, 2, 1, 64), tensor(sdl, 5, 4, 1, 128), sdl.dplr_hd_tensor(FAKE, 4, 1, 0)
+
+    def decode(desc=one, n=8, slots=FAKE, q=kq, k=kq, v=vv, decay=g, S=FAKE, o=vv, status=None):
+        return sdl.dplr_hd_decode_step(desc, n, slots, q, k, v, decay, S, o, status, None)
+
+    assert decode(desc=d) == 1 and decode(n=0) == 1 and decode(slots=None) == 1 and decode(S=None) == 1
+    assert decode(slots=FAKE + 1) == 1 and decode(status=FAKE + 1) == 1
+    assert all(decode(**{n: None}) == 1 for n in ("q", "k", "v", "decay", "o"))
+
+
+# ---- the reference itself
+
+def inputs(B=1, H=2, Hq=2, T=20, dk=32, dv=32, seed=0):
+    r = np.random.default_rng(seed)
+    return dict(q=r.standard_normal((B, Hq, T, dk)), k=r.standard_normal((B, Hq, T, dk)) / dk ** 0.5,
+                v=r.standard_normal((B, H, T, dv)), g=-0.3 * r.random((B, H, T)), S0=r.standard_normal((B, H, dk, dv)))
+
+
+def test_reference_is_the_oracle_without_a_low_rank_term():
+    """Generic mode with A = B = 0 and the same decay in every channel, float32 inputs (so that both read the same)."""
+    x = {n: v.astype(np.float32) for n, v in inputs().items()}
+    o, S, _, _ = ref.forward(**x)
+    B, H, T, dk = x["q"].shape
+    decay = np.broadcast_to(x["g"][..., None], (B, H, T, dk)).copy()
+    zero = np.zeros((B, H, T, 1, dk), np.float32)
+    o2, S2 = oracle.forward("generic", x["q"], None, None, decay, None, A=zero, Bm=zero, K=x["k"][:, :, :, None].copy(),
+                            V=x["v"][:, :, :, None].copy(), S0=x["S0"])
+    assert np.abs(o - o2).max() <= 1e-10 * np.abs(o).max() and np.abs(S - S2).max() <= 1e-10 * np.abs(S).max()
+
+
+def test_reference_gradients_against_differences():
+    x = inputs(H=4, Hq=2, T=7, dk=3, dv=5, seed=1)
+    r = np.random.default_rng(2)
+    dO, dST = r.standard_normal((1, 4, 7, 5)), r.standard_normal((1, 4, 3, 5))
+    got = ref.backward(x["q"], x["k"], x["v"], x["g"], dO, dST, x["S0"])
+    loss = lambda y: (ref.forward(**y)[0] * dO).sum() + (ref.forward(**y)[1] * dST).sum()  # noqa: E731
+    for n, name in (("q", "q"), ("k", "k"), ("v", "v"), ("g", "decay"), ("S0", "S0")):
+        u = r.standard_normal(x[n].shape)
+        hi, lo = dict(x), dict(x)
+        hi[n], lo[n] = x[n] + 1e-6 * u, x[n] - 1e-6 * u
+        assert abs((loss(hi) - loss(lo)) / 2e-6 - (got[name] * u).sum()) <= 1e-6 * np.linalg.norm(got[name])
