@@ -91,6 +91,21 @@ bool tensor_map_2d(CUtensorMap* map, const void* base, bool bf16, uint64_t rows,
     return true;
 }
 
+bool tensor_map_rows(CUtensorMap* map, const void* base, int D, long long T, int heads, int B, long long st, long long sh,
+                     long long sb, uint32_t box_rows) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)T, (cuuint64_t)heads, (cuuint64_t)B};
+    cuuint64_t strides[3] = {(cuuint64_t)st * 2, (cuuint64_t)sh * 2, (cuuint64_t)sb * 2};
+    cuuint32_t box[4] = {64, box_rows, 1, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+long long wait_limit() { return g_wait_cycles.load(std::memory_order_relaxed); }
+
 dplr_status make_plan(const dplr_desc* d, Plan* pl) {
     if (!d) return DPLR_ERR_INVALID_ARG;
     if (d->mode != DPLR_GDN && d->mode != DPLR_HDLA && d->mode != DPLR_GENERIC) return DPLR_ERR_INVALID_ARG;

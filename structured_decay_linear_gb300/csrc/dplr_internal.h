@@ -81,6 +81,15 @@ cudaError_t launch_state_scan(const Plan& pl, const ScanArgs& a, cudaStream_t s)
 bool tensor_map_2d(CUtensorMap* map, const void* base, bool bf16, uint64_t rows, uint64_t cols, uint32_t box_rows,
                    uint32_t box_cols);
 
+// A 4-D tensor map of bf16 rows [B][heads][T][D] with element strides sb, sh, st (features contiguous), read in
+// 128-byte-swizzled boxes of 64 features x box_rows tokens of one head; tokens past T read as zero. Encoded anew on
+// every call.
+bool tensor_map_rows(CUtensorMap* map, const void* base, int D, long long T, int heads, int B, long long st, long long sh,
+                     long long sb, uint32_t box_rows);
+
+// The limit (SM cycles) of a kernel's bounded waits: dplr_la_set_wait_limit's, or the default.
+long long wait_limit();
+
 // Tensor-core HDLA path (bf16 inputs, dk = dv = 128): chunk maps, then the chain over chunks.
 bool hdla_tc_supported(const Plan& pl);
 void hdla_tc_offsets(const Plan& pl, size_t* off_P, size_t* off_c, size_t* off_Q, size_t* total);

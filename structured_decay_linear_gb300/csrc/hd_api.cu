@@ -98,13 +98,23 @@ Cut cut(int T, int want, int unit, int least, int most) {
 // CTAs that one segment per sequence gives a pass over a state of DZ columns.
 long long base_ctas(const dplr_hd_desc* d, int DZ) { return (long long)d->B * d->H * (DZ / fp32_zblock(DZ)); }
 
+bool on_tensor_cores(const dplr_hd_desc* d) { return tc_supported(d->in_dtype == DPLR_BF16, d->dk, d->dv); }
+
 Cut forward_cut(const dplr_hd_desc* d) {
+    if (on_tensor_cores(d)) {
+        const long long want = kSMs / ((long long)d->B * d->H);
+        return cut(d->T, want < 1 ? 1 : (int)want, kChunk, 512, 0);
+    }
     const long long target = 2LL * kSMs;
     const long long want = target / base_ctas(d, d->dv);
     return cut(d->T, want < 1 ? 1 : (int)want, 32, 128, 0);
 }
 
 Cut backward_cut(const dplr_hd_desc* d) {
+    if (on_tensor_cores(d)) {
+        const long long want = kSMs / ((long long)d->B * d->H);
+        return cut(d->T, want < 1 ? 1 : (int)want, kChunk, 256, 512);
+    }
     const long long target = 2LL * kSMs;
     const long long want = target / base_ctas(d, d->dv);
     return cut(d->T, want < 1 ? 1 : (int)want, 32, 128, 512);
@@ -132,7 +142,7 @@ struct BackwardPlan { Cut c; int nzq; size_t fwd, bwd, gsum, dotq, dotk, seg, pa
 BackwardPlan backward_plan(const dplr_hd_desc* d) {
     BackwardPlan p{};
     p.c = backward_cut(d);
-    p.nzq = d->dk / fp32_zblock(d->dk);
+    p.nzq = on_tensor_cores(d) ? 1 : d->dk / fp32_zblock(d->dk);
     const size_t bh = (size_t)d->B * d->H, tok = bh * d->T;
     size_t off = kAlign;
     auto take = [&](size_t bytes) { const size_t at = off; off = up(off + bytes); return at; };
@@ -167,7 +177,9 @@ Pass base_pass(const Gates& g, int dv, int DX, int DZ, bool transposed) {
 
 void output(Pass& p, const View& o) { p.o = const_cast<void*>(o.p); p.ob = o.sb; p.oh = o.sh; p.ot = o.st; }
 
-cudaError_t launch(const Launch& a, cudaStream_t s) { return launch_fp32(a, s); }
+cudaError_t launch(const Launch& a, bool tensor_cores, cudaStream_t s) {
+    return tensor_cores ? launch_tc(a, s) : launch_fp32(a, s);
+}
 
 cudaError_t copy_state(float* dst, const float* src, size_t bytes, cudaStream_t s) {
     if (!dst || dst == src) return cudaSuccess;
@@ -190,7 +202,7 @@ dplr_status dplr_hd_check(const dplr_hd_desc* desc) { return check_desc(desc); }
 
 const char* dplr_hd_path(const dplr_hd_desc* desc) {
     if (check_desc(desc) != DPLR_OK) return "";
-    return "hd_fp32";
+    return on_tensor_cores(desc) ? "hd_tcgen05" : "hd_fp32";
 }
 
 size_t dplr_hd_workspace_size(const dplr_hd_desc* desc) {
@@ -221,6 +233,7 @@ dplr_status dplr_hd_forward(const dplr_hd_desc* desc, const dplr_hd_tensor* q, c
     a.geo = dense(desc, pl.c);
     a.B = desc->B; a.bf16 = desc->in_dtype == DPLR_BF16; a.npass = 1;
     a.status = static_cast<int*>(workspace);
+    a.wait_cycles = wait_limit();
     Pass& p = a.pass[0];
     p = base_pass(g, desc->dv, desc->dk, desc->dv, false);
     p.x = vq; p.y = vk; p.z = vv;
@@ -228,7 +241,7 @@ dplr_status dplr_hd_forward(const dplr_hd_desc* desc, const dplr_hd_tensor* q, c
         p.bound = reinterpret_cast<float*>(ws + pl.bound);
         p.gsum = reinterpret_cast<float*>(ws + pl.gsum);
         p.states_only = 1;
-        HD_CUDA(launch(a, s));
+        HD_CUDA(launch(a, on_tensor_cores(desc), s));
         Scan sc{};
         sc.geo = a.geo; sc.B = desc->B; sc.dk = desc->dk; sc.dv = desc->dv;
         sc.fwd = p.bound; sc.fwd_ext = S0; sc.gsum = p.gsum;
@@ -237,7 +250,7 @@ dplr_status dplr_hd_forward(const dplr_hd_desc* desc, const dplr_hd_tensor* q, c
     }
     p.ext_in = S0; p.ext_out = S_T;
     output(p, vo);
-    HD_CUDA(launch(a, s));
+    HD_CUDA(launch(a, on_tensor_cores(desc), s));
     return DPLR_OK;
 }
 
@@ -279,6 +292,7 @@ dplr_status dplr_hd_backward(const dplr_hd_desc* desc, const dplr_hd_tensor* q, 
     a.geo = dense(desc, pl.c);
     a.B = desc->B; a.bf16 = desc->in_dtype == DPLR_BF16;
     a.status = static_cast<int*>(workspace);
+    a.wait_cycles = wait_limit();
     const int K = desc->dk, V = desc->dv;
     if (many) {
         a.npass = 2;
@@ -290,7 +304,7 @@ dplr_status dplr_hd_backward(const dplr_hd_desc* desc, const dplr_hd_tensor* q, 
         b = base_pass(g, V, K, V, false);
         b.y = vq; b.z = vdo; b.reverse = 1; b.bound = at(pl.bwd);
         b.states_only = 1;
-        HD_CUDA(launch(a, s));
+        HD_CUDA(launch(a, on_tensor_cores(desc), s));
         Scan sc{};
         sc.geo = a.geo; sc.B = desc->B; sc.dk = K; sc.dv = V;
         sc.fwd = at(pl.fwd); sc.fwd_ext = S0; sc.upto_end = 1;
@@ -327,7 +341,7 @@ dplr_status dplr_hd_backward(const dplr_hd_desc* desc, const dplr_hd_tensor* q, 
         pq.w = vq; pq.dots = at(pl.dotq);
         pk.w = vk; pk.dots = at(pl.dotk);
     }
-    HD_CUDA(launch(a, s));
+    HD_CUDA(launch(a, on_tensor_cores(desc), s));
     if (ddecay) {
         GateGrad gg{};
         gg.B = desc->B; gg.H = desc->H; gg.T = desc->T; gg.nseg = pl.c.nseg; gg.L = pl.c.L; gg.dk = K; gg.dv = V;
@@ -390,6 +404,7 @@ dplr_status dplr_hd_forward_packed(const dplr_hd_desc* desc, int32_t R, int32_t 
     a.geo.n_slots = n_slots;
     a.B = 1; a.bf16 = desc->in_dtype == DPLR_BF16; a.max_blocks = (int)max_blocks; a.npass = 1;
     a.status = static_cast<int*>(workspace);
+    a.wait_cycles = wait_limit();
     Pass& p = a.pass[0];
     p = base_pass(g, desc->dv, desc->dk, desc->dv, false);
     p.x = vq; p.y = vk; p.z = vv;
@@ -398,7 +413,7 @@ dplr_status dplr_hd_forward_packed(const dplr_hd_desc* desc, int32_t R, int32_t 
         p.bound = reinterpret_cast<float*>(ws + kAlign);
         p.gsum = reinterpret_cast<float*>(ws + up(kAlign + n * state_bytes(desc)));
         p.states_only = 1;
-        HD_CUDA(launch(a, s));
+        HD_CUDA(launch(a, on_tensor_cores(desc), s));
         Scan sc{};
         sc.geo = a.geo; sc.B = 1; sc.R = R; sc.dk = desc->dk; sc.dv = desc->dv;
         sc.fwd = p.bound; sc.fwd_ext = S; sc.gsum = p.gsum;
@@ -407,7 +422,7 @@ dplr_status dplr_hd_forward_packed(const dplr_hd_desc* desc, int32_t R, int32_t 
     }
     p.ext_in = S; p.ext_out = S;
     output(p, vo);
-    HD_CUDA(launch(a, s));
+    HD_CUDA(launch(a, on_tensor_cores(desc), s));
     return DPLR_OK;
 }
 

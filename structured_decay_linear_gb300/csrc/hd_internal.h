@@ -123,6 +123,10 @@ cudaError_t launch_decode(const View& q, const View& k, const View& v, const flo
 int fp32_zblock(int DZ);
 cudaError_t launch_fp32(const Launch& a, cudaStream_t s);
 
+// Tensor-core kernels: bf16, head sizes 64 and 128; one CTA per segment of one (batch, head).
+bool tc_supported(bool bf16, int dk, int dv);
+cudaError_t launch_tc(const Launch& a, cudaStream_t s);
+
 // Turns segments' own contributions into boundary states, in place. Forward: the contribution of segment i lies at
 // boundary i + 1, and boundary 0 is ext (or zero); backward: that of segment i at boundary i, boundary nseg is ext.
 // Both arrays may be given (the gradient's two scans in one launch). `upto_end`: forward goes on to boundary nseg.

@@ -1,0 +1,690 @@
+// Linear attention with one decay per head on the tensor cores: bf16 rows, DX and DZ in {64, 128}, both directions of
+// time, dense and ragged batches (hd_internal.h has the operator).
+//
+// One CTA walks a segment of one (batch, head) in chunks of 128 tokens and keeps the fp32 state R [DX][DZ] in tensor
+// memory (lane i, column j) for the whole segment. G: inclusive cumulative log-gates of the chunk, n its tokens,
+//   D  = X Y^T                                  (tcgen05 M = 128, N = 128, K = DX)
+//   P  = D . e^{G_r - G_c} (c <= r)             (CUDA cores; back into tensor memory as bf16)    backward: e^{G_c - G_r}, c >= r
+//   Op = P Z                                    (M = 128, N = DZ, K = 128; A in tensor memory)
+//   Oi = X R                                    (M = 128, N = DZ, K = DX; R as bf16 in shared memory)
+//   o  = e^{G_r} Oi + Op                        (CUDA cores)                                     backward: e^{G_n - G_r}
+//   R <- e^{G_n} R + Y~^T Z, Y~_c = e^{G_n - G_c} y_c (M = DX, N = DZ, K = 128, fp32 accumulator) backward: Y~_c = e^{G_c} y_c
+//
+// Roundings. x, y, z are bf16 already: D is exact up to fp32 accumulation. Y~ enters the state, which is returned and
+// carried over whole sequences in fp32, as two bf16 parts (hi + lo, 2^-17). P and the R in front of the readout are
+// rounded to bf16 once: they only reach o, which is rounded to bf16 itself. Where per-token dots of the unrounded o
+// are asked for (the gradient of the gates is a sum in which they nearly cancel), P and R have two parts too (SPLIT).
+//
+// Exponents. Sums of gates are formed in 64 bits (in units of log2) and kept as fp32 offsets from the start of blocks
+// of 32 tokens, with the differences of the starts: the exponent of a pair is accurate however much was forgotten
+// before both, and never positive, so nothing overflows for any gate.
+//
+// Work split: three groups of four warps (thread = lane of tensor memory) and three single warps:
+//   A  the state: R to bf16 in shared memory, e^{G_n} R back        B  Y~ from Y
+//   C  P from D, then o from Oi and Op                              copies (TMA), MMA issue, gates
+// The issuer's order within a chunk, D Oi R Op, leaves the CUDA-core phases of a chunk under the other products.
+// Each row sequence is read once by TMA in the 128-byte swizzle; the same tile serves K-major (D, Oi) and MN-major (Op,
+// R) operands. x and y have one buffer, z two (one with SPLIT): x and y are free again early in a chunk.
+//
+// A pass for states only (the segments' own contributions) walks the chunks from the far end, so that the weights
+// e^{(gates behind the token)} need no rescaling of R: its accumulator is touched by MMAs alone, and all three groups
+// form Y~.
+//
+// Bound: by the bytes of x, y, z and o (1 KB a token and head at 128 x 128): a chunk is 128 KB, 5.6 K cycles of its
+// share of HBM bandwidth on 152 SMs, against 2.6 K cycles of products and about 2.5 K of each group's work.
+#include <cstring>
+
+#include "hd_internal.h"
+#include "tc_common.cuh"
+
+namespace dplr {
+namespace hd {
+namespace {
+
+using namespace tc;
+
+constexpr int C = kChunk;                  // 128
+constexpr int kGrp = 128;
+constexpr int NT = 3 * kGrp + 96;          // groups A, B, C; warps 12 (copies), 13 (MMA issue), 14 (gates)
+constexpr uint32_t kHalf = C * 128;        // bytes of a half tile: 128 rows of 64 bf16
+constexpr uint32_t TM_R = 0, TM_D = 128, TM_OI = 256, TM_OP = 384, kTmemCols = 512;
+constexpr double kLog2e = 1.4426950408889634;
+
+struct alignas(128) Args {
+    CUtensorMap map[3][3];    // [pass][x, y, z]
+    Launch l;
+};
+
+// Per-chunk gate values (fp32, log2 units), double-buffered.
+struct GateBuf {
+    float rc[C];        // G_t minus its block's start
+    float ad[4][4];     // start of block i minus start of block j
+    float an[4];        // block start (plus what lies in front of the chunk, in a states pass backward in time)
+    float tn[4];        // chunk end minus block start (plus what lies behind the chunk, in a states pass)
+    float en;           // e^{G_n}
+    float pad[7];
+};
+static_assert(sizeof(GateBuf) % 16 == 0, "16-byte rows");
+
+template <int DX, int DZ, bool SPLIT, bool STATES>
+struct Layout {
+    static constexpr int XB = DX * 256, ZB = DZ * 256;        // bytes of a tile: D / 64 half tiles
+    static constexpr int NZ = (SPLIT && !STATES) ? 1 : 2;     // z buffers
+    static constexpr int NY = STATES ? 2 : 1;                 // y buffers (a states pass has no x)
+    static constexpr int RB = STATES ? 0 : DX * DZ * 2;       // R as bf16: DZ / 64 halves of DX rows of 128 bytes
+    static constexpr int T_X = 0;
+    static constexpr int T_Y = T_X + (STATES ? 0 : XB);
+    static constexpr int T_YH = T_Y + NY * XB;
+    static constexpr int T_YL = T_YH + XB;
+    static constexpr int T_Z = T_YL + XB;                     // (a 64-feature Y~ read as M = 128 runs into what follows)
+    static constexpr int T_R = T_Z + NZ * ZB;
+    static constexpr int GATES = T_R + RB * (SPLIT ? 2 : 1);
+    static constexpr int BARS = GATES + 2 * (int)sizeof(GateBuf);
+    static constexpr int TOTAL = BARS + 256;
+    static_assert(TOTAL <= 227 * 1024, "shared memory budget");
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 4-D tiled copy: 64 features x 128 tokens of one head.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int c0, int t, int h, int b, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+        :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(t), "r"(h), "r"(b), "r"(smem_addr(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32_nowait(uint32_t taddr, const float (&v)[32]) {
+    uint32_t r[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(v[i]);
+    tmem_st16(taddr, r);
+    tmem_st16(taddr + 16, r + 16);
+}
+
+// The y rows of a chunk times their weights, as hi + lo, by `nt` threads; rows from n on become zero whatever they hold.
+template <int DX>
+__device__ __forceinline__ void scale_rows(uint32_t ty, uint32_t th, uint32_t tl, const GateBuf& g, bool rev, int n, int tid,
+                                           int nt) {
+    constexpr int PER = DX / 8;     // 16-byte pieces of a row
+#pragma unroll 4
+    for (int i = tid; i < C * PER; i += nt) {
+        const int t = i / PER, c = i % PER, blk = t >> 5;
+        const float w = ex2(rev ? g.an[blk] + g.rc[t] : g.tn[blk] - g.rc[t]);
+        const uint32_t off = (uint32_t)(c >> 3) * kHalf + swz(t, c & 7);
+        uint32_t u[4];
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "r"(ty + off));
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            split2(__uint_as_float(u[e] << 16) * w, __uint_as_float(u[e] & 0xFFFF0000u) * w, h[e], l[e]);
+            if (t >= n) h[e] = l[e] = 0u;
+        }
+        sts128(th + off, h[0], h[1], h[2], h[3]);
+        sts128(tl + off, l[0], l[1], l[2], l[3]);
+    }
+}
+
+// Rows n .. 127 of a z tile become zero: they may belong to another request and hold anything.
+template <int DZ>
+__device__ __forceinline__ void clear_rows(uint32_t tz, int n, int tid, int nt) {
+    constexpr int PER = DZ / 8;
+    for (int i = n * PER + tid; i < C * PER; i += nt) {
+        const int t = i / PER, c = i % PER;
+        sts128(tz + (uint32_t)(c >> 3) * kHalf + swz(t, c & 7), 0u, 0u, 0u, 0u);
+    }
+}
+
+template <int DX, int DZ, bool SPLIT, bool STATES>
+__global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Args a) {
+    using Ly = Layout<DX, DZ, SPLIT, STATES>;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    const uint32_t sb = smem_addr(smem);
+    const Pass& p = a.l.pass[blockIdx.y];
+    const CUtensorMap* maps = a.map[blockIdx.y];
+    if (sb & 1023u) {   // the swizzled tiles need 1024-byte alignment
+        if (threadIdx.x == 0) atomicExch(a.l.status, (int)DPLR_ERR_CUDA);
+        return;
+    }
+    Segment sg;
+    if (!locate(a.l.geo, blockIdx.x, sg)) return;
+    if (p.states_only == 1 && (p.reverse ? sg.first : sg.last)) return;
+
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Ly::BARS);
+    uint64_t* full_x = bars + 0;
+    uint64_t* full_y = bars + 1;     // [2]
+    uint64_t* full_z = bars + 3;     // [2]
+    uint64_t* free_z = bars + 5;     // [2] Op of the chunk that used the buffer
+    uint64_t* g_full = bars + 7;     // [2]
+    uint64_t* g_free = bars + 9;     // [2] one arrival per group
+    uint64_t* d_done = bars + 11;    // D
+    uint64_t* oi_done = bars + 12;   // Oi
+    uint64_t* r_done = bars + 13;    // R
+    uint64_t* op_done = bars + 14;   // Op
+    uint64_t* y_ready = bars + 15;   // B: Y~ (and a cleared z)
+    uint64_t* r_ready = bars + 16;   // A: R scaled, its bf16 copy written
+    uint64_t* p_ready = bars + 17;   // C: P
+    uint64_t* o_free = bars + 18;    // C: Oi and Op read
+    uint64_t* drain = bars + 19;
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 20);
+    GateBuf* gates = reinterpret_cast<GateBuf*>(smem + Ly::GATES);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int grp = warp >> 2, gt = tid & (kGrp - 1);
+    const bool rev = p.reverse;
+    const int nchunk = (sg.n + C - 1) / C;
+    // chunk of step j: in the pass's direction; a states pass comes from the far end
+    const bool down = STATES ? !rev : rev;
+    auto chunk = [&](int j) { return down ? nchunk - 1 - j : j; };
+    auto rows_of = [&](int j) { return min(C, sg.n - chunk(j) * C); };
+    const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const long long wl = a.l.wait_cycles;
+
+    if (tid == 0) {
+        for (int i = 0; i < 20; ++i) mbar_init(bars + i, i == 9 || i == 10 ? (STATES ? 1 : 3) : 1);
+        mbar_fence_init();
+    }
+    if (warp == 0) tmem_alloc(tmem_holder, kTmemCols);
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tmem = *tmem_holder;
+    bool failed = false;
+
+    // A bounded wait of `n` threads (named barrier `id`) on a phase: the first warp of them polls.
+    auto group_wait = [&](uint64_t* bar, uint32_t parity, uint32_t id, uint32_t n, bool polls) -> bool {
+        bool got = true;
+        if (polls) got = mbar_wait(bar, parity, wl);
+        const bool bad = named_sync_or(id, n, !got);
+        fence_after_sync();
+        return !bad;
+    };
+
+    if (warp == 12) {
+        // =================== copies ===================
+        if (lane == 0) {
+            const int hx = sg.h / p.x.div, hy = sg.h / p.y.div, hz = sg.h / p.z.div;
+            int nx = 0, ny = 0, nz = 0;    // copies started
+            auto load = [&](uint32_t dst, int which, int D, int h, int j, uint64_t* bar) {
+                mbar_expect_tx(bar, D * 256);
+                for (int x = 0; x < D / 64; ++x)
+                    tma_load_4d(dst + x * kHalf, &maps[which], 64 * x, sg.t0 + chunk(j) * C, h, sg.b, bar);
+            };
+            for (int j = 0; j < nchunk; ++j) {
+                if (STATES) {
+                    const int s = j & 1;
+                    if (j >= 2 && !mbar_wait(&free_z[s], ((j - 2) >> 1) & 1, wl)) { failed = true; break; }
+                    load(sb + Ly::T_Y + s * Ly::XB, 1, DX, hy, j, &full_y[s]);
+                    ++ny;
+                    load(sb + Ly::T_Z + s * Ly::ZB, 2, DZ, hz, j, &full_z[s]);
+                    ++nz;
+                } else {
+                    // y once D and Y~ of the chunk before are formed, x once its Oi is, z once the Op of its buffer is
+                    if (j >= 1 && (!mbar_wait(d_done, (j - 1) & 1, wl) || !mbar_wait(y_ready, (j - 1) & 1, wl))) { failed = true; break; }
+                    load(sb + Ly::T_Y, 1, DX, hy, j, full_y);
+                    ++ny;
+                    if (j >= 1 && !mbar_wait(oi_done, (j - 1) & 1, wl)) { failed = true; break; }
+                    load(sb + Ly::T_X, 0, DX, hx, j, full_x);
+                    ++nx;
+                    const int s = j % Ly::NZ;
+                    if (j >= Ly::NZ && !mbar_wait(&free_z[s], ((j - Ly::NZ) / Ly::NZ) & 1, wl)) { failed = true; break; }
+                    load(sb + Ly::T_Z + s * Ly::ZB, 2, DZ, hz, j, &full_z[s]);
+                    ++nz;
+                }
+            }
+            if (failed) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
+            // no copy may land after the CTA has gone (another role may have given up): wait for the last into each buffer
+            const long long most = 400000000LL;
+            if (nx > 0) mbar_wait(full_x, (nx - 1) & 1, most);
+            for (int s = 0; s < Ly::NY; ++s)
+                if (ny > s) mbar_wait(&full_y[s], ((ny - 1 - s) / Ly::NY) & 1, most);
+            for (int s = 0; s < Ly::NZ; ++s)
+                if (nz > s) mbar_wait(&full_z[s], ((nz - 1 - s) / Ly::NZ) & 1, most);
+        }
+        __syncwarp();
+    } else if (warp == 13) {
+        // =================== MMA issue (lane 0; the others wait at the end) ===================
+        if (lane == 0) {
+            auto wait1 = [&](uint64_t* bar, uint32_t parity) -> bool {
+                const bool ok = mbar_wait(bar, parity, wl);
+                fence_after_sync();
+                return ok;
+            };
+            const uint32_t idD = idesc_bf16(128, C, false, false);
+            const uint32_t idO = idesc_bf16(128, DZ, false, true);
+            const uint32_t idR = idesc_bf16(128, DZ, true, true);
+            auto mma_D = [&]() {
+#pragma unroll
+                for (int h = 0; h < DX / 64; ++h)
+                    mma_chain(tmem + TM_D, smem_desc_sw128(sb + Ly::T_X + h * kHalf, 16, 1024), 32,
+                              smem_desc_sw128(sb + Ly::T_Y + h * kHalf, 16, 1024), 32, idD, 64, h > 0);
+                mma_commit(d_done);
+            };
+            auto mma_Oi = [&]() {
+#pragma unroll
+                for (int s = 0; s < (SPLIT ? 2 : 1); ++s)
+#pragma unroll
+                    for (int h = 0; h < DX / 64; ++h)
+                        mma_chain(tmem + TM_OI, smem_desc_sw128(sb + Ly::T_X + h * kHalf, 16, 1024), 32,
+                                  smem_desc_sw128(sb + Ly::T_R + s * Ly::RB + h * 64 * 128, DX * 128, 1024), 2048, idO, 64,
+                                  s > 0 || h > 0);
+                mma_commit(oi_done);
+            };
+            auto mma_R = [&](uint32_t tz, bool acc) {
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+                    mma_chain(tmem + TM_R, smem_desc_sw128(sb + (s ? Ly::T_YL : Ly::T_YH), kHalf, 1024), 2048,
+                              smem_desc_sw128(tz, kHalf, 1024), 2048, idR, C, acc || s > 0);
+            };
+            auto mma_Op = [&](uint32_t tz) {
+#pragma unroll
+                for (int s = 0; s < (SPLIT ? 2 : 1); ++s)
+                    mma_chain_tmem_a(tmem + TM_OP, tmem + TM_D + 64 * s, smem_desc_sw128(tz, kHalf, 1024), 2048, idO, C, s > 0);
+            };
+            for (int j = 0; j < nchunk; ++j) {
+                const int s = STATES ? (j & 1) : j % Ly::NZ;
+                const uint32_t tz = sb + Ly::T_Z + s * Ly::ZB, zpar = STATES ? (j >> 1) & 1 : (j / Ly::NZ) & 1;
+                if (STATES) {
+                    if (!wait1(y_ready, j & 1) || !wait1(&full_z[s], zpar)) { failed = true; break; }
+                    mma_R(tz, j > 0);
+                    mma_commit(&free_z[s]);
+                    mma_commit(r_done);
+                    continue;
+                }
+                if (!wait1(full_x, j & 1) || !wait1(full_y, j & 1)) { failed = true; break; }
+                mma_D();
+                if (!wait1(r_ready, j & 1) || (j > 0 && !wait1(o_free, (j - 1) & 1))) { failed = true; break; }
+                mma_Oi();
+                if (!wait1(y_ready, j & 1) || !wait1(&full_z[s], zpar)) { failed = true; break; }
+                mma_R(tz, true);
+                mma_commit(r_done);
+                if (!wait1(p_ready, j & 1)) { failed = true; break; }
+                mma_Op(tz);
+                mma_commit(&free_z[s]);
+                mma_commit(op_done);
+            }
+            if (failed) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
+            mma_commit(drain);       // every MMA this thread issued: none may run on freed tensor memory
+            mbar_wait(drain, 0, 400000000LL);
+        }
+        __syncwarp();
+    } else if (warp == 14) {
+        // =================== gates: lane holds tokens 4 lane .. 4 lane + 3 ===================
+        const float* gp = p.g + sg.b * p.gb + sg.h * p.gh;
+        auto raw = [&](int j, float (&r)[4]) {
+            const int n = rows_of(j);
+            const long long t0 = (long long)sg.t0 + chunk(j) * C;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = 4 * lane + i;
+                const float g = t < n ? gp[(t0 + t) * p.gt] : 0.f;
+                r[i] = g < kMinGate ? kMinGate : g;
+            }
+        };
+        float cur[4], nxt[4];
+        if (nchunk > 0) raw(0, cur);
+        double passed = 0.0;    // gates of the chunks before (log2 units)
+        for (int j = 0; j < nchunk; ++j) {
+            if (j + 1 < nchunk) raw(j + 1, nxt);
+            double x[4];
+            x[0] = (double)cur[0];
+#pragma unroll
+            for (int i = 1; i < 4; ++i) x[i] = x[i - 1] + (double)cur[i];
+            double s = x[3];
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const double y = __shfl_up_sync(0xffffffffu, s, off);
+                if (lane >= off) s += y;
+            }
+            const double all = __shfl_sync(0xffffffffu, s, 31);
+            const double before = s - x[3];                                         // exclusive
+            const double start = __shfl_sync(0xffffffffu, before, lane & ~7);       // of this lane's block
+            const int b = j & 1;
+            bool ok = true;
+            if (j >= 2) ok = mbar_wait(&g_free[b], ((j - 2) >> 1) & 1, wl);
+            if (!__all_sync(0xffffffffu, ok)) { failed = true; break; }
+            GateBuf& g = gates[b];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) g.rc[4 * lane + i] = (float)(((before - start) + x[i]) * kLog2e);
+            {   // lane i j of the first 16: start_i - start_j
+                const double si = __shfl_sync(0xffffffffu, before, 8 * ((lane >> 2) & 3));
+                const double sj = __shfl_sync(0xffffffffu, before, 8 * (lane & 3));
+                if (lane < 16) g.ad[lane >> 2][lane & 3] = (float)((si - sj) * kLog2e);
+                if (lane < 4) {
+                    g.an[lane] = (float)((sj + (STATES ? passed : 0.0)) * kLog2e);
+                    g.tn[lane] = (float)((all - sj + (STATES ? passed : 0.0)) * kLog2e);
+                }
+                if (lane == 0) g.en = ex2((float)(all * kLog2e));
+            }
+            passed += all;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&g_full[b]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) cur[i] = nxt[i];
+        }
+        if (failed && lane == 0) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
+        if (STATES && p.gsum && lane == 0) p.gsum[sg.entry] = (float)passed;
+    } else if (STATES) {
+        // =================== all groups: Y~; then the state ===================
+        constexpr uint32_t N = 3 * kGrp;
+        for (int j = 0; j < nchunk; ++j) {
+            const int s = j & 1, n = rows_of(j);
+            if (!group_wait(&g_full[s], (j >> 1) & 1, 1, N, warp == 0) || !group_wait(&full_y[s], (j >> 1) & 1, 1, N, warp == 0) ||
+                (j > 0 && !group_wait(r_done, (j - 1) & 1, 1, N, warp == 0)) ||
+                (n < C && !group_wait(&full_z[s], (j >> 1) & 1, 1, N, warp == 0))) { failed = true; break; }
+            scale_rows<DX>(sb + Ly::T_Y + s * Ly::XB, sb + Ly::T_YH, sb + Ly::T_YL, gates[s], rev, n, tid, N);
+            if (n < C) clear_rows<DZ>(sb + Ly::T_Z + s * Ly::ZB, n, tid, N);
+            fence_async_smem();
+            named_sync(1, N);
+            if (tid == 0) { mbar_arrive(y_ready); mbar_arrive(&g_free[s]); }
+        }
+        if (!failed && nchunk > 0 && !group_wait(r_done, (nchunk - 1) & 1, 1, N, warp == 0)) failed = true;
+        if (!failed && grp == 0 && gt < (DX == 64 && warp >= 2 ? 0 : kGrp)) {
+            float* dst = p.bound + (rev ? sg.entry : sg.entry + sg.step) * (long long)(DX * DZ) + gt * p.six;
+#pragma unroll
+            for (int c = 0; c < DZ; c += 32) {
+                float v[32];
+                tmem_ld32(tmem + TM_R + lane_off + c, v);
+                if (p.siz == 1) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        *reinterpret_cast<float4*>(dst + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) dst[(c + i) * p.siz] = v[i];
+                }
+            }
+        }
+        if (failed && tid == 0) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
+    } else if (grp == 0) {
+        // =================== A: the state (thread = row of R; with DX = 64 two warps only keep step) ===================
+        const bool mine = DX == 128 || warp < 2;
+        const float* src = nullptr;
+        if (p.bound && !sg.alone) src = p.bound + (rev ? sg.entry + sg.step : sg.entry) * (long long)(DX * DZ);
+        else if (p.ext_in && !sg.fresh) src = p.ext_in + sg.ext * (long long)(DX * DZ);
+        const uint32_t tr = sb + Ly::T_R;
+        for (int j = 0; j < nchunk; ++j) {
+            const int b = j & 1;
+            if (!group_wait(&g_full[b], (j >> 1) & 1, 1, kGrp, warp == 0) ||
+                (j > 0 && (!group_wait(oi_done, (j - 1) & 1, 1, kGrp, warp == 0) ||
+                           !group_wait(r_done, (j - 1) & 1, 1, kGrp, warp == 0)))) { failed = true; break; }
+            const float en = gates[b].en;
+            if (mine) {
+#pragma unroll
+                for (int c = 0; c < DZ; c += 32) {
+                    float v[32];
+                    if (j > 0) {
+                        tmem_ld32(tmem + TM_R + lane_off + c, v);
+                    } else if (src) {
+                        const float* s = src + gt * p.six + c * p.siz;
+                        if (p.siz == 1) {
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4) {
+                                const float4 x = *reinterpret_cast<const float4*>(s + i);
+                                v[i] = x.x; v[i + 1] = x.y; v[i + 2] = x.z; v[i + 3] = x.w;
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = s[i * p.siz];
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = 0.f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        const uint32_t off = (uint32_t)((c + i) >> 6) * (DX * 128) + swz(gt, ((c + i) & 63) >> 3);
+                        uint32_t h[4], l[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if (SPLIT) split2(v[i + 2 * e], v[i + 2 * e + 1], h[e], l[e]);
+                            else h[e] = pack_bf16(v[i + 2 * e], v[i + 2 * e + 1]);
+                        }
+                        sts128(tr + off, h[0], h[1], h[2], h[3]);
+                        if (SPLIT) sts128(tr + Ly::RB + off, l[0], l[1], l[2], l[3]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] *= en;
+                    tmem_st32_nowait(tmem + TM_R + lane_off + c, v);
+                }
+                tmem_wait_st();
+            }
+            fence_async_smem();
+            fence_before_sync();
+            named_sync(1, kGrp);
+            if (gt == 0) { mbar_arrive(r_ready); mbar_arrive(&g_free[b]); }
+        }
+        if (!failed && nchunk > 0 && !group_wait(r_done, (nchunk - 1) & 1, 1, kGrp, warp == 0)) failed = true;
+        if (!failed && mine && p.ext_out && (rev ? sg.first : sg.last)) {
+            float* dst = p.ext_out + sg.ext * (long long)(DX * DZ) + gt * p.six;
+#pragma unroll
+            for (int c = 0; c < DZ; c += 32) {
+                float v[32];
+                tmem_ld32(tmem + TM_R + lane_off + c, v);
+                if (p.siz == 1) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        *reinterpret_cast<float4*>(dst + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) dst[(c + i) * p.siz] = v[i];
+                }
+            }
+        }
+        if (failed && gt == 0) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
+    } else if (grp == 1) {
+        // =================== B: Y~ ===================
+        for (int j = 0; j < nchunk; ++j) {
+            const int b = j & 1, n = rows_of(j), s = j % Ly::NZ;
+            const bool poll = warp == 4;
+            if (!group_wait(&g_full[b], (j >> 1) & 1, 2, kGrp, poll) || !group_wait(full_y, j & 1, 2, kGrp, poll) ||
+                (j > 0 && !group_wait(r_done, (j - 1) & 1, 2, kGrp, poll)) ||
+                (n < C && !group_wait(&full_z[s], (j / Ly::NZ) & 1, 2, kGrp, poll))) { failed = true; break; }
+            scale_rows<DX>(sb + Ly::T_Y, sb + Ly::T_YH, sb + Ly::T_YL, gates[b], rev, n, gt, kGrp);
+            if (n < C) clear_rows<DZ>(sb + Ly::T_Z + s * Ly::ZB, n, gt, kGrp);
+            fence_async_smem();
+            named_sync(2, kGrp);
+            if (gt == 0) { mbar_arrive(y_ready); mbar_arrive(&g_free[b]); }
+        }
+        if (failed && gt == 0) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
+    } else {
+        // =================== C: P, then the outputs (thread = row) ===================
+        const int w = warp & 3;
+        const bool poll = w == 0;
+        for (int j = 0; j < nchunk; ++j) {
+            const int b = j & 1, n = rows_of(j);
+            if (!group_wait(&g_full[b], (j >> 1) & 1, 3, kGrp, poll) || !group_wait(d_done, j & 1, 3, kGrp, poll)) { failed = true; break; }
+            const GateBuf& g = gates[b];
+            const float rc = g.rc[gt];
+            // block q of 32 columns: D -> P (hi, lo) packed
+            auto block = [&](int q, uint32_t (&h)[16], uint32_t (&l)[16]) {
+                if (rev ? q < w : q > w) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) h[i] = l[i] = 0u;
+                    return;
+                }
+                float v[32];
+                tmem_ld32(tmem + TM_D + lane_off + 32 * q, v);
+                const float base = g.ad[w][q] + rc;
+                const float4* col = reinterpret_cast<const float4*>(g.rc + 32 * q);
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                    const float4 cc = col[i >> 2];
+                    const float cv[4] = {cc.x, cc.y, cc.z, cc.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float d = base - cv[e];
+                        v[i + e] *= ex2(rev ? -d : d);
+                    }
+                }
+                if (q == w) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (rev ? i < lane : i > lane) v[i] = 0.f;
+                }
+                if (rev && n < C) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (32 * q + i >= n) v[i] = 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    if (SPLIT) split2(v[2 * i], v[2 * i + 1], h[i], l[i]);
+                    else h[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+                }
+            };
+            const uint32_t td = tmem + TM_D + lane_off;
+            if (SPLIT) {    // lo lands on columns 64 .. 127 of D: blocks 2 and 3 are read first
+                uint32_t h2[16], l2[16], h3[16], l3[16];
+                block(2, h2, l2);
+                block(3, h3, l3);
+                {
+                    uint32_t h[16], l[16];
+                    block(0, h, l);
+                    tmem_st16(td, h);
+                    tmem_st16(td + 64, l);
+                    block(1, h, l);
+                    tmem_st16(td + 16, h);
+                    tmem_st16(td + 80, l);
+                }
+                tmem_st16(td + 32, h2);
+                tmem_st16(td + 96, l2);
+                tmem_st16(td + 48, h3);
+                tmem_st16(td + 112, l3);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t h[16], l[16];
+                    block(q, h, l);
+                    tmem_st16(td + 16 * q, h);
+                }
+            }
+            tmem_wait_st();
+            fence_before_sync();
+            named_sync(3, kGrp);
+            if (gt == 0) mbar_arrive(p_ready);
+            // ---- o
+            const float cx = ex2(rev ? g.tn[w] - rc : g.an[w] + rc);
+            if (!group_wait(oi_done, j & 1, 3, kGrp, poll) || !group_wait(op_done, j & 1, 3, kGrp, poll)) { failed = true; break; }
+            if (gt == 0) mbar_arrive(&g_free[b]);     // every thread of the group has read its gates
+            const long long t = (long long)sg.t0 + chunk(j) * C + gt;
+            const bool live = gt < n;
+            const long long at = sg.b * p.ob + sg.h * p.oh + t * p.ot;
+            float dot = 0.f;
+#pragma unroll
+            for (int c = 0; c < DZ; c += 32) {
+                float u[32], v[32];
+                tmem_ld32(tmem + TM_OI + lane_off + c, u);
+                tmem_ld32(tmem + TM_OP + lane_off + c, v);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = fmaf(cx, u[i], v[i]);
+                if (live) {
+                    if (SPLIT) {
+                        const uint4* wp = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.w.p) +
+                                                                         sg.b * p.w.sb + (sg.h / p.w.div) * p.w.sh + t * p.w.st + c);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint4 x = wp[i];
+                            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                dot = fmaf(__uint_as_float(xs[e] << 16), v[8 * i + 2 * e], dot);
+                                dot = fmaf(__uint_as_float(xs[e] & 0xFFFF0000u), v[8 * i + 2 * e + 1], dot);
+                            }
+                        }
+                    }
+                    if (p.o_f32) {
+                        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.o) + at + c);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    } else {
+                        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + at + c);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            dst[i] = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                                                pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+                    }
+                }
+            }
+            if (SPLIT && live) p.dots[((long long)sg.b * a.l.geo.H + sg.h) * a.l.geo.T + t] = dot;
+            fence_before_sync();
+            named_sync(3, kGrp);
+            if (gt == 0) mbar_arrive(o_free);
+        }
+        if (failed && gt == 0) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
+    }
+    fence_before_sync();
+    __syncthreads();
+    if (warp == 0) tmem_dealloc(tmem, kTmemCols);
+}
+
+// A row sequence as [batch][head][token][feature]: boxes of 64 features x 128 tokens of one head.
+bool map_rows(CUtensorMap* m, const View& v, int D, long long T, int heads, int B) {
+    return tensor_map_rows(m, v.p, D, T, heads, B, v.st, v.sh, v.sb, C);
+}
+
+template <int DX, int DZ, bool SPLIT, bool STATES>
+cudaError_t run(const Args& a, long long n, cudaStream_t s) {
+    static std::atomic<uint64_t> set{0};
+    constexpr int bytes = Layout<DX, DZ, SPLIT, STATES>::TOTAL;
+    auto f = hd_tc_kernel<DX, DZ, SPLIT, STATES>;
+    const cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(f), bytes, set);
+    if (e != cudaSuccess) return e;
+    f<<<dim3((unsigned)n, (unsigned)a.l.npass), NT, bytes, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <int DX, int DZ>
+cudaError_t run_kind(const Args& a, bool split, bool states, long long n, cudaStream_t s) {
+    if (states) return run<DX, DZ, false, true>(a, n, s);
+    return split ? run<DX, DZ, true, false>(a, n, s) : run<DX, DZ, false, false>(a, n, s);
+}
+
+}  // namespace
+
+bool tc_supported(bool bf16, int dk, int dv) { return bf16 && (dk == 64 || dk == 128) && (dv == 64 || dv == 128); }
+
+cudaError_t launch_tc(const Launch& l, cudaStream_t s) {
+    const long long n = units(l.geo, l.B, l.max_blocks);
+    if (n == 0) return cudaSuccess;
+    if (n >= (1LL << 31)) return cudaErrorInvalidValue;
+    // passes of one size and kind go in one launch
+    bool done[3] = {};
+    for (int i = 0; i < l.npass; ++i) {
+        if (done[i]) continue;
+        const Pass& q = l.pass[i];
+        Args a;
+        std::memset(&a, 0, sizeof(a));
+        a.l = l;
+        a.l.npass = 0;
+        for (int j = i; j < l.npass; ++j) {
+            const Pass& p = l.pass[j];
+            if (done[j] || p.DX != q.DX || p.DZ != q.DZ || (p.dots != nullptr) != (q.dots != nullptr) ||
+                (p.states_only != 0) != (q.states_only != 0))
+                continue;
+            done[j] = true;
+            const int k = a.l.npass++;
+            a.l.pass[k] = p;
+            const int H = l.geo.H;
+            const long long T = l.geo.T;
+            if (!p.states_only && !map_rows(&a.map[k][0], p.x, p.DX, T, H / p.x.div, l.B)) return cudaErrorInvalidValue;
+            if (!map_rows(&a.map[k][1], p.y, p.DX, T, H / p.y.div, l.B)) return cudaErrorInvalidValue;
+            if (!map_rows(&a.map[k][2], p.z, p.DZ, T, H / p.z.div, l.B)) return cudaErrorInvalidValue;
+        }
+        const bool split = q.dots != nullptr, states = q.states_only != 0;
+        cudaError_t e;
+        if (q.DX == 128 && q.DZ == 128) e = run_kind<128, 128>(a, split, states, n, s);
+        else if (q.DX == 128) e = run_kind<128, 64>(a, split, states, n, s);
+        else if (q.DZ == 128) e = run_kind<64, 128>(a, split, states, n, s);
+        else e = run_kind<64, 64>(a, split, states, n, s);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace hd
+}  // namespace dplr

@@ -221,13 +221,19 @@ def test_backward(sdl, dtype, B, H, Hq, T, dk, dv):
     dST = 0.3 * torch.randn(B, H, dk, dv, device="cuda", generator=g) if T % 3 != 1 else None
     b = sdl.HeadDecayBackward(x["q"].dtype, B, H, T, dk, dv, q_heads=Hq, per_head=per_head, token_major=T % 4 < 2)
     got = b(dO, dST, **x)
-    check_grads(dtype, got, grads_want(x, dO, dST))
+    w = grads_want(x, dO, dST)
+    check_grads(dtype, got, w)
     assert b.device_status() == 0
     first = {n: t.clone() for n, t in got.items()}
     got = b(dO, dST, **x)
     assert all(torch.equal(first[n], got[n]) for n in first)
     less = b(dO, dST, **x, decay_grad=False)
-    assert "decay" not in less and all(torch.equal(first[n], less[n]) for n in less)
+    assert "decay" not in less
+    if b.path == "hd_fp32":
+        assert all(torch.equal(first[n], less[n]) for n in less)
+    # on the tensor cores dq and dk then take one-part operands (2^-8, not 2^-16, before the output's own rounding to
+    # bf16): not the same bits, but within the bound that counts those roundings
+    check_grads(dtype, less, {n: w[n] for n in less})
 
 
 def test_backward_against_differences(sdl):
