@@ -15,19 +15,24 @@
 // rounded to bf16 once: they only reach o, which is rounded to bf16 itself. Where per-token dots of the unrounded o
 // are asked for (the gradient of the gates is a sum in which they nearly cancel), P and R have two parts too (SPLIT).
 //
-// Exponents. Sums of gates are formed in 64 bits (in units of log2) and kept as fp32 offsets from the start of blocks
-// of 32 tokens, with the differences of the starts: the exponent of a pair is accurate however much was forgotten
-// before both, and never positive, so nothing overflows for any gate.
+// Exponents. Sums of gates are formed in 64 bits (in units of log2) and kept as fp32 offsets from the start of blocks of
+// 32 tokens, so that they are accurate however much was forgotten before. Within a diagonal 32 x 32 block of P the
+// factor of a pair is one exponential; between blocks it is a product of three, each of a sum that is not positive
+// (forward: row to its block's start, that start to the column block's end, that end to the column), two of them per
+// token and one per pair of blocks: a quarter of the exponentials, and nothing overflows for any gate.
 //
-// Work split: three groups of four warps (thread = lane of tensor memory) and three single warps:
+// Work split: four groups of four warps (thread = lane of tensor memory) and three single warps:
 //   A  the state: R to bf16 in shared memory, e^{G_n} R back        B  Y~ from Y
-//   C  P from D, then o from Oi and Op                              copies (TMA), MMA issue, gates
+//   C  P from D                                                     O  o from Oi and Op
+//   copies (TMA), MMA issue, gates
 // The issuer's order within a chunk, D Oi R Op, leaves the CUDA-core phases of a chunk under the other products.
 // Each row sequence is read once by TMA in the 128-byte swizzle; the same tile serves K-major (D, Oi) and MN-major (Op,
-// R) operands. x and y have one buffer, z two (one with SPLIT): x and y are free again early in a chunk.
+// R) operands. A full chunk's o leaves by TMA from a tile of its own (16-byte stores of rows by lanes took 3.2 K cycles
+// of the SM's store path); a ragged one, an fp32 one, and with SPLIT (whose second part of R takes the tile's place)
+// every one is stored from registers.
 //
 // A pass for states only (the segments' own contributions) walks the chunks from the far end, so that the weights
-// e^{(gates behind the token)} need no rescaling of R: its accumulator is touched by MMAs alone, and all three groups
+// e^{(gates behind the token)} need no rescaling of R: its accumulator is touched by MMAs alone, and all four groups
 // form Y~.
 //
 // Bound: by the bytes of x, y, z and o (1 KB a token and head at 128 x 128): a chunk is 128 KB, 5.6 K cycles of its
@@ -45,31 +50,33 @@ using namespace tc;
 
 constexpr int C = kChunk;                  // 128
 constexpr int kGrp = 128;
-constexpr int NT = 3 * kGrp + 96;          // groups A, B, C; warps 12 (copies), 13 (MMA issue), 14 (gates)
+constexpr int NT = 4 * kGrp + 96;          // groups A, B, C, O; warps 16 (copies), 17 (MMA issue), 18 (gates)
 constexpr uint32_t kHalf = C * 128;        // bytes of a half tile: 128 rows of 64 bf16
 constexpr uint32_t TM_R = 0, TM_D = 128, TM_OI = 256, TM_OP = 384, kTmemCols = 512;
 constexpr double kLog2e = 1.4426950408889634;
 
 struct alignas(128) Args {
-    CUtensorMap map[3][3];    // [pass][x, y, z]
+    CUtensorMap map[3][4];    // [pass][x, y, z, o]
     Launch l;
 };
 
-// Per-chunk gate values (fp32, log2 units), double-buffered.
+// Per-chunk gate values, double-buffered; A_i: cumulative gates at the start of block i of 32 tokens (log2 units).
 struct GateBuf {
     float rc[C];        // G_t minus its block's start
-    float ad[4][4];     // start of block i minus start of block j
-    float an[4];        // block start (plus what lies in front of the chunk, in a states pass backward in time)
-    float tn[4];        // chunk end minus block start (plus what lies behind the chunk, in a states pass)
+    float cf[C];        // forward e^{A_{i+1} - G_t}, backward e^{G_t - A_i}: a token as a column of P, and as a row of Y~
+    float f[4][4];      // between row block i and column block j: forward e^{A_i - A_{j+1}}, backward e^{A_j - A_{i+1}}
+    float bl[4];        // A_{i+1} - A_i
+    float ce[4];        // Y~: times this. Forward e^{G_n - A_{i+1}}, backward e^{A_i} (a states pass: and the chunks between)
+    float re[4];        // Oi: a row's factor times this. Forward e^{A_i}, backward e^{G_n - A_{i+1}}
     float en;           // e^{G_n}
-    float pad[7];
+    float pad[3];
 };
 static_assert(sizeof(GateBuf) % 16 == 0, "16-byte rows");
 
 template <int DX, int DZ, bool SPLIT, bool STATES>
 struct Layout {
     static constexpr int XB = DX * 256, ZB = DZ * 256;        // bytes of a tile: D / 64 half tiles
-    static constexpr int NZ = (SPLIT && !STATES) ? 1 : 2;     // z buffers
+    static constexpr int NZ = STATES ? 2 : 1;                 // z buffers
     static constexpr int NY = STATES ? 2 : 1;                 // y buffers (a states pass has no x)
     static constexpr int RB = STATES ? 0 : DX * DZ * 2;       // R as bf16: DZ / 64 halves of DX rows of 128 bytes
     static constexpr int T_X = 0;
@@ -78,7 +85,9 @@ struct Layout {
     static constexpr int T_YL = T_YH + XB;
     static constexpr int T_Z = T_YL + XB;                     // (a 64-feature Y~ read as M = 128 runs into what follows)
     static constexpr int T_R = T_Z + NZ * ZB;
-    static constexpr int GATES = T_R + RB * (SPLIT ? 2 : 1);
+    static constexpr int T_O = T_R + RB * (SPLIT ? 2 : 1);    // o on its way out
+    static constexpr bool STAGED = !SPLIT && !STATES;
+    static constexpr int GATES = T_O + (STAGED ? ZB : 0);
     static constexpr int BARS = GATES + 2 * (int)sizeof(GateBuf);
     static constexpr int TOTAL = BARS + 256;
     static_assert(TOTAL <= 227 * 1024, "shared memory budget");
@@ -98,6 +107,32 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, int c0, int t, int h, int b, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];"
+                 :: "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(t), "r"(h), "r"(b), "r"(src) : "memory");
+}
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// 32 columns of two accumulators, both loads in flight at once.
+__device__ __forceinline__ void tmem_ld32_pair(uint32_t ta, uint32_t tb, float (&x)[32], float (&y)[32]) {
+    uint32_t r[64];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t* q = r + 16 * i;
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+            : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3]), "=r"(q[4]), "=r"(q[5]), "=r"(q[6]), "=r"(q[7]), "=r"(q[8]),
+              "=r"(q[9]), "=r"(q[10]), "=r"(q[11]), "=r"(q[12]), "=r"(q[13]), "=r"(q[14]), "=r"(q[15])
+            : "r"((i < 2 ? ta : tb) + 16 * (i & 1)));
+    }
+    // the wait takes the registers as operands, so that no use of them moves in front of it
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 64; ++i) asm volatile("" : "+r"(r[i]));
+#pragma unroll
+    for (int i = 0; i < 32; ++i) { x[i] = __uint_as_float(r[i]); y[i] = __uint_as_float(r[32 + i]); }
+}
+
 __device__ __forceinline__ void tmem_st32_nowait(uint32_t taddr, const float (&v)[32]) {
     uint32_t r[32];
 #pragma unroll
@@ -108,21 +143,27 @@ __device__ __forceinline__ void tmem_st32_nowait(uint32_t taddr, const float (&v
 
 // The y rows of a chunk times their weights, as hi + lo, by `nt` threads; rows from n on become zero whatever they hold.
 template <int DX>
-__device__ __forceinline__ void scale_rows(uint32_t ty, uint32_t th, uint32_t tl, const GateBuf& g, bool rev, int n, int tid,
-                                           int nt) {
+__device__ __forceinline__ void scale_rows(uint32_t ty, uint32_t th, uint32_t tl, const GateBuf& g, int n, int tid, int nt) {
     constexpr int PER = DX / 8;     // 16-byte pieces of a row
-#pragma unroll 4
+#pragma unroll 2
     for (int i = tid; i < C * PER; i += nt) {
-        const int t = i / PER, c = i % PER, blk = t >> 5;
-        const float w = ex2(rev ? g.an[blk] + g.rc[t] : g.tn[blk] - g.rc[t]);
+        const int t = i / PER, c = i % PER;
+        const float w = g.cf[t] * g.ce[t >> 5];
+        const float2 w2 = make_float2(w, w);
         const uint32_t off = (uint32_t)(c >> 3) * kHalf + swz(t, c & 7);
         uint32_t u[4];
         asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "r"(ty + off));
         uint32_t h[4], l[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            split2(__uint_as_float(u[e] << 16) * w, __uint_as_float(u[e] & 0xFFFF0000u) * w, h[e], l[e]);
-            if (t >= n) h[e] = l[e] = 0u;
+            const float2 x = __fmul2_rn(make_float2(__uint_as_float(u[e] << 16), __uint_as_float(u[e] & 0xFFFF0000u)), w2);
+            h[e] = pack_bf16(x.x, x.y);
+            const float2 r = __fadd2_rn(x, make_float2(-__uint_as_float(h[e] << 16), -__uint_as_float(h[e] & 0xFFFF0000u)));
+            l[e] = pack_bf16(r.x, r.y);
+        }
+        if (t >= n) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[e] = l[e] = 0u;
         }
         sts128(th + off, h[0], h[1], h[2], h[3]);
         sts128(tl + off, l[0], l[1], l[2], l[3]);
@@ -185,7 +226,7 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
     const long long wl = a.l.wait_cycles;
 
     if (tid == 0) {
-        for (int i = 0; i < 20; ++i) mbar_init(bars + i, i == 9 || i == 10 ? (STATES ? 1 : 3) : 1);
+        for (int i = 0; i < 20; ++i) mbar_init(bars + i, i == 9 || i == 10 ? (STATES ? 1 : 4) : 1);
         mbar_fence_init();
     }
     if (warp == 0) tmem_alloc(tmem_holder, kTmemCols);
@@ -204,7 +245,7 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
         return !bad;
     };
 
-    if (warp == 12) {
+    if (warp == 16) {
         // =================== copies ===================
         if (lane == 0) {
             const int hx = sg.h / p.x.div, hy = sg.h / p.y.div, hz = sg.h / p.z.div;
@@ -246,7 +287,7 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                 if (nz > s) mbar_wait(&full_z[s], ((nz - 1 - s) / Ly::NZ) & 1, most);
         }
         __syncwarp();
-    } else if (warp == 13) {
+    } else if (warp == 17) {
         // =================== MMA issue (lane 0; the others wait at the end) ===================
         if (lane == 0) {
             auto wait1 = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -281,9 +322,13 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                               smem_desc_sw128(tz, kHalf, 1024), 2048, idR, C, acc || s > 0);
             };
             auto mma_Op = [&](uint32_t tz) {
+                const uint64_t dz = smem_desc_sw128(tz, kHalf, 1024);
 #pragma unroll
                 for (int s = 0; s < (SPLIT ? 2 : 1); ++s)
-                    mma_chain_tmem_a(tmem + TM_OP, tmem + TM_D + 64 * s, smem_desc_sw128(tz, kHalf, 1024), 2048, idO, C, s > 0);
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)     // 16 tokens: 8 columns of P
+                        mma_bf16_tmem_a(tmem + TM_OP, tmem + TM_D + 32 * (ks >> 1) + 8 * (ks & 1) + 16 * s,
+                                        dadd(dz, 2048 * ks), idO, (s > 0 || ks > 0) ? 1u : 0u);
             };
             for (int j = 0; j < nchunk; ++j) {
                 const int s = STATES ? (j & 1) : j % Ly::NZ;
@@ -312,7 +357,7 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
             mbar_wait(drain, 0, 400000000LL);
         }
         __syncwarp();
-    } else if (warp == 14) {
+    } else if (warp == 18) {
         // =================== gates: lane holds tokens 4 lane .. 4 lane + 3 ===================
         const float* gp = p.g + sg.b * p.gb + sg.h * p.gh;
         auto raw = [&](int j, float (&r)[4]) {
@@ -342,21 +387,29 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
             }
             const double all = __shfl_sync(0xffffffffu, s, 31);
             const double before = s - x[3];                                         // exclusive
-            const double start = __shfl_sync(0xffffffffu, before, lane & ~7);       // of this lane's block
+            // this lane's block: its start, its end
+            const double start = __shfl_sync(0xffffffffu, before, lane & ~7), end = __shfl_sync(0xffffffffu, s, lane | 7);
             const int b = j & 1;
             bool ok = true;
             if (j >= 2) ok = mbar_wait(&g_free[b], ((j - 2) >> 1) & 1, wl);
             if (!__all_sync(0xffffffffu, ok)) { failed = true; break; }
             GateBuf& g = gates[b];
+            const double far = STATES ? passed : 0.0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) g.rc[4 * lane + i] = (float)(((before - start) + x[i]) * kLog2e);
-            {   // lane i j of the first 16: start_i - start_j
-                const double si = __shfl_sync(0xffffffffu, before, 8 * ((lane >> 2) & 3));
-                const double sj = __shfl_sync(0xffffffffu, before, 8 * (lane & 3));
-                if (lane < 16) g.ad[lane >> 2][lane & 3] = (float)((si - sj) * kLog2e);
+            for (int i = 0; i < 4; ++i) {
+                const float up = (float)(((before - start) + x[i]) * kLog2e);
+                g.rc[4 * lane + i] = up;
+                g.cf[4 * lane + i] = ex2(rev ? up : (float)((end - before - x[i]) * kLog2e));
+            }
+            {   // lanes 4 i + j of the first 16: blocks i and j
+                const int bi = (lane >> 2) & 3, bj = lane & 3;
+                const double si = __shfl_sync(0xffffffffu, before, 8 * bi), sj = __shfl_sync(0xffffffffu, before, 8 * bj);
+                const double ei = __shfl_sync(0xffffffffu, s, 8 * bi + 7), ej = __shfl_sync(0xffffffffu, s, 8 * bj + 7);
+                if (lane < 16) g.f[bi][bj] = ex2((float)((rev ? sj - ei : si - ej) * kLog2e));
                 if (lane < 4) {
-                    g.an[lane] = (float)((sj + (STATES ? passed : 0.0)) * kLog2e);
-                    g.tn[lane] = (float)((all - sj + (STATES ? passed : 0.0)) * kLog2e);
+                    g.bl[lane] = (float)((ej - sj) * kLog2e);
+                    g.ce[lane] = ex2((float)(((rev ? sj : all - ej) + far) * kLog2e));
+                    g.re[lane] = ex2((float)((rev ? all - ej : sj) * kLog2e));
                 }
                 if (lane == 0) g.en = ex2((float)(all * kLog2e));
             }
@@ -370,13 +423,13 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
         if (STATES && p.gsum && lane == 0) p.gsum[sg.entry] = (float)passed;
     } else if (STATES) {
         // =================== all groups: Y~; then the state ===================
-        constexpr uint32_t N = 3 * kGrp;
+        constexpr uint32_t N = 4 * kGrp;
         for (int j = 0; j < nchunk; ++j) {
             const int s = j & 1, n = rows_of(j);
             if (!group_wait(&g_full[s], (j >> 1) & 1, 1, N, warp == 0) || !group_wait(&full_y[s], (j >> 1) & 1, 1, N, warp == 0) ||
                 (j > 0 && !group_wait(r_done, (j - 1) & 1, 1, N, warp == 0)) ||
                 (n < C && !group_wait(&full_z[s], (j >> 1) & 1, 1, N, warp == 0))) { failed = true; break; }
-            scale_rows<DX>(sb + Ly::T_Y + s * Ly::XB, sb + Ly::T_YH, sb + Ly::T_YL, gates[s], rev, n, tid, N);
+            scale_rows<DX>(sb + Ly::T_Y + s * Ly::XB, sb + Ly::T_YH, sb + Ly::T_YL, gates[s], n, tid, N);
             if (n < C) clear_rows<DZ>(sb + Ly::T_Z + s * Ly::ZB, n, tid, N);
             fence_async_smem();
             named_sync(1, N);
@@ -385,7 +438,7 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
         if (!failed && nchunk > 0 && !group_wait(r_done, (nchunk - 1) & 1, 1, N, warp == 0)) failed = true;
         if (!failed && grp == 0 && gt < (DX == 64 && warp >= 2 ? 0 : kGrp)) {
             float* dst = p.bound + (rev ? sg.entry : sg.entry + sg.step) * (long long)(DX * DZ) + gt * p.six;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < DZ; c += 32) {
                 float v[32];
                 tmem_ld32(tmem + TM_R + lane_off + c, v);
@@ -414,7 +467,7 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                            !group_wait(r_done, (j - 1) & 1, 1, kGrp, warp == 0)))) { failed = true; break; }
             const float en = gates[b].en;
             if (mine) {
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < DZ; c += 32) {
                     float v[32];
                     if (j > 0) {
@@ -461,7 +514,7 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
         if (!failed && nchunk > 0 && !group_wait(r_done, (nchunk - 1) & 1, 1, kGrp, warp == 0)) failed = true;
         if (!failed && mine && p.ext_out && (rev ? sg.first : sg.last)) {
             float* dst = p.ext_out + sg.ext * (long long)(DX * DZ) + gt * p.six;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < DZ; c += 32) {
                 float v[32];
                 tmem_ld32(tmem + TM_R + lane_off + c, v);
@@ -484,108 +537,115 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
             if (!group_wait(&g_full[b], (j >> 1) & 1, 2, kGrp, poll) || !group_wait(full_y, j & 1, 2, kGrp, poll) ||
                 (j > 0 && !group_wait(r_done, (j - 1) & 1, 2, kGrp, poll)) ||
                 (n < C && !group_wait(&full_z[s], (j / Ly::NZ) & 1, 2, kGrp, poll))) { failed = true; break; }
-            scale_rows<DX>(sb + Ly::T_Y, sb + Ly::T_YH, sb + Ly::T_YL, gates[b], rev, n, gt, kGrp);
+            scale_rows<DX>(sb + Ly::T_Y, sb + Ly::T_YH, sb + Ly::T_YL, gates[b], n, gt, kGrp);
             if (n < C) clear_rows<DZ>(sb + Ly::T_Z + s * Ly::ZB, n, gt, kGrp);
             fence_async_smem();
             named_sync(2, kGrp);
             if (gt == 0) { mbar_arrive(y_ready); mbar_arrive(&g_free[b]); }
         }
         if (failed && gt == 0) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
-    } else {
-        // =================== C: P, then the outputs (thread = row) ===================
+    } else if (grp == 2) {
+        // =================== C: P (thread = row) ===================
         const int w = warp & 3;
         const bool poll = w == 0;
+        const float sgn = rev ? 1.f : -1.f;
         for (int j = 0; j < nchunk; ++j) {
             const int b = j & 1, n = rows_of(j);
             if (!group_wait(&g_full[b], (j >> 1) & 1, 3, kGrp, poll) || !group_wait(d_done, j & 1, 3, kGrp, poll)) { failed = true; break; }
             const GateBuf& g = gates[b];
-            const float rc = g.rc[gt];
-            // block q of 32 columns: D -> P (hi, lo) packed
-            auto block = [&](int q, uint32_t (&h)[16], uint32_t (&l)[16]) {
+            const float rc = g.rc[gt], row = ex2(rev ? g.bl[w] - rc : rc);
+            // blocks of 32 columns, each packed in place: hi in its first 16 columns, lo in the others. The loops over
+            // blocks stay loops: unrolled, the roles' straight-line code outran the instruction cache (no_instruction
+            // was the largest stall, a chunk took 11.4 K cycles).
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+                uint32_t h[16], l[16];
                 if (rev ? q < w : q > w) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) h[i] = l[i] = 0u;
-                    return;
-                }
-                float v[32];
-                tmem_ld32(tmem + TM_D + lane_off + 32 * q, v);
-                const float base = g.ad[w][q] + rc;
-                const float4* col = reinterpret_cast<const float4*>(g.rc + 32 * q);
+                } else {
+                    float v[32];
+                    tmem_ld32(tmem + TM_D + lane_off + 32 * q, v);
+                    if (q == w) {
+                        const float base = -sgn * rc;
+                        const float4* col = reinterpret_cast<const float4*>(g.rc + 32 * q);
 #pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                    const float4 cc = col[i >> 2];
-                    const float cv[4] = {cc.x, cc.y, cc.z, cc.w};
+                        for (int i = 0; i < 32; i += 4) {
+                            const float4 cc = col[i >> 2];
+                            v[i] *= ex2(fmaf(sgn, cc.x, base));
+                            v[i + 1] *= ex2(fmaf(sgn, cc.y, base));
+                            v[i + 2] *= ex2(fmaf(sgn, cc.z, base));
+                            v[i + 3] *= ex2(fmaf(sgn, cc.w, base));
+                        }
+                    } else {
+                        const float rf = row * g.f[w][q];
+                        const float2 r2 = make_float2(rf, rf);
+                        const float4* col = reinterpret_cast<const float4*>(g.cf + 32 * q);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float d = base - cv[e];
-                        v[i + e] *= ex2(rev ? -d : d);
+                        for (int i = 0; i < 32; i += 4) {
+                            const float4 cc = col[i >> 2];
+                            const float2 x = __fmul2_rn(make_float2(v[i], v[i + 1]), __fmul2_rn(make_float2(cc.x, cc.y), r2));
+                            const float2 y = __fmul2_rn(make_float2(v[i + 2], v[i + 3]), __fmul2_rn(make_float2(cc.z, cc.w), r2));
+                            v[i] = x.x; v[i + 1] = x.y; v[i + 2] = y.x; v[i + 3] = y.y;
+                        }
+                    }
+                    // columns that this row sees: up to its own token, or from it to the chunk's last
+                    if (q == w || (rev && n < C)) {
+                        const int lo = rev ? (q == w ? lane : 0) : 0, hi = rev ? n - 1 - 32 * q : lane;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (i < lo || i > hi) v[i] = 0.f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        if (SPLIT) split2(v[2 * i], v[2 * i + 1], h[i], l[i]);
+                        else h[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
                     }
                 }
-                if (q == w) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (rev ? i < lane : i > lane) v[i] = 0.f;
-                }
-                if (rev && n < C) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (32 * q + i >= n) v[i] = 0.f;
-                }
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    if (SPLIT) split2(v[2 * i], v[2 * i + 1], h[i], l[i]);
-                    else h[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-                }
-            };
-            const uint32_t td = tmem + TM_D + lane_off;
-            if (SPLIT) {    // lo lands on columns 64 .. 127 of D: blocks 2 and 3 are read first
-                uint32_t h2[16], l2[16], h3[16], l3[16];
-                block(2, h2, l2);
-                block(3, h3, l3);
-                {
-                    uint32_t h[16], l[16];
-                    block(0, h, l);
-                    tmem_st16(td, h);
-                    tmem_st16(td + 64, l);
-                    block(1, h, l);
-                    tmem_st16(td + 16, h);
-                    tmem_st16(td + 80, l);
-                }
-                tmem_st16(td + 32, h2);
-                tmem_st16(td + 96, l2);
-                tmem_st16(td + 48, h3);
-                tmem_st16(td + 112, l3);
-            } else {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t h[16], l[16];
-                    block(q, h, l);
-                    tmem_st16(td + 16 * q, h);
-                }
+                tmem_st16(tmem + TM_D + lane_off + 32 * q, h);
+                if (SPLIT) tmem_st16(tmem + TM_D + lane_off + 32 * q + 16, l);
             }
             tmem_wait_st();
             fence_before_sync();
             named_sync(3, kGrp);
-            if (gt == 0) mbar_arrive(p_ready);
-            // ---- o
-            const float cx = ex2(rev ? g.tn[w] - rc : g.an[w] + rc);
-            if (!group_wait(oi_done, j & 1, 3, kGrp, poll) || !group_wait(op_done, j & 1, 3, kGrp, poll)) { failed = true; break; }
+            if (gt == 0) { mbar_arrive(p_ready); mbar_arrive(&g_free[b]); }
+        }
+        if (failed && gt == 0) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
+    } else {
+        // =================== O: the outputs (thread = row) ===================
+        const int w = warp & 3;
+        const bool poll = w == 0;
+        bool storing = false;      // (thread 0) a store may still read the tile
+        for (int j = 0; j < nchunk; ++j) {
+            const int b = j & 1, n = rows_of(j);
+            if (!group_wait(&g_full[b], (j >> 1) & 1, 4, kGrp, poll)) { failed = true; break; }
+            const float rc = gates[b].rc[gt];
+            const float cx = ex2(rev ? gates[b].bl[w] - rc : rc) * gates[b].re[w];
+            if (storing) bulk_wait_read();
+            if (!group_wait(oi_done, j & 1, 4, kGrp, poll)) { failed = true; break; }
             if (gt == 0) mbar_arrive(&g_free[b]);     // every thread of the group has read its gates
-            const long long t = (long long)sg.t0 + chunk(j) * C + gt;
+            if (!group_wait(op_done, j & 1, 4, kGrp, poll)) { failed = true; break; }
+            const bool staged = Ly::STAGED && n == C && !p.o_f32;
+            const int t0 = sg.t0 + chunk(j) * C;
             const bool live = gt < n;
-            const long long at = sg.b * p.ob + sg.h * p.oh + t * p.ot;
+            const long long at = sg.b * p.ob + sg.h * p.oh + (long long)(t0 + gt) * p.ot;
             float dot = 0.f;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < DZ; c += 32) {
                 float u[32], v[32];
-                tmem_ld32(tmem + TM_OI + lane_off + c, u);
-                tmem_ld32(tmem + TM_OP + lane_off + c, v);
+                tmem_ld32_pair(tmem + TM_OI + lane_off + c, tmem + TM_OP + lane_off + c, u, v);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] = fmaf(cx, u[i], v[i]);
-                if (live) {
+                if (staged) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8)
+                        sts128(sb + Ly::T_O + (uint32_t)((c + i) >> 6) * kHalf + swz(gt, ((c + i) & 63) >> 3),
+                               pack_bf16(v[i], v[i + 1]), pack_bf16(v[i + 2], v[i + 3]), pack_bf16(v[i + 4], v[i + 5]),
+                               pack_bf16(v[i + 6], v[i + 7]));
+                } else if (live) {
                     if (SPLIT) {
-                        const uint4* wp = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.w.p) +
-                                                                         sg.b * p.w.sb + (sg.h / p.w.div) * p.w.sh + t * p.w.st + c);
+                        const uint4* wp = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.w.p) + sg.b * p.w.sb +
+                                                                         (sg.h / p.w.div) * p.w.sh + (long long)(t0 + gt) * p.w.st + c);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const uint4 x = wp[i];
@@ -610,11 +670,22 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                     }
                 }
             }
-            if (SPLIT && live) p.dots[((long long)sg.b * a.l.geo.H + sg.h) * a.l.geo.T + t] = dot;
+            if (SPLIT && live) p.dots[((long long)sg.b * a.l.geo.H + sg.h) * a.l.geo.T + t0 + gt] = dot;
+            if (staged) fence_async_smem();
             fence_before_sync();
-            named_sync(3, kGrp);
-            if (gt == 0) mbar_arrive(o_free);
+            named_sync(4, kGrp);
+            if (gt == 0) {
+                mbar_arrive(o_free);
+                if (staged) {
+#pragma unroll
+                    for (int x = 0; x < DZ / 64; ++x)
+                        tma_store_4d(&maps[3], 64 * x, t0, sg.h, sg.b, sb + Ly::T_O + x * kHalf);
+                    bulk_commit();
+                    storing = true;
+                }
+            }
         }
+        if (storing) bulk_wait_all();
         if (failed && gt == 0) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
     }
     fence_before_sync();
@@ -674,6 +745,9 @@ cudaError_t launch_tc(const Launch& l, cudaStream_t s) {
             if (!p.states_only && !map_rows(&a.map[k][0], p.x, p.DX, T, H / p.x.div, l.B)) return cudaErrorInvalidValue;
             if (!map_rows(&a.map[k][1], p.y, p.DX, T, H / p.y.div, l.B)) return cudaErrorInvalidValue;
             if (!map_rows(&a.map[k][2], p.z, p.DZ, T, H / p.z.div, l.B)) return cudaErrorInvalidValue;
+            if (!p.states_only && !p.o_f32 &&
+                !map_rows(&a.map[k][3], View{p.o, p.ob, p.oh, p.ot, 1}, p.DZ, T, H, l.B))
+                return cudaErrorInvalidValue;
         }
         const bool split = q.dots != nullptr, states = q.states_only != 0;
         cudaError_t e;
