@@ -15,7 +15,7 @@
 // rounded to bf16 once: they only reach o, which is rounded to bf16 itself. Where per-token dots of the unrounded o
 // are asked for (the gradient of the gates is a sum in which they nearly cancel), P and R have two parts too (SPLIT).
 //
-// Exponents. Sums of gates are formed in 64 bits (in units of log2) and kept as fp32 offsets from the start of blocks of
+// Exponents. Sums of gates are formed in 64-bit fixed point (in units of log2) and kept as fp32 offsets from the start of blocks of
 // 32 tokens, so that they are accurate however much was forgotten before. Within a diagonal 32 x 32 block of P the
 // factor of a pair is one exponential; between blocks it is a product of three, each of a sum that is not positive
 // (forward: row to its block's start, that start to the column block's end, that end to the column), two of them per
@@ -141,6 +141,29 @@ __device__ __forceinline__ void tmem_st32_nowait(uint32_t taddr, const float (&v
     tmem_st16(taddr + 16, r + 16);
 }
 
+// Sixteen bytes of a y row times the row's weight, as hi + lo (zero if `off`, whatever they hold).
+__device__ __forceinline__ void scale16(const uint32_t (&u)[4], float w, bool off, uint32_t th, uint32_t tl) {
+    const float2 w2 = make_float2(w, w);
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 x = __fmul2_rn(make_float2(__uint_as_float(u[e] << 16), __uint_as_float(u[e] & 0xFFFF0000u)), w2);
+        h[e] = pack_bf16(x.x, x.y);
+        const float2 r = __fadd2_rn(x, make_float2(-__uint_as_float(h[e] << 16), -__uint_as_float(h[e] & 0xFFFF0000u)));
+        l[e] = pack_bf16(r.x, r.y);
+    }
+    if (off) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[e] = l[e] = 0u;
+    }
+    sts128(th, h[0], h[1], h[2], h[3]);
+    sts128(tl, l[0], l[1], l[2], l[3]);
+}
+
+__device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&u)[4]) {
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "r"(addr));
+}
+
 // The y rows of a chunk times their weights, as hi + lo, by `nt` threads; rows from n on become zero whatever they hold.
 template <int DX>
 __device__ __forceinline__ void scale_rows(uint32_t ty, uint32_t th, uint32_t tl, const GateBuf& g, int n, int tid, int nt) {
@@ -148,25 +171,10 @@ __device__ __forceinline__ void scale_rows(uint32_t ty, uint32_t th, uint32_t tl
 #pragma unroll 2
     for (int i = tid; i < C * PER; i += nt) {
         const int t = i / PER, c = i % PER;
-        const float w = g.cf[t] * g.ce[t >> 5];
-        const float2 w2 = make_float2(w, w);
         const uint32_t off = (uint32_t)(c >> 3) * kHalf + swz(t, c & 7);
         uint32_t u[4];
-        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "r"(ty + off));
-        uint32_t h[4], l[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 x = __fmul2_rn(make_float2(__uint_as_float(u[e] << 16), __uint_as_float(u[e] & 0xFFFF0000u)), w2);
-            h[e] = pack_bf16(x.x, x.y);
-            const float2 r = __fadd2_rn(x, make_float2(-__uint_as_float(h[e] << 16), -__uint_as_float(h[e] & 0xFFFF0000u)));
-            l[e] = pack_bf16(r.x, r.y);
-        }
-        if (t >= n) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) h[e] = l[e] = 0u;
-        }
-        sts128(th + off, h[0], h[1], h[2], h[3]);
-        sts128(tl + off, l[0], l[1], l[2], l[3]);
+        lds128(ty + off, u);
+        scale16(u, g.cf[t] * g.ce[t >> 5], t >= n, th + off, tl + off);
     }
 }
 
@@ -211,7 +219,8 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
     uint64_t* p_ready = bars + 17;   // C: P
     uint64_t* o_free = bars + 18;    // C: Oi and Op read
     uint64_t* drain = bars + 19;
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 20);
+    uint64_t* y_read = bars + 20;    // B: the y tile is in its registers
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 21);
     GateBuf* gates = reinterpret_cast<GateBuf*>(smem + Ly::GATES);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -226,7 +235,7 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
     const long long wl = a.l.wait_cycles;
 
     if (tid == 0) {
-        for (int i = 0; i < 20; ++i) mbar_init(bars + i, i == 9 || i == 10 ? (STATES ? 1 : 4) : 1);
+        for (int i = 0; i < 21; ++i) mbar_init(bars + i, i == 9 || i == 10 ? (STATES ? 1 : 4) : 1);
         mbar_fence_init();
     }
     if (warp == 0) tmem_alloc(tmem_holder, kTmemCols);
@@ -264,8 +273,9 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                     load(sb + Ly::T_Z + s * Ly::ZB, 2, DZ, hz, j, &full_z[s]);
                     ++nz;
                 } else {
-                    // y once D and Y~ of the chunk before are formed, x once its Oi is, z once the Op of its buffer is
-                    if (j >= 1 && (!mbar_wait(d_done, (j - 1) & 1, wl) || !mbar_wait(y_ready, (j - 1) & 1, wl))) { failed = true; break; }
+                    // y once the D before is formed and its tile in B's registers, x once its Oi is, z once the Op of its
+                    // buffer is
+                    if (j >= 1 && (!mbar_wait(d_done, (j - 1) & 1, wl) || !mbar_wait(y_read, (j - 1) & 1, wl))) { failed = true; break; }
                     load(sb + Ly::T_Y, 1, DX, hy, j, full_y);
                     ++ny;
                     if (j >= 1 && !mbar_wait(oi_done, (j - 1) & 1, wl)) { failed = true; break; }
@@ -359,60 +369,66 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
         __syncwarp();
     } else if (warp == 18) {
         // =================== gates: lane holds tokens 4 lane .. 4 lane + 3 ===================
+        // Sums in fixed point (log2 units, 32 fractional bits, 64 in all): exact, and unlike 64-bit floating point (with
+        // which this warp took 6.6 K cycles a chunk and held up all others) a few integer instructions each.
         const float* gp = p.g + sg.b * p.gb + sg.h * p.gh;
         auto raw = [&](int j, float (&r)[4]) {
             const int n = rows_of(j);
             const long long t0 = (long long)sg.t0 + chunk(j) * C;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = 4 * lane + i;
-                const float g = t < n ? gp[(t0 + t) * p.gt] : 0.f;
-                r[i] = g < kMinGate ? kMinGate : g;
-            }
+            for (int i = 0; i < 4; ++i) r[i] = 4 * lane + i < n ? gp[(t0 + 4 * lane + i) * p.gt] : 0.f;
         };
+        auto real = [](long long x) { return (float)x * 2.3283064365386963e-10f; };     // 2^-32
         float cur[4], nxt[4];
         if (nchunk > 0) raw(0, cur);
-        double passed = 0.0;    // gates of the chunks before (log2 units)
+        long long passed = 0;    // gates of the chunks before
+        float lost = 0.f;        // NaN once a gate was: it then reaches everything behind
         for (int j = 0; j < nchunk; ++j) {
             if (j + 1 < nchunk) raw(j + 1, nxt);
-            double x[4];
-            x[0] = (double)cur[0];
+            long long x[4];
+            bool nan = false;
 #pragma unroll
-            for (int i = 1; i < 4; ++i) x[i] = x[i - 1] + (double)cur[i];
-            double s = x[3];
+            for (int i = 0; i < 4; ++i) {
+                nan |= !(cur[i] <= 1e4f);        // (gates are not positive; one that large is no gate either)
+                const float g = cur[i] < kMinGate ? kMinGate : cur[i];
+                x[i] = __float2ll_rn(g * (float)kLog2e * 4294967296.f) + (i > 0 ? x[i - 1] : 0);
+            }
+            if (__any_sync(0xffffffffu, nan)) lost = __int_as_float(0x7fc00000);
+            long long s = x[3];
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
-                const double y = __shfl_up_sync(0xffffffffu, s, off);
+                const long long y = __shfl_up_sync(0xffffffffu, s, off);
                 if (lane >= off) s += y;
             }
-            const double all = __shfl_sync(0xffffffffu, s, 31);
-            const double before = s - x[3];                                         // exclusive
+            const long long all = __shfl_sync(0xffffffffu, s, 31);
+            const long long before = s - x[3];                                       // exclusive
             // this lane's block: its start, its end
-            const double start = __shfl_sync(0xffffffffu, before, lane & ~7), end = __shfl_sync(0xffffffffu, s, lane | 7);
+            const long long start = __shfl_sync(0xffffffffu, before, lane & ~7), end = __shfl_sync(0xffffffffu, s, lane | 7);
+            // lanes 4 i + j of the first 16: blocks i and j
+            const int bi = (lane >> 2) & 3, bj = lane & 3;
+            const long long si = __shfl_sync(0xffffffffu, before, 8 * bi), sj = __shfl_sync(0xffffffffu, before, 8 * bj);
+            const long long ei = __shfl_sync(0xffffffffu, s, 8 * bi + 7), ej = __shfl_sync(0xffffffffu, s, 8 * bj + 7);
             const int b = j & 1;
             bool ok = true;
             if (j >= 2) ok = mbar_wait(&g_free[b], ((j - 2) >> 1) & 1, wl);
             if (!__all_sync(0xffffffffu, ok)) { failed = true; break; }
             GateBuf& g = gates[b];
-            const double far = STATES ? passed : 0.0;
+            const long long far = STATES ? passed : 0;
+            float up[4], cf[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float up = (float)(((before - start) + x[i]) * kLog2e);
-                g.rc[4 * lane + i] = up;
-                g.cf[4 * lane + i] = ex2(rev ? up : (float)((end - before - x[i]) * kLog2e));
+                up[i] = real(before - start + x[i]) + lost;
+                cf[i] = ex2(rev ? up[i] : real(end - before - x[i])) + lost;
             }
-            {   // lanes 4 i + j of the first 16: blocks i and j
-                const int bi = (lane >> 2) & 3, bj = lane & 3;
-                const double si = __shfl_sync(0xffffffffu, before, 8 * bi), sj = __shfl_sync(0xffffffffu, before, 8 * bj);
-                const double ei = __shfl_sync(0xffffffffu, s, 8 * bi + 7), ej = __shfl_sync(0xffffffffu, s, 8 * bj + 7);
-                if (lane < 16) g.f[bi][bj] = ex2((float)((rev ? sj - ei : si - ej) * kLog2e));
-                if (lane < 4) {
-                    g.bl[lane] = (float)((ej - sj) * kLog2e);
-                    g.ce[lane] = ex2((float)(((rev ? sj : all - ej) + far) * kLog2e));
-                    g.re[lane] = ex2((float)((rev ? all - ej : sj) * kLog2e));
-                }
-                if (lane == 0) g.en = ex2((float)(all * kLog2e));
+            *reinterpret_cast<float4*>(g.rc + 4 * lane) = make_float4(up[0], up[1], up[2], up[3]);
+            *reinterpret_cast<float4*>(g.cf + 4 * lane) = make_float4(cf[0], cf[1], cf[2], cf[3]);
+            if (lane < 16) g.f[bi][bj] = ex2(real(rev ? sj - ei : si - ej));
+            if (lane < 4) {
+                g.bl[lane] = real(ej - sj);
+                g.ce[lane] = ex2(real((rev ? sj : all - ej) + far));
+                g.re[lane] = ex2(real(rev ? all - ej : sj));
             }
+            if (lane == 0) g.en = ex2(real(all)) + lost;
             passed += all;
             __syncwarp();
             if (lane == 0) mbar_arrive(&g_full[b]);
@@ -420,7 +436,7 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
             for (int i = 0; i < 4; ++i) cur[i] = nxt[i];
         }
         if (failed && lane == 0) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
-        if (STATES && p.gsum && lane == 0) p.gsum[sg.entry] = (float)passed;
+        if (STATES && p.gsum && lane == 0) p.gsum[sg.entry] = real(passed) * 0.6931471805599453f + lost;
     } else if (STATES) {
         // =================== all groups: Y~; then the state ===================
         constexpr uint32_t N = 4 * kGrp;
@@ -531,13 +547,32 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
         if (failed && gt == 0) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
     } else if (grp == 1) {
         // =================== B: Y~ ===================
+        // The whole y tile goes into registers as soon as it has landed, so that the next one is on its way while this
+        // one's parts are formed and while the R of the chunk before still reads the parts of its own.
+        constexpr int PER = DX / 8, IT = C * PER / kGrp;     // 16-byte pieces of a row, pieces of a thread
+        const int t0 = gt / PER, c = gt % PER;               // piece i: token t0 + i (kGrp / PER), always column c
+        const uint32_t col = (uint32_t)(c >> 3) * kHalf;
         for (int j = 0; j < nchunk; ++j) {
             const int b = j & 1, n = rows_of(j), s = j % Ly::NZ;
             const bool poll = warp == 4;
-            if (!group_wait(&g_full[b], (j >> 1) & 1, 2, kGrp, poll) || !group_wait(full_y, j & 1, 2, kGrp, poll) ||
-                (j > 0 && !group_wait(r_done, (j - 1) & 1, 2, kGrp, poll)) ||
+            if (!group_wait(full_y, j & 1, 2, kGrp, poll)) { failed = true; break; }
+            uint32_t u[IT][4];
+#pragma unroll
+            for (int i = 0; i < IT; ++i) lds128(sb + Ly::T_Y + col + swz(t0 + i * (kGrp / PER), c & 7), u[i]);
+            // (the shared loads have completed when the barriers of the next waits are passed: their values are used behind)
+#pragma unroll
+            for (int i = 0; i < IT; ++i) asm volatile("" : "+r"(u[i][0]), "+r"(u[i][1]), "+r"(u[i][2]), "+r"(u[i][3]));
+            named_sync(2, kGrp);
+            if (gt == 0) mbar_arrive(y_read);
+            if (!group_wait(&g_full[b], (j >> 1) & 1, 2, kGrp, poll) || (j > 0 && !group_wait(r_done, (j - 1) & 1, 2, kGrp, poll)) ||
                 (n < C && !group_wait(&full_z[s], (j / Ly::NZ) & 1, 2, kGrp, poll))) { failed = true; break; }
-            scale_rows<DX>(sb + Ly::T_Y, sb + Ly::T_YH, sb + Ly::T_YL, gates[b], n, gt, kGrp);
+            const GateBuf& g = gates[b];
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                const int t = t0 + i * (kGrp / PER);
+                const uint32_t off = col + swz(t, c & 7);
+                scale16(u[i], g.cf[t] * g.ce[t >> 5], t >= n, sb + Ly::T_YH + off, sb + Ly::T_YL + off);
+            }
             if (n < C) clear_rows<DZ>(sb + Ly::T_Z + s * Ly::ZB, n, gt, kGrp);
             fence_async_smem();
             named_sync(2, kGrp);
