@@ -21,7 +21,7 @@
 // (forward: row to its block's start, that start to the column block's end, that end to the column), two of them per
 // token and one per pair of blocks: a quarter of the exponentials, and nothing overflows for any gate.
 //
-// Work split: four groups of four warps (thread = lane of tensor memory) and three single warps:
+// Work split: groups of four warps (thread = lane of tensor memory; B has eight) and three single warps:
 //   A  the state: R to bf16 in shared memory, e^{G_n} R back        B  Y~ from Y
 //   C  P from D                                                     O  o from Oi and Op
 //   copies (TMA), MMA issue, gates
@@ -38,6 +38,7 @@
 // Bound: by the bytes of x, y, z and o (1 KB a token and head at 128 x 128): a chunk is 128 KB, 5.6 K cycles of its
 // share of HBM bandwidth on 152 SMs, against 2.6 K cycles of products and about 2.5 K of each group's work.
 #include <cstring>
+#include <type_traits>
 
 #include "hd_internal.h"
 #include "tc_common.cuh"
@@ -50,7 +51,9 @@ using namespace tc;
 
 constexpr int C = kChunk;                  // 128
 constexpr int kGrp = 128;
-constexpr int NT = 4 * kGrp + 96;          // groups A, B, C, O; warps 16 (copies), 17 (MMA issue), 18 (gates)
+constexpr int kAhead = 3;                  // chunks between a row's way into L2 and into shared memory
+constexpr int kGrpB = 2 * kGrp;            // group B has eight warps
+constexpr int NT = 5 * kGrp + 96;          // groups A, B, C, O; warps 20 (copies), 21 (MMA issue), 22 (gates)
 constexpr uint32_t kHalf = C * 128;        // bytes of a half tile: 128 rows of 64 bf16
 constexpr uint32_t TM_R = 0, TM_D = 128, TM_OI = 256, TM_OP = 384, kTmemCols = 512;
 constexpr double kLog2e = 1.4426950408889634;
@@ -89,7 +92,7 @@ struct Layout {
     static constexpr bool STAGED = !SPLIT && !STATES;
     static constexpr int GATES = T_O + (STAGED ? ZB : 0);
     static constexpr int BARS = GATES + 2 * (int)sizeof(GateBuf);
-    static constexpr int TOTAL = BARS + 256;
+    static constexpr int TOTAL = BARS + 256;   // 23 barriers, the address of the tensor memory
     static_assert(TOTAL <= 227 * 1024, "shared memory budget");
 };
 
@@ -107,6 +110,10 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* map, int c0, int t, int h, int b) {
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];"
+                 :: "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(t), "r"(h), "r"(b) : "memory");
+}
 __device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, int c0, int t, int h, int b, uint32_t src) {
     asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];"
                  :: "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(t), "r"(h), "r"(b), "r"(src) : "memory");
@@ -142,6 +149,7 @@ __device__ __forceinline__ void tmem_st32_nowait(uint32_t taddr, const float (&v
 }
 
 // Sixteen bytes of a y row times the row's weight, as hi + lo (zero if `off`, whatever they hold).
+template <bool CHECK>
 __device__ __forceinline__ void scale16(const uint32_t (&u)[4], float w, bool off, uint32_t th, uint32_t tl) {
     const float2 w2 = make_float2(w, w);
     uint32_t h[4], l[4];
@@ -149,10 +157,11 @@ __device__ __forceinline__ void scale16(const uint32_t (&u)[4], float w, bool of
     for (int e = 0; e < 4; ++e) {
         const float2 x = __fmul2_rn(make_float2(__uint_as_float(u[e] << 16), __uint_as_float(u[e] & 0xFFFF0000u)), w2);
         h[e] = pack_bf16(x.x, x.y);
-        const float2 r = __fadd2_rn(x, make_float2(-__uint_as_float(h[e] << 16), -__uint_as_float(h[e] & 0xFFFF0000u)));
+        const float2 r = __ffma2_rn(make_float2(__uint_as_float(h[e] << 16), __uint_as_float(h[e] & 0xFFFF0000u)),
+                                    make_float2(-1.f, -1.f), x);
         l[e] = pack_bf16(r.x, r.y);
     }
-    if (off) {
+    if (CHECK && off) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) h[e] = l[e] = 0u;
     }
@@ -174,7 +183,7 @@ __device__ __forceinline__ void scale_rows(uint32_t ty, uint32_t th, uint32_t tl
         const uint32_t off = (uint32_t)(c >> 3) * kHalf + swz(t, c & 7);
         uint32_t u[4];
         lds128(ty + off, u);
-        scale16(u, g.cf[t] * g.ce[t >> 5], t >= n, th + off, tl + off);
+        scale16<true>(u, g.cf[t] * g.ce[t >> 5], t >= n, th + off, tl + off);
     }
 }
 
@@ -212,15 +221,17 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
     uint64_t* g_free = bars + 9;     // [2] one arrival per group
     uint64_t* d_done = bars + 11;    // D
     uint64_t* oi_done = bars + 12;   // Oi
-    uint64_t* r_done = bars + 13;    // R
+    uint64_t* r_done = bars + 13;    // R (all of its tokens)
     uint64_t* op_done = bars + 14;   // Op
-    uint64_t* y_ready = bars + 15;   // B: Y~ (and a cleared z)
+    uint64_t* y_ready = bars + 15;   // B: Y~ of the first 64 tokens (and a cleared z); a states pass: all of it
     uint64_t* r_ready = bars + 16;   // A: R scaled, its bf16 copy written
     uint64_t* p_ready = bars + 17;   // C: P
     uint64_t* o_free = bars + 18;    // C: Oi and Op read
     uint64_t* drain = bars + 19;
     uint64_t* y_read = bars + 20;    // B: the y tile is in its registers
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 21);
+    uint64_t* y_rest = bars + 21;    // B: Y~ of the other 64 tokens
+    uint64_t* r_half = bars + 22;    // R from the first 64 tokens
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 23);
     GateBuf* gates = reinterpret_cast<GateBuf*>(smem + Ly::GATES);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -235,7 +246,7 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
     const long long wl = a.l.wait_cycles;
 
     if (tid == 0) {
-        for (int i = 0; i < 21; ++i) mbar_init(bars + i, i == 9 || i == 10 ? (STATES ? 1 : 4) : 1);
+        for (int i = 0; i < 23; ++i) mbar_init(bars + i, i == 9 || i == 10 ? (STATES ? 1 : 4) : 1);
         mbar_fence_init();
     }
     if (warp == 0) tmem_alloc(tmem_holder, kTmemCols);
@@ -254,7 +265,7 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
         return !bad;
     };
 
-    if (warp == 16) {
+    if (warp == 20) {
         // =================== copies ===================
         if (lane == 0) {
             const int hx = sg.h / p.x.div, hy = sg.h / p.y.div, hz = sg.h / p.z.div;
@@ -264,7 +275,20 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                 for (int x = 0; x < D / 64; ++x)
                     tma_load_4d(dst + x * kHalf, &maps[which], 64 * x, sg.t0 + chunk(j) * C, h, sg.b, bar);
             };
+            // Shared memory has room for one x and one y tile only, and a load under load takes 3 K cycles or more: the
+            // rows are brought into L2 kAhead chunks before they are wanted.
+            auto prefetch = [&](int j) {
+                if (j >= nchunk) return;
+                const int t = sg.t0 + chunk(j) * C;
+                for (int x = 0; x < DX / 64; ++x) {
+                    tma_prefetch_4d(&maps[1], 64 * x, t, hy, sg.b);
+                    if (!STATES) tma_prefetch_4d(&maps[0], 64 * x, t, hx, sg.b);
+                }
+                for (int x = 0; x < DZ / 64; ++x) tma_prefetch_4d(&maps[2], 64 * x, t, hz, sg.b);
+            };
+            for (int j = 1; j < kAhead; ++j) prefetch(j);
             for (int j = 0; j < nchunk; ++j) {
+                if (j > 0 || kAhead == 1) prefetch(j + kAhead - 1);
                 if (STATES) {
                     const int s = j & 1;
                     if (j >= 2 && !mbar_wait(&free_z[s], ((j - 2) >> 1) & 1, wl)) { failed = true; break; }
@@ -297,7 +321,7 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                 if (nz > s) mbar_wait(&full_z[s], ((nz - 1 - s) / Ly::NZ) & 1, most);
         }
         __syncwarp();
-    } else if (warp == 17) {
+    } else if (warp == 21) {
         // =================== MMA issue (lane 0; the others wait at the end) ===================
         if (lane == 0) {
             auto wait1 = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -325,11 +349,11 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                                   s > 0 || h > 0);
                 mma_commit(oi_done);
             };
-            auto mma_R = [&](uint32_t tz, bool acc) {
+            auto mma_R = [&](uint32_t tz, int half, bool acc) {      // 64 tokens: four slices of 2048 bytes
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
-                    mma_chain(tmem + TM_R, smem_desc_sw128(sb + (s ? Ly::T_YL : Ly::T_YH), kHalf, 1024), 2048,
-                              smem_desc_sw128(tz, kHalf, 1024), 2048, idR, C, acc || s > 0);
+                    mma_chain(tmem + TM_R, smem_desc_sw128(sb + (s ? Ly::T_YL : Ly::T_YH) + 8192 * half, kHalf, 1024), 2048,
+                              smem_desc_sw128(tz + 8192 * half, kHalf, 1024), 2048, idR, 64, acc || s > 0);
             };
             auto mma_Op = [&](uint32_t tz) {
                 const uint64_t dz = smem_desc_sw128(tz, kHalf, 1024);
@@ -345,7 +369,8 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                 const uint32_t tz = sb + Ly::T_Z + s * Ly::ZB, zpar = STATES ? (j >> 1) & 1 : (j / Ly::NZ) & 1;
                 if (STATES) {
                     if (!wait1(y_ready, j & 1) || !wait1(&full_z[s], zpar)) { failed = true; break; }
-                    mma_R(tz, j > 0);
+                    mma_R(tz, 0, j > 0);
+                    mma_R(tz, 1, true);
                     mma_commit(&free_z[s]);
                     mma_commit(r_done);
                     continue;
@@ -355,7 +380,10 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                 if (!wait1(r_ready, j & 1) || (j > 0 && !wait1(o_free, (j - 1) & 1))) { failed = true; break; }
                 mma_Oi();
                 if (!wait1(y_ready, j & 1) || !wait1(&full_z[s], zpar)) { failed = true; break; }
-                mma_R(tz, true);
+                mma_R(tz, 0, true);
+                mma_commit(r_half);
+                if (!wait1(y_rest, j & 1)) { failed = true; break; }
+                mma_R(tz, 1, true);
                 mma_commit(r_done);
                 if (!wait1(p_ready, j & 1)) { failed = true; break; }
                 mma_Op(tz);
@@ -367,7 +395,7 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
             mbar_wait(drain, 0, 400000000LL);
         }
         __syncwarp();
-    } else if (warp == 18) {
+    } else if (warp == 22) {
         // =================== gates: lane holds tokens 4 lane .. 4 lane + 3 ===================
         // Sums in fixed point (log2 units, 32 fractional bits, 64 in all): exact, and unlike 64-bit floating point (with
         // which this warp took 6.6 K cycles a chunk and held up all others) a few integer instructions each.
@@ -439,7 +467,7 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
         if (STATES && p.gsum && lane == 0) p.gsum[sg.entry] = real(passed) * 0.6931471805599453f + lost;
     } else if (STATES) {
         // =================== all groups: Y~; then the state ===================
-        constexpr uint32_t N = 4 * kGrp;
+        constexpr uint32_t N = 5 * kGrp;
         for (int j = 0; j < nchunk; ++j) {
             const int s = j & 1, n = rows_of(j);
             if (!group_wait(&g_full[s], (j >> 1) & 1, 1, N, warp == 0) || !group_wait(&full_y[s], (j >> 1) & 1, 1, N, warp == 0) ||
@@ -517,7 +545,10 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                         if (SPLIT) sts128(tr + Ly::RB + off, l[0], l[1], l[2], l[3]);
                     }
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] *= en;
+                    for (int i = 0; i < 32; i += 2) {
+                        const float2 x = __fmul2_rn(make_float2(v[i], v[i + 1]), make_float2(en, en));
+                        v[i] = x.x; v[i + 1] = x.y;
+                    }
                     tmem_st32_nowait(tmem + TM_R + lane_off + c, v);
                 }
                 tmem_wait_st();
@@ -545,41 +576,56 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
             }
         }
         if (failed && gt == 0) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
-    } else if (grp == 1) {
+    } else if (grp <= 2) {
         // =================== B: Y~ ===================
         // The whole y tile goes into registers as soon as it has landed, so that the next one is on its way while this
         // one's parts are formed and while the R of the chunk before still reads the parts of its own.
-        constexpr int PER = DX / 8, IT = C * PER / kGrp;     // 16-byte pieces of a row, pieces of a thread
-        const int t0 = gt / PER, c = gt % PER;               // piece i: token t0 + i (kGrp / PER), always column c
+        constexpr int PER = DX / 8, IT = C * PER / kGrpB;    // 16-byte pieces of a row, pieces of a thread
+        const int bt = tid - kGrp, t0 = bt / PER, c = bt % PER;   // piece i: token t0 + i (kGrpB / PER), always column c
         const uint32_t col = (uint32_t)(c >> 3) * kHalf;
         for (int j = 0; j < nchunk; ++j) {
             const int b = j & 1, n = rows_of(j), s = j % Ly::NZ;
             const bool poll = warp == 4;
-            if (!group_wait(full_y, j & 1, 2, kGrp, poll)) { failed = true; break; }
+            if (!group_wait(full_y, j & 1, 2, kGrpB, poll)) { failed = true; break; }
             uint32_t u[IT][4];
 #pragma unroll
-            for (int i = 0; i < IT; ++i) lds128(sb + Ly::T_Y + col + swz(t0 + i * (kGrp / PER), c & 7), u[i]);
+            for (int i = 0; i < IT; ++i) lds128(sb + Ly::T_Y + col + swz(t0 + i * (kGrpB / PER), c & 7), u[i]);
             // (the shared loads have completed when the barriers of the next waits are passed: their values are used behind)
 #pragma unroll
             for (int i = 0; i < IT; ++i) asm volatile("" : "+r"(u[i][0]), "+r"(u[i][1]), "+r"(u[i][2]), "+r"(u[i][3]));
-            named_sync(2, kGrp);
-            if (gt == 0) mbar_arrive(y_read);
-            if (!group_wait(&g_full[b], (j >> 1) & 1, 2, kGrp, poll) || (j > 0 && !group_wait(r_done, (j - 1) & 1, 2, kGrp, poll)) ||
-                (n < C && !group_wait(&full_z[s], (j / Ly::NZ) & 1, 2, kGrp, poll))) { failed = true; break; }
+            named_sync(2, kGrpB);
+            if (bt == 0) mbar_arrive(y_read);
+            if (!group_wait(&g_full[b], (j >> 1) & 1, 2, kGrpB, poll) || (j > 0 && !group_wait(r_half, (j - 1) & 1, 2, kGrpB, poll)) ||
+                (n < C && !group_wait(&full_z[s], (j / Ly::NZ) & 1, 2, kGrpB, poll))) { failed = true; break; }
             const GateBuf& g = gates[b];
+            // two halves of 64 tokens, so that the products of one run while the other is formed
+            auto half = [&](auto check, int h) {
+                constexpr int TS = kGrpB / PER, HI = IT / 2;     // tokens between two pieces, pieces of a half
+                float w[HI];       // read ahead of the stores, which the compiler moves no load across
 #pragma unroll
-            for (int i = 0; i < IT; ++i) {
-                const int t = t0 + i * (kGrp / PER);
-                const uint32_t off = col + swz(t, c & 7);
-                scale16(u[i], g.cf[t] * g.ce[t >> 5], t >= n, sb + Ly::T_YH + off, sb + Ly::T_YL + off);
-            }
-            if (n < C) clear_rows<DZ>(sb + Ly::T_Z + s * Ly::ZB, n, gt, kGrp);
+                for (int i = 0; i < HI; ++i) w[i] = g.cf[t0 + (h * HI + i) * TS] * g.ce[(h * HI + i) * TS / 32];
+#pragma unroll
+                for (int i = 0; i < HI; ++i) {
+                    const int t = t0 + (h * HI + i) * TS;
+                    const uint32_t off = col + swz(t, c & 7);
+                    scale16<check.value>(u[h * HI + i], w[i], t >= n, sb + Ly::T_YH + off, sb + Ly::T_YL + off);
+                }
+            };
+            if (n == C) half(std::false_type{}, 0);
+            else half(std::true_type{}, 0);
+            if (n < C) clear_rows<DZ>(sb + Ly::T_Z + s * Ly::ZB, n, bt, kGrpB);
             fence_async_smem();
-            named_sync(2, kGrp);
-            if (gt == 0) { mbar_arrive(y_ready); mbar_arrive(&g_free[b]); }
+            named_sync(2, kGrpB);
+            if (bt == 0) mbar_arrive(y_ready);
+            if (j > 0 && !group_wait(r_done, (j - 1) & 1, 2, kGrpB, poll)) { failed = true; break; }
+            if (n == C) half(std::false_type{}, 1);
+            else half(std::true_type{}, 1);
+            fence_async_smem();
+            named_sync(2, kGrpB);
+            if (bt == 0) { mbar_arrive(y_rest); mbar_arrive(&g_free[b]); }
         }
-        if (failed && gt == 0) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
-    } else if (grp == 2) {
+        if (failed && bt == 0) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
+    } else if (grp == 3) {
         // =================== C: P (thread = row) ===================
         const int w = warp & 3;
         const bool poll = w == 0;
@@ -602,15 +648,15 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                     float v[32];
                     tmem_ld32(tmem + TM_D + lane_off + 32 * q, v);
                     if (q == w) {
-                        const float base = -sgn * rc;
+                        const float2 s2 = make_float2(sgn, sgn), b2 = make_float2(-sgn * rc, -sgn * rc);
                         const float4* col = reinterpret_cast<const float4*>(g.rc + 32 * q);
 #pragma unroll
                         for (int i = 0; i < 32; i += 4) {
                             const float4 cc = col[i >> 2];
-                            v[i] *= ex2(fmaf(sgn, cc.x, base));
-                            v[i + 1] *= ex2(fmaf(sgn, cc.y, base));
-                            v[i + 2] *= ex2(fmaf(sgn, cc.z, base));
-                            v[i + 3] *= ex2(fmaf(sgn, cc.w, base));
+                            const float2 x = __ffma2_rn(make_float2(cc.x, cc.y), s2, b2), y = __ffma2_rn(make_float2(cc.z, cc.w), s2, b2);
+                            const float2 vx = __fmul2_rn(make_float2(v[i], v[i + 1]), make_float2(ex2(x.x), ex2(x.y)));
+                            const float2 vy = __fmul2_rn(make_float2(v[i + 2], v[i + 3]), make_float2(ex2(y.x), ex2(y.y)));
+                            v[i] = vx.x; v[i + 1] = vx.y; v[i + 2] = vy.x; v[i + 3] = vy.y;
                         }
                     } else {
                         const float rf = row * g.f[w][q];
@@ -626,10 +672,11 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                     }
                     // columns that this row sees: up to its own token, or from it to the chunk's last
                     if (q == w || (rev && n < C)) {
-                        const int lo = rev ? (q == w ? lane : 0) : 0, hi = rev ? n - 1 - 32 * q : lane;
+                        uint32_t seen = q == w ? (rev ? ~0u << lane : ~0u >> (31 - lane)) : ~0u;
+                        if (rev && 32 * q + 31 >= n) seen &= 32 * q >= n ? 0u : ~0u >> (32 - (n - 32 * q));
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            if (i < lo || i > hi) v[i] = 0.f;
+                            if (!(seen & (1u << i))) v[i] = 0.f;
                     }
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
@@ -670,7 +717,10 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                 float u[32], v[32];
                 tmem_ld32_pair(tmem + TM_OI + lane_off + c, tmem + TM_OP + lane_off + c, u, v);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = fmaf(cx, u[i], v[i]);
+                for (int i = 0; i < 32; i += 2) {
+                    const float2 x = __ffma2_rn(make_float2(u[i], u[i + 1]), make_float2(cx, cx), make_float2(v[i], v[i + 1]));
+                    v[i] = x.x; v[i + 1] = x.y;
+                }
                 if (staged) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 8)
