@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import Optional, Tuple
 
@@ -706,29 +707,22 @@ def dplr_hd_decode_step(desc, n_slots, slots, q, k, v, decay, S, o, status, stre
                                              S, _ref(o), status, stream))
 
 
-def _hd(t: torch.Tensor) -> dplr_hd_tensor:
-    """A [B,H,T,d] (or [B,H,T] gates) tensor with its own strides."""
-    st = t.stride()
-    return dplr_hd_tensor(t.data_ptr(), st[0], st[1], st[2])
+class _Slots:
+    """The dplr_hd_tensor arguments of one prepared call, in one buffer that each call fills anew: a call's host time is
+    its launches', and building a ctypes structure per tensor and call took longer than those."""
+
+    def __init__(self, n: int):
+        self.buf = ctypes.create_string_buffer(32 * n)
+        at = ctypes.addressof(self.buf)
+        self.refs = [ctypes.cast(at + 32 * i, ctypes.POINTER(dplr_hd_tensor)) for i in range(n)]
+        self.fill = struct.Struct(f"={4 * n}q").pack_into
+
+    def __call__(self, *values):
+        self.fill(self.buf, 0, *values)
 
 
-def _hd_rows(t: torch.Tensor) -> dplr_hd_tensor:
-    """A [tokens,H,d] (or [tokens,H] gates) tensor as one batch entry."""
-    st = t.stride()
-    return dplr_hd_tensor(t.data_ptr(), 0, st[1], st[0])
-
-
-def _hd_step(t: torch.Tensor) -> dplr_hd_tensor:
-    """A [rows,H,d] (or [rows,H] gates) tensor whose rows are batch entries of one token."""
-    st = t.stride()
-    return dplr_hd_tensor(t.data_ptr(), st[0], st[1], 0)
-
-
-_HEAD_GATES = lambda t: dplr_hd_tensor(t.data_ptr(), 0, 0, 0)  # noqa: E731
-
-
-def _need_view(t, name, device, dtype, shape, features=True):
-    """Like _need, for a tensor that may be strided (its feature axis contiguous)."""
+def _refuse(t, name, device, dtype, shape):
+    """Says what is wrong with a tensor that _bad found wrong."""
     if t is None:
         raise ValueError(f"{name} is required")
     if t.device != device:
@@ -737,13 +731,8 @@ def _need_view(t, name, device, dtype, shape, features=True):
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if features and t.numel() > 0:
-        if t.stride(-1) != 1:
-            raise ValueError(f"{name} must be contiguous along its last axis")
-        if any(n > 1 and (s <= 0 or s * t.element_size() % 16) for n, s in zip(t.shape[:-1], t.stride()[:-1])):
-            raise ValueError(f"{name} needs strides that are positive multiples of 16 bytes")
-        if t.data_ptr() % 16:
-            raise ValueError(f"{name} must start on a 16-byte boundary")
+    raise ValueError(f"{name} must be contiguous along its last axis, start on a 16-byte boundary and have strides that "
+                     "are positive multiples of 16 bytes")
 
 
 class _HeadDecayBase:
@@ -759,6 +748,8 @@ class _HeadDecayBase:
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
         self.path = dplr_hd_path(self.desc)
+        self._unit = 16 // self.in_dtype.itemsize       # strides are multiples of this
+        self._desc_ref = ctypes.byref(self.desc)
 
     def _workspace(self, nbytes, name):
         if nbytes == 0:
@@ -773,17 +764,50 @@ class _HeadDecayBase:
             return torch.zeros((B, T, heads, d), dtype=dt, device=self.device).transpose(1, 2)
         return torch.zeros((B, heads, T, d), dtype=dt, device=self.device)
 
-    def _stream(self, stream):
-        return (stream if stream is not None else torch.cuda.current_stream(self.device)).cuda_stream
+    def _at(self, t, name, shape):
+        """Address and strides of a row tensor (features last), checked."""
+        if t is None or t.dtype is not self.in_dtype or t.shape != shape or t.device != self.device:
+            _refuse(t, name, self.device, self.in_dtype, shape)
+        p, st, u = t.data_ptr(), t.stride(), self._unit
+        if t.numel() and (st[-1] != 1 or p & 15):
+            _refuse(t, name, self.device, self.in_dtype, shape)
+        for n, s in zip(shape, st[:-1]):
+            if n > 1 and (s <= 0 or s % u) and t.numel():
+                _refuse(t, name, self.device, self.in_dtype, shape)
+        return p, st
 
-    def _gates(self, decay, shape, wrap):
+    def _gates(self, t, shape):
+        """Address and strides of the log-gates, checked (all strides 0 with per_head)."""
+        want = (self.H,) if self.per_head else shape
+        if t is None or t.dtype is not torch.float32 or t.shape != want or t.device != self.device:
+            _refuse(t, "decay", self.device, torch.float32, want)
+        st = t.stride()
         if self.per_head:
-            _need(decay, "decay", self.device, torch.float32, (self.H,))
-            return _HEAD_GATES(decay)
-        _need_view(decay, "decay", self.device, torch.float32, shape, features=False)
-        if any(s < 0 for s in decay.stride()):
+            if self.H > 1 and st[0] != 1:
+                raise ValueError("decay must be contiguous")
+            return t.data_ptr(), (0, 0, 0)
+        if min(st) < 0:
             raise ValueError("decay needs non-negative strides")
-        return wrap(decay)
+        return t.data_ptr(), st
+
+    def _state(self, t, name, shape):
+        if t is None:
+            return None
+        if t.dtype is not torch.float32 or t.shape != shape or t.device != self.device or not t.is_contiguous():
+            _need(t, name, self.device, torch.float32, shape)
+        return t.data_ptr()
+
+    def _call(self, fn, name, stream, *args):
+        """The C call on this object's device and a stream, as its last argument."""
+        i = self.device.index
+        s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(i)
+        if torch.cuda.current_device() == i:
+            st = fn(self._desc_ref, *args, s)
+        else:
+            with torch.cuda.device(i):
+                st = fn(self._desc_ref, *args, s)
+        if st != DPLR_OK:
+            raise DplrError(st, name)
 
     def device_status(self, clear: bool = False) -> int:
         """The workspace's device status word (0, or DPLR_ERR_TIMEOUT after a bounded wait gave up), read
@@ -808,23 +832,25 @@ class HeadDecay(_HeadDecayBase):
             self._workspace(dplr_hd_workspace_size(self.desc), "dplr_hd_workspace_size")
             self.o = self._rows(H, dv, token_major)
             self.S_T = torch.empty((B, H, dk, dv), dtype=torch.float32, device=self.device)
+        self._fn, self._slots = library().dplr_hd_forward, _Slots(5)
 
     def __call__(self, q, k, v, decay, S0=None,
                  stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
         """q, k [B,Hq,T,dk], v [B,H,T,dv], strided as they are; decay [B,H,T] fp32, or [H] with per_head."""
-        B, H, Hq, T, dev, dt = self.B, self.H, self.Hq, self.T, self.device, self.in_dtype
-        _need_view(q, "q", dev, dt, (B, Hq, T, self.dk))
-        _need_view(k, "k", dev, dt, (B, Hq, T, self.dk))
-        _need_view(v, "v", dev, dt, (B, H, T, self.dv))
-        g = self._gates(decay, (B, H, T), _hd)
-        if S0 is not None:
-            _need(S0, "S0", dev, torch.float32, (B, H, self.dk, self.dv))
-        with torch.cuda.device(dev):
-            st = dplr_hd_forward(self.desc, _hd(q), _hd(k), _hd(v), g, _ptr(S0), _hd(self.o), _ptr(self.S_T),
-                                 _ptr(self.workspace), self.ws_bytes, self._stream(stream))
-        if st != DPLR_OK:
-            raise DplrError(st, "dplr_hd_forward")
-        return self.o, self.S_T
+        B, H, T = self.B, self.H, self.T
+        qk = (B, self.Hq, T, self.dk)
+        (pq, sq), (pk, sk) = self._at(q, "q", qk), self._at(k, "k", qk)
+        pv, sv = self._at(v, "v", (B, H, T, self.dv))
+        pg, sg = self._gates(decay, (B, H, T))
+        o, so = self.o, self.o.stride()
+        f = self._slots
+        f(pq, sq[0], sq[1], sq[2], pk, sk[0], sk[1], sk[2], pv, sv[0], sv[1], sv[2], pg, sg[0], sg[1], sg[2], o.data_ptr(),
+          so[0], so[1], so[2])
+        r = f.refs
+        self._call(self._fn, "dplr_hd_forward", stream, r[0], r[1], r[2], r[3],
+                   self._state(S0, "S0", (B, H, self.dk, self.dv)), r[4], self.S_T.data_ptr(), self.workspace.data_ptr(),
+                   self.ws_bytes)
+        return o, self.S_T
 
 
 class HeadDecayBackward(_HeadDecayBase):
@@ -840,27 +866,24 @@ class HeadDecayBackward(_HeadDecayBase):
             self.grads = {"q": self._rows(self.Hq, dk, token_major), "k": self._rows(self.Hq, dk, token_major),
                           "v": self._rows(H, dv, token_major), "decay": f(H) if per_head else f(B, H, T),
                           "S0": f(B, H, dk, dv)}
+        self._fn, self._slots = library().dplr_hd_backward, _Slots(8)
 
     def __call__(self, dO, dST, q, k, v, decay, S0=None, decay_grad: bool = True,
                  stream: Optional[torch.cuda.Stream] = None) -> dict:
         """Gradients of HeadDecay's inputs (a dict, also kept in .grads) given dO [B,H,T,dv] in the inputs' type and
         dST (fp32 or None: zero). Without `decay_grad` the gradient of the gates is not computed (and not returned)."""
-        B, H, Hq, T, dev, dt = self.B, self.H, self.Hq, self.T, self.device, self.in_dtype
-        _need_view(dO, "dO", dev, dt, (B, H, T, self.dv))
-        _need_view(q, "q", dev, dt, (B, Hq, T, self.dk))
-        _need_view(k, "k", dev, dt, (B, Hq, T, self.dk))
-        _need_view(v, "v", dev, dt, (B, H, T, self.dv))
-        g = self._gates(decay, (B, H, T), _hd)
-        for name, t in (("S0", S0), ("dST", dST)):
-            if t is not None:
-                _need(t, name, dev, torch.float32, (B, H, self.dk, self.dv))
+        B, H, T = self.B, self.H, self.T
+        qk, vo, state = (B, self.Hq, T, self.dk), (B, H, T, self.dv), (B, H, self.dk, self.dv)
+        at = [self._at(q, "q", qk), self._at(k, "k", qk), self._at(v, "v", vo), self._gates(decay, (B, H, T)),
+              self._at(dO, "dO", vo)]
         G = self.grads
-        with torch.cuda.device(dev):
-            st = dplr_hd_backward(self.desc, _hd(q), _hd(k), _hd(v), g, _ptr(S0), _hd(dO), _ptr(dST), _hd(G["q"]),
-                                  _hd(G["k"]), _hd(G["v"]), _ptr(G["decay"]) if decay_grad else None, _ptr(G["S0"]),
-                                  _ptr(self.workspace), self.ws_bytes, self._stream(stream))
-        if st != DPLR_OK:
-            raise DplrError(st, "dplr_hd_backward")
+        at += [(G[n].data_ptr(), G[n].stride()) for n in ("q", "k", "v")]
+        f = self._slots
+        f(*[x for p, st in at for x in (p, st[0], st[1], st[2])])
+        r = f.refs
+        self._call(self._fn, "dplr_hd_backward", stream, r[0], r[1], r[2], r[3], self._state(S0, "S0", state), r[4],
+                   self._state(dST, "dST", state), r[5], r[6], r[7], G["decay"].data_ptr() if decay_grad else None,
+                   G["S0"].data_ptr(), self.workspace.data_ptr(), self.ws_bytes)
         return G if decay_grad else {n: t for n, t in G.items() if n != "decay"}
 
 
@@ -882,21 +905,25 @@ class RequestPlan:
         self.blocks = f(self.capacity // self.block + self.R, 4)
         self.token_slot, self.token_pos = f(self.capacity), f(self.capacity)
         self.status = f(1)
-
-    @property
-    def tables(self) -> dict:
-        return {"starts": self.starts, "blocks": self.blocks, "block_starts": self.block_starts,
-                "token_slot": self.token_slot, "token_pos": self.token_pos}
+        self.tables = {"starts": self.starts, "blocks": self.blocks, "block_starts": self.block_starts,
+                       "token_slot": self.token_slot, "token_pos": self.token_pos}
+        self._fn = library().dplr_hd_plan
 
     def __call__(self, lengths, slots, context, stream: Optional[torch.cuda.Stream] = None) -> dict:
         """lengths, slots, context: int32 [R] on the device. Returns the tables (see device_status for refused input)."""
-        for name, t in (("lengths", lengths), ("slots", slots), ("context", context)):
-            _need(t, name, self.device, torch.int32, (self.R,))
-        with torch.cuda.device(self.device):
-            s = stream if stream is not None else torch.cuda.current_stream(self.device)
-            st = dplr_hd_plan(self.R, self.capacity, self.block, self.n_slots, _ptr(lengths), _ptr(slots),
-                              _ptr(context), _ptr(self.starts), _ptr(self.blocks), _ptr(self.block_starts),
-                              _ptr(self.token_slot), _ptr(self.token_pos), _ptr(self.status), s.cuda_stream)
+        dev, i = self.device, self.device.index
+        for t, name in ((lengths, "lengths"), (slots, "slots"), (context, "context")):
+            if t is None or t.dtype is not torch.int32 or t.shape != (self.R,) or t.device != dev or not t.is_contiguous():
+                _need(t, name, dev, torch.int32, (self.R,))
+        s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(i)
+        args = (self.R, self.capacity, self.block, self.n_slots, lengths.data_ptr(), slots.data_ptr(), context.data_ptr(),
+                self.starts.data_ptr(), self.blocks.data_ptr(), self.block_starts.data_ptr(), self.token_slot.data_ptr(),
+                self.token_pos.data_ptr(), self.status.data_ptr(), s)
+        if torch.cuda.current_device() == i:
+            st = self._fn(*args)
+        else:
+            with torch.cuda.device(i):
+                st = self._fn(*args)
         if st != DPLR_OK:
             raise DplrError(st, "dplr_hd_plan")
         self.slots, self.context = slots, context     # the packed forward reads them
@@ -924,25 +951,25 @@ class HeadDecayPacked(_HeadDecayBase):
         with torch.cuda.device(self.device):
             self._workspace(dplr_hd_packed_workspace_size(self.desc, plan.R, plan.block), "dplr_hd_packed_workspace_size")
             self.o = torch.zeros((capacity, H, dv), dtype=self.in_dtype, device=self.device)
+        self._fn, self._slots = library().dplr_hd_forward_packed, _Slots(5)
 
     def __call__(self, q, k, v, decay, S, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
         """q, k [capacity,Hq,dk], v [capacity,H,dv], decay [capacity,H] fp32 or [H]; S [slots,H,dk,dv] fp32 is updated."""
-        p, n, dev, dt = self.plan, self.T, self.device, self.in_dtype
+        p, n, H = self.plan, self.T, self.H
         if not hasattr(p, "slots"):
             raise ValueError("call the plan first: it makes the tables")
-        _need_view(q, "q", dev, dt, (n, self.Hq, self.dk))
-        _need_view(k, "k", dev, dt, (n, self.Hq, self.dk))
-        _need_view(v, "v", dev, dt, (n, self.H, self.dv))
-        g = self._gates(decay, (n, self.H), _hd_rows)
-        _need(S, "S", dev, torch.float32, (self.n_slots, self.H, self.dk, self.dv))
-        with torch.cuda.device(dev):
-            st = dplr_hd_forward_packed(self.desc, p.R, p.block, self.n_slots, _ptr(p.blocks), _ptr(p.block_starts),
-                                        _ptr(p.slots), _ptr(p.context), _hd_rows(q), _hd_rows(k), _hd_rows(v), g,
-                                        _ptr(S), _hd_rows(self.o), _ptr(self.workspace), self.ws_bytes,
-                                        self._stream(stream))
-        if st != DPLR_OK:
-            raise DplrError(st, "dplr_hd_forward_packed")
-        return self.o
+        qk, o = (n, self.Hq, self.dk), self.o
+        at = [self._at(q, "q", qk), self._at(k, "k", qk), self._at(v, "v", (n, H, self.dv)),
+              self._gates(decay, (n, H)), (o.data_ptr(), o.stride())]
+        if S is None:
+            raise ValueError("S is required")
+        f = self._slots
+        f(*[x for ptr, st in at for x in (ptr, 0, st[1], st[0])])
+        r = f.refs
+        self._call(self._fn, "dplr_hd_forward_packed", stream, p.R, p.block, self.n_slots, p.blocks.data_ptr(),
+                   p.block_starts.data_ptr(), p.slots.data_ptr(), p.context.data_ptr(), r[0], r[1], r[2], r[3],
+                   self._state(S, "S", (self.n_slots, H, self.dk, self.dv)), r[4], self.workspace.data_ptr(), self.ws_bytes)
+        return o
 
 
 def default_block(desc: dplr_hd_desc, requests: int) -> int:
@@ -960,6 +987,7 @@ class HeadDecayDecode(_HeadDecayBase):
         self.n_slots = int(slots)
         self.o = torch.zeros((rows, H, dv), dtype=self.in_dtype, device=self.device)
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._fn, self._slots = library().dplr_hd_decode_step, _Slots(5)
 
     def device_status(self, clear: bool = False) -> int:
         """DPLR_ERR_INVALID_ARG if a row's slot was out of range or an earlier row's since the word was cleared."""
@@ -971,16 +999,20 @@ class HeadDecayDecode(_HeadDecayBase):
     def __call__(self, q, k, v, decay, S, slots, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
         """q, k [rows,Hq,dk], v [rows,H,dv], decay [rows,H] fp32 or [H]; S [slots,H,dk,dv] fp32 is updated in place;
         slots [rows] int32: each row's state, -1 for a row without one."""
-        n, dev, dt = self.B, self.device, self.in_dtype
-        _need_view(q, "q", dev, dt, (n, self.Hq, self.dk))
-        _need_view(k, "k", dev, dt, (n, self.Hq, self.dk))
-        _need_view(v, "v", dev, dt, (n, self.H, self.dv))
-        g = self._gates(decay, (n, self.H), _hd_step)
-        _need(S, "S", dev, torch.float32, (self.n_slots, self.H, self.dk, self.dv))
-        _need(slots, "slots", dev, torch.int32, (n,))
-        with torch.cuda.device(dev):
-            st = dplr_hd_decode_step(self.desc, self.n_slots, _ptr(slots), _hd_step(q), _hd_step(k), _hd_step(v), g,
-                                     _ptr(S), _hd_step(self.o), _ptr(self.status), self._stream(stream))
-        if st != DPLR_OK:
-            raise DplrError(st, "dplr_hd_decode_step")
-        return self.o
+        n, H = self.B, self.H
+        qk, o = (n, self.Hq, self.dk), self.o
+        (pq, sq), (pk, sk) = self._at(q, "q", qk), self._at(k, "k", qk)
+        pv, sv = self._at(v, "v", (n, H, self.dv))
+        pg, sg = self._gates(decay, (n, H))
+        if S is None:
+            raise ValueError("S is required")
+        if slots is None or slots.dtype is not torch.int32 or slots.shape != (n,) or slots.device != self.device or \
+                not slots.is_contiguous():
+            _need(slots, "slots", self.device, torch.int32, (n,))
+        f = self._slots
+        f(pq, sq[0], sq[1], 0, pk, sk[0], sk[1], 0, pv, sv[0], sv[1], 0, pg, sg[0], sg[1], 0, o.data_ptr(), H * self.dv,
+          self.dv, 0)
+        r = f.refs
+        self._call(self._fn, "dplr_hd_decode_step", stream, self.n_slots, slots.data_ptr(), r[0], r[1], r[2], r[3],
+                   self._state(S, "S", (self.n_slots, H, self.dk, self.dv)), r[4], self.status.data_ptr())
+        return o
