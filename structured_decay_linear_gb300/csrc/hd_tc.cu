@@ -51,7 +51,6 @@ using namespace tc;
 
 constexpr int C = kChunk;                  // 128
 constexpr int kGrp = 128;
-constexpr int kAhead = 3;                  // chunks between a row's way into L2 and into shared memory
 constexpr int kGrpB = 2 * kGrp;            // group B has eight warps
 constexpr int NT = 5 * kGrp + 96;          // groups A, B, C, O; warps 20 (copies), 21 (MMA issue), 22 (gates)
 constexpr uint32_t kHalf = C * 128;        // bytes of a half tile: 128 rows of 64 bf16
@@ -61,6 +60,7 @@ constexpr double kLog2e = 1.4426950408889634;
 struct alignas(128) Args {
     CUtensorMap map[3][4];    // [pass][x, y, z, o]
     Launch l;
+    long long total;          // units of work: segments times passes
 };
 
 // Per-chunk gate values, double-buffered; A_i: cumulative gates at the start of block i of 32 tokens (log2 units).
@@ -197,20 +197,61 @@ __device__ __forceinline__ void clear_rows(uint32_t tz, int n, int tid, int nt) 
     }
 }
 
+// Row `row` of the state in tensor memory (this thread's lane) to an array of [DX][DZ] states.
+template <int DX, int DZ>
+__device__ __forceinline__ void store_state(float* state, const Pass& p, int row, uint32_t taddr) {
+    float* dst = state + row * p.six;
+#pragma unroll 1
+    for (int c = 0; c < DZ; c += 32) {
+        float v[32];
+        tmem_ld32(taddr + c, v);
+        if (p.siz == 1) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<float4*>(dst + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) dst[(c + i) * p.siz] = v[i];
+        }
+    }
+}
+
+// One unit of work: a segment in a pass. Every role of a CTA walks the same units, u = blockIdx.x, + gridDim.x, ..; its
+// chunks are numbered through, so that copies, gates and products of a unit run into those of the one before.
+struct Work {
+    const Pass* p;
+    const CUtensorMap* maps;
+    Segment sg;
+    bool rev, down;
+    int nchunk;
+    __device__ __forceinline__ int chunk(int j) const { return down ? nchunk - 1 - j : j; }
+    __device__ __forceinline__ int rows(int j) const { return min(C, sg.n - chunk(j) * C); }
+};
+
+// False: nothing to do.
+template <bool STATES>
+__device__ __forceinline__ bool find_work(const Args& a, long long u, Work& w) {
+    const int pi = (int)(u % a.l.npass);      // the passes of a segment side by side: they read the same rows
+    w.p = &a.l.pass[pi];
+    w.maps = a.map[pi];
+    if (!locate(a.l.geo, u / a.l.npass, w.sg)) return false;
+    w.rev = w.p->reverse;
+    if (w.p->states_only == 1 && (w.rev ? w.sg.first : w.sg.last)) return false;
+    w.nchunk = (w.sg.n + C - 1) / C;
+    // chunk of step j: in the pass's direction; a states pass comes from the far end
+    w.down = STATES ? !w.rev : w.rev;
+    return w.nchunk > 0;
+}
+
 template <int DX, int DZ, bool SPLIT, bool STATES>
 __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Args a) {
     using Ly = Layout<DX, DZ, SPLIT, STATES>;
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t sb = smem_addr(smem);
-    const Pass& p = a.l.pass[blockIdx.y];
-    const CUtensorMap* maps = a.map[blockIdx.y];
     if (sb & 1023u) {   // the swizzled tiles need 1024-byte alignment
         if (threadIdx.x == 0) atomicExch(a.l.status, (int)DPLR_ERR_CUDA);
         return;
     }
-    Segment sg;
-    if (!locate(a.l.geo, blockIdx.x, sg)) return;
-    if (p.states_only == 1 && (p.reverse ? sg.first : sg.last)) return;
 
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Ly::BARS);
     uint64_t* full_x = bars + 0;
@@ -236,12 +277,6 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int grp = warp >> 2, gt = tid & (kGrp - 1);
-    const bool rev = p.reverse;
-    const int nchunk = (sg.n + C - 1) / C;
-    // chunk of step j: in the pass's direction; a states pass comes from the far end
-    const bool down = STATES ? !rev : rev;
-    auto chunk = [&](int j) { return down ? nchunk - 1 - j : j; };
-    auto rows_of = [&](int j) { return min(C, sg.n - chunk(j) * C); };
     const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const long long wl = a.l.wait_cycles;
 
@@ -265,59 +300,60 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
         return !bad;
     };
 
+    // units of this CTA; `it` numbers its chunks through
+#define HD_UNITS(w)                                                                        \
+    for (long long u_ = blockIdx.x; u_ < a.total && !failed; u_ += gridDim.x)              \
+        if (Work w; find_work<STATES>(a, u_, w))
+
     if (warp == 20) {
         // =================== copies ===================
         if (lane == 0) {
-            const int hx = sg.h / p.x.div, hy = sg.h / p.y.div, hz = sg.h / p.z.div;
-            int nx = 0, ny = 0, nz = 0;    // copies started
-            auto load = [&](uint32_t dst, int which, int D, int h, int j, uint64_t* bar) {
-                mbar_expect_tx(bar, D * 256);
-                for (int x = 0; x < D / 64; ++x)
-                    tma_load_4d(dst + x * kHalf, &maps[which], 64 * x, sg.t0 + chunk(j) * C, h, sg.b, bar);
-            };
-            // Shared memory has room for one x and one y tile only, and a load under load takes 3 K cycles or more: the
-            // rows are brought into L2 kAhead chunks before they are wanted.
-            auto prefetch = [&](int j) {
-                if (j >= nchunk) return;
-                const int t = sg.t0 + chunk(j) * C;
-                for (int x = 0; x < DX / 64; ++x) {
-                    tma_prefetch_4d(&maps[1], 64 * x, t, hy, sg.b);
-                    if (!STATES) tma_prefetch_4d(&maps[0], 64 * x, t, hx, sg.b);
-                }
-                for (int x = 0; x < DZ / 64; ++x) tma_prefetch_4d(&maps[2], 64 * x, t, hz, sg.b);
-            };
-            for (int j = 1; j < kAhead; ++j) prefetch(j);
-            for (int j = 0; j < nchunk; ++j) {
-                if (j > 0 || kAhead == 1) prefetch(j + kAhead - 1);
-                if (STATES) {
-                    const int s = j & 1;
-                    if (j >= 2 && !mbar_wait(&free_z[s], ((j - 2) >> 1) & 1, wl)) { failed = true; break; }
-                    load(sb + Ly::T_Y + s * Ly::XB, 1, DX, hy, j, &full_y[s]);
-                    ++ny;
-                    load(sb + Ly::T_Z + s * Ly::ZB, 2, DZ, hz, j, &full_z[s]);
-                    ++nz;
-                } else {
-                    // y once the D before is formed and its tile in B's registers, x once its Oi is, z once the Op of its
-                    // buffer is
-                    if (j >= 1 && (!mbar_wait(d_done, (j - 1) & 1, wl) || !mbar_wait(y_read, (j - 1) & 1, wl))) { failed = true; break; }
-                    load(sb + Ly::T_Y, 1, DX, hy, j, full_y);
-                    ++ny;
-                    if (j >= 1 && !mbar_wait(oi_done, (j - 1) & 1, wl)) { failed = true; break; }
-                    load(sb + Ly::T_X, 0, DX, hx, j, full_x);
-                    ++nx;
-                    const int s = j % Ly::NZ;
-                    if (j >= Ly::NZ && !mbar_wait(&free_z[s], ((j - Ly::NZ) / Ly::NZ) & 1, wl)) { failed = true; break; }
-                    load(sb + Ly::T_Z + s * Ly::ZB, 2, DZ, hz, j, &full_z[s]);
-                    ++nz;
+            uint32_t it = 0, nx = 0, ny = 0, nz = 0;    // chunks; copies started
+            HD_UNITS(w) {
+                const Pass& p = *w.p;
+                const Segment& sg = w.sg;
+                const int hx = sg.h / p.x.div, hy = sg.h / p.y.div, hz = sg.h / p.z.div;
+                for (int j = 0; j < w.nchunk; ++j, ++it) {
+                    const int t = sg.t0 + w.chunk(j) * C;
+                    // Shared memory has room for one x and one y tile: the rows start on their way into L2 while the
+                    // buffers are still in use.
+                    for (int x = 0; x < DX / 64; ++x) {
+                        tma_prefetch_4d(&w.maps[1], 64 * x, t, hy, sg.b);
+                        if (!STATES) tma_prefetch_4d(&w.maps[0], 64 * x, t, hx, sg.b);
+                    }
+                    for (int x = 0; x < DZ / 64; ++x) tma_prefetch_4d(&w.maps[2], 64 * x, t, hz, sg.b);
+                    auto load = [&](uint32_t dst, int which, int D, int h, uint64_t* bar) {
+                        mbar_expect_tx(bar, D * 256);
+                        for (int x = 0; x < D / 64; ++x) tma_load_4d(dst + x * kHalf, &w.maps[which], 64 * x, t, h, sg.b, bar);
+                    };
+                    const int s = it % Ly::NZ;
+                    if (STATES) {
+                        if (it >= 2 && !mbar_wait(&free_z[s], ((it - 2) >> 1) & 1, wl)) { failed = true; break; }
+                        load(sb + Ly::T_Y + s * Ly::XB, 1, DX, hy, &full_y[s]);
+                        load(sb + Ly::T_Z + s * Ly::ZB, 2, DZ, hz, &full_z[s]);
+                    } else {
+                        // y once the D before is formed and its tile in B's registers, x once its Oi is, z once the Op
+                        // of its buffer is
+                        if (it >= 1 && (!mbar_wait(d_done, (it - 1) & 1, wl) || !mbar_wait(y_read, (it - 1) & 1, wl))) { failed = true; break; }
+                        load(sb + Ly::T_Y, 1, DX, hy, full_y);
+                        ++ny;
+                        if (it >= 1 && !mbar_wait(oi_done, (it - 1) & 1, wl)) { failed = true; break; }
+                        load(sb + Ly::T_X, 0, DX, hx, full_x);
+                        ++nx;
+                        if (it >= Ly::NZ && !mbar_wait(&free_z[s], ((it - Ly::NZ) / Ly::NZ) & 1, wl)) { failed = true; break; }
+                        load(sb + Ly::T_Z + s * Ly::ZB, 2, DZ, hz, &full_z[s]);
+                        ++nz;
+                    }
+                    if (STATES) { ++ny; ++nz; }
                 }
             }
             if (failed) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
             // no copy may land after the CTA has gone (another role may have given up): wait for the last into each buffer
             const long long most = 400000000LL;
             if (nx > 0) mbar_wait(full_x, (nx - 1) & 1, most);
-            for (int s = 0; s < Ly::NY; ++s)
+            for (uint32_t s = 0; s < Ly::NY; ++s)
                 if (ny > s) mbar_wait(&full_y[s], ((ny - 1 - s) / Ly::NY) & 1, most);
-            for (int s = 0; s < Ly::NZ; ++s)
+            for (uint32_t s = 0; s < Ly::NZ; ++s)
                 if (nz > s) mbar_wait(&full_z[s], ((nz - 1 - s) / Ly::NZ) & 1, most);
         }
         __syncwarp();
@@ -364,31 +400,34 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                         mma_bf16_tmem_a(tmem + TM_OP, tmem + TM_D + 32 * (ks >> 1) + 8 * (ks & 1) + 16 * s,
                                         dadd(dz, 2048 * ks), idO, (s > 0 || ks > 0) ? 1u : 0u);
             };
-            for (int j = 0; j < nchunk; ++j) {
-                const int s = STATES ? (j & 1) : j % Ly::NZ;
-                const uint32_t tz = sb + Ly::T_Z + s * Ly::ZB, zpar = STATES ? (j >> 1) & 1 : (j / Ly::NZ) & 1;
-                if (STATES) {
-                    if (!wait1(y_ready, j & 1) || !wait1(&full_z[s], zpar)) { failed = true; break; }
-                    mma_R(tz, 0, j > 0);
+            uint32_t it = 0;
+            HD_UNITS(w) {
+                for (int j = 0; j < w.nchunk; ++j, ++it) {
+                    const uint32_t par = it & 1, s = it % Ly::NZ, zpar = (it / Ly::NZ) & 1;
+                    const uint32_t tz = sb + Ly::T_Z + s * Ly::ZB;
+                    if (STATES) {
+                        if (!wait1(y_ready, par) || !wait1(&full_z[s], zpar)) { failed = true; break; }
+                        mma_R(tz, 0, j > 0);
+                        mma_R(tz, 1, true);
+                        mma_commit(&free_z[s]);
+                        mma_commit(r_done);
+                        continue;
+                    }
+                    if (!wait1(full_x, par) || !wait1(full_y, par)) { failed = true; break; }
+                    mma_D();
+                    if (!wait1(r_ready, par) || (it > 0 && !wait1(o_free, par ^ 1))) { failed = true; break; }
+                    mma_Oi();
+                    if (!wait1(y_ready, par) || !wait1(&full_z[s], zpar)) { failed = true; break; }
+                    mma_R(tz, 0, true);
+                    mma_commit(r_half);
+                    if (!wait1(y_rest, par)) { failed = true; break; }
                     mma_R(tz, 1, true);
-                    mma_commit(&free_z[s]);
                     mma_commit(r_done);
-                    continue;
+                    if (!wait1(p_ready, par)) { failed = true; break; }
+                    mma_Op(tz);
+                    mma_commit(&free_z[s]);
+                    mma_commit(op_done);
                 }
-                if (!wait1(full_x, j & 1) || !wait1(full_y, j & 1)) { failed = true; break; }
-                mma_D();
-                if (!wait1(r_ready, j & 1) || (j > 0 && !wait1(o_free, (j - 1) & 1))) { failed = true; break; }
-                mma_Oi();
-                if (!wait1(y_ready, j & 1) || !wait1(&full_z[s], zpar)) { failed = true; break; }
-                mma_R(tz, 0, true);
-                mma_commit(r_half);
-                if (!wait1(y_rest, j & 1)) { failed = true; break; }
-                mma_R(tz, 1, true);
-                mma_commit(r_done);
-                if (!wait1(p_ready, j & 1)) { failed = true; break; }
-                mma_Op(tz);
-                mma_commit(&free_z[s]);
-                mma_commit(op_done);
             }
             if (failed) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
             mma_commit(drain);       // every MMA this thread issued: none may run on freed tensor memory
@@ -399,20 +438,24 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
         // =================== gates: lane holds tokens 4 lane .. 4 lane + 3 ===================
         // Sums in fixed point (log2 units, 32 fractional bits, 64 in all): exact, and unlike 64-bit floating point (with
         // which this warp took 6.6 K cycles a chunk and held up all others) a few integer instructions each.
-        const float* gp = p.g + sg.b * p.gb + sg.h * p.gh;
+        auto real = [](long long x) { return (float)x * 2.3283064365386963e-10f; };     // 2^-32
+        uint32_t it = 0;
+        HD_UNITS(w) {
+        const Pass& p = *w.p;
+        const bool rev = w.rev;
+        const float* gp = p.g + w.sg.b * p.gb + w.sg.h * p.gh;
         auto raw = [&](int j, float (&r)[4]) {
-            const int n = rows_of(j);
-            const long long t0 = (long long)sg.t0 + chunk(j) * C;
+            const int n = w.rows(j);
+            const long long t0 = (long long)w.sg.t0 + w.chunk(j) * C;
 #pragma unroll
             for (int i = 0; i < 4; ++i) r[i] = 4 * lane + i < n ? gp[(t0 + 4 * lane + i) * p.gt] : 0.f;
         };
-        auto real = [](long long x) { return (float)x * 2.3283064365386963e-10f; };     // 2^-32
         float cur[4], nxt[4];
-        if (nchunk > 0) raw(0, cur);
+        raw(0, cur);
         long long passed = 0;    // gates of the chunks before
         float lost = 0.f;        // NaN once a gate was: it then reaches everything behind
-        for (int j = 0; j < nchunk; ++j) {
-            if (j + 1 < nchunk) raw(j + 1, nxt);
+        for (int j = 0; j < w.nchunk; ++j, ++it) {
+            if (j + 1 < w.nchunk) raw(j + 1, nxt);
             long long x[4];
             bool nan = false;
 #pragma unroll
@@ -436,9 +479,9 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
             const int bi = (lane >> 2) & 3, bj = lane & 3;
             const long long si = __shfl_sync(0xffffffffu, before, 8 * bi), sj = __shfl_sync(0xffffffffu, before, 8 * bj);
             const long long ei = __shfl_sync(0xffffffffu, s, 8 * bi + 7), ej = __shfl_sync(0xffffffffu, s, 8 * bj + 7);
-            const int b = j & 1;
+            const int b = it & 1;
             bool ok = true;
-            if (j >= 2) ok = mbar_wait(&g_free[b], ((j - 2) >> 1) & 1, wl);
+            if (it >= 2) ok = mbar_wait(&g_free[b], ((it - 2) >> 1) & 1, wl);
             if (!__all_sync(0xffffffffu, ok)) { failed = true; break; }
             GateBuf& g = gates[b];
             const long long far = STATES ? passed : 0;
@@ -463,52 +506,51 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
 #pragma unroll
             for (int i = 0; i < 4; ++i) cur[i] = nxt[i];
         }
+        if (STATES && p.gsum && lane == 0 && !failed) p.gsum[w.sg.entry] = real(passed) * 0.6931471805599453f + lost;
+        }
         if (failed && lane == 0) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
-        if (STATES && p.gsum && lane == 0) p.gsum[sg.entry] = real(passed) * 0.6931471805599453f + lost;
     } else if (STATES) {
         // =================== all groups: Y~; then the state ===================
         constexpr uint32_t N = 5 * kGrp;
-        for (int j = 0; j < nchunk; ++j) {
-            const int s = j & 1, n = rows_of(j);
-            if (!group_wait(&g_full[s], (j >> 1) & 1, 1, N, warp == 0) || !group_wait(&full_y[s], (j >> 1) & 1, 1, N, warp == 0) ||
-                (j > 0 && !group_wait(r_done, (j - 1) & 1, 1, N, warp == 0)) ||
-                (n < C && !group_wait(&full_z[s], (j >> 1) & 1, 1, N, warp == 0))) { failed = true; break; }
-            scale_rows<DX>(sb + Ly::T_Y + s * Ly::XB, sb + Ly::T_YH, sb + Ly::T_YL, gates[s], n, tid, N);
-            if (n < C) clear_rows<DZ>(sb + Ly::T_Z + s * Ly::ZB, n, tid, N);
-            fence_async_smem();
-            named_sync(1, N);
-            if (tid == 0) { mbar_arrive(y_ready); mbar_arrive(&g_free[s]); }
-        }
-        if (!failed && nchunk > 0 && !group_wait(r_done, (nchunk - 1) & 1, 1, N, warp == 0)) failed = true;
-        if (!failed && grp == 0 && gt < (DX == 64 && warp >= 2 ? 0 : kGrp)) {
-            float* dst = p.bound + (rev ? sg.entry : sg.entry + sg.step) * (long long)(DX * DZ) + gt * p.six;
-#pragma unroll 1
-            for (int c = 0; c < DZ; c += 32) {
-                float v[32];
-                tmem_ld32(tmem + TM_R + lane_off + c, v);
-                if (p.siz == 1) {
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-                        *reinterpret_cast<float4*>(dst + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) dst[(c + i) * p.siz] = v[i];
-                }
+        uint32_t it = 0;
+        HD_UNITS(w) {
+            const Pass& p = *w.p;
+            const Segment& sg = w.sg;
+            for (int j = 0; j < w.nchunk; ++j, ++it) {
+                const uint32_t s = it & 1, par = (it >> 1) & 1;
+                const int n = w.rows(j);
+                if (!group_wait(&g_full[s], par, 1, N, warp == 0) || !group_wait(&full_y[s], par, 1, N, warp == 0) ||
+                    (it > 0 && !group_wait(r_done, s ^ 1, 1, N, warp == 0)) ||
+                    (n < C && !group_wait(&full_z[s], par, 1, N, warp == 0))) { failed = true; break; }
+                scale_rows<DX>(sb + Ly::T_Y + s * Ly::XB, sb + Ly::T_YH, sb + Ly::T_YL, gates[s], n, tid, N);
+                if (n < C) clear_rows<DZ>(sb + Ly::T_Z + s * Ly::ZB, n, tid, N);
+                fence_async_smem();
+                fence_before_sync();      // (the state of the unit before has been read)
+                named_sync(1, N);
+                if (tid == 0) { mbar_arrive(y_ready); mbar_arrive(&g_free[s]); }
             }
+            if (failed || !group_wait(r_done, (it & 1) ^ 1, 1, N, warp == 0)) { failed = true; break; }
+            if (grp == 0 && (DX == 128 || warp < 2))
+                store_state<DX, DZ>(p.bound + (w.rev ? sg.entry : sg.entry + sg.step) * (long long)(DX * DZ), p, gt,
+                                    tmem + TM_R + lane_off);
         }
         if (failed && tid == 0) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
     } else if (grp == 0) {
         // =================== A: the state (thread = row of R; with DX = 64 two warps only keep step) ===================
         const bool mine = DX == 128 || warp < 2;
-        const float* src = nullptr;
-        if (p.bound && !sg.alone) src = p.bound + (rev ? sg.entry + sg.step : sg.entry) * (long long)(DX * DZ);
-        else if (p.ext_in && !sg.fresh) src = p.ext_in + sg.ext * (long long)(DX * DZ);
         const uint32_t tr = sb + Ly::T_R;
-        for (int j = 0; j < nchunk; ++j) {
-            const int b = j & 1;
-            if (!group_wait(&g_full[b], (j >> 1) & 1, 1, kGrp, warp == 0) ||
-                (j > 0 && (!group_wait(oi_done, (j - 1) & 1, 1, kGrp, warp == 0) ||
-                           !group_wait(r_done, (j - 1) & 1, 1, kGrp, warp == 0)))) { failed = true; break; }
+        uint32_t it = 0;
+        HD_UNITS(w) {
+        const Pass& p = *w.p;
+        const Segment& sg = w.sg;
+        const float* src = nullptr;
+        if (p.bound && !sg.alone) src = p.bound + (w.rev ? sg.entry + sg.step : sg.entry) * (long long)(DX * DZ);
+        else if (p.ext_in && !sg.fresh) src = p.ext_in + sg.ext * (long long)(DX * DZ);
+        for (int j = 0; j < w.nchunk; ++j, ++it) {
+            const uint32_t b = it & 1;
+            if (!group_wait(&g_full[b], (it >> 1) & 1, 1, kGrp, warp == 0) ||
+                (it > 0 && (!group_wait(oi_done, b ^ 1, 1, kGrp, warp == 0) ||
+                            !group_wait(r_done, b ^ 1, 1, kGrp, warp == 0)))) { failed = true; break; }
             const float en = gates[b].en;
             if (mine) {
 #pragma unroll 1
@@ -558,22 +600,10 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
             named_sync(1, kGrp);
             if (gt == 0) { mbar_arrive(r_ready); mbar_arrive(&g_free[b]); }
         }
-        if (!failed && nchunk > 0 && !group_wait(r_done, (nchunk - 1) & 1, 1, kGrp, warp == 0)) failed = true;
-        if (!failed && mine && p.ext_out && (rev ? sg.first : sg.last)) {
-            float* dst = p.ext_out + sg.ext * (long long)(DX * DZ) + gt * p.six;
-#pragma unroll 1
-            for (int c = 0; c < DZ; c += 32) {
-                float v[32];
-                tmem_ld32(tmem + TM_R + lane_off + c, v);
-                if (p.siz == 1) {
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-                        *reinterpret_cast<float4*>(dst + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) dst[(c + i) * p.siz] = v[i];
-                }
-            }
+        // the state it ends with
+        if (failed || !group_wait(r_done, (it & 1) ^ 1, 1, kGrp, warp == 0)) { failed = true; break; }
+        if (mine && p.ext_out && (w.rev ? sg.first : sg.last))
+            store_state<DX, DZ>(p.ext_out + sg.ext * (long long)(DX * DZ), p, gt, tmem + TM_R + lane_off);
         }
         if (failed && gt == 0) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
     } else if (grp <= 2) {
@@ -583,10 +613,13 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
         constexpr int PER = DX / 8, IT = C * PER / kGrpB;    // 16-byte pieces of a row, pieces of a thread
         const int bt = tid - kGrp, t0 = bt / PER, c = bt % PER;   // piece i: token t0 + i (kGrpB / PER), always column c
         const uint32_t col = (uint32_t)(c >> 3) * kHalf;
-        for (int j = 0; j < nchunk; ++j) {
-            const int b = j & 1, n = rows_of(j), s = j % Ly::NZ;
-            const bool poll = warp == 4;
-            if (!group_wait(full_y, j & 1, 2, kGrpB, poll)) { failed = true; break; }
+        const bool poll = warp == 4;
+        uint32_t it = 0;
+        HD_UNITS(w)
+        for (int j = 0; j < w.nchunk; ++j, ++it) {
+            const uint32_t b = it & 1, s = it % Ly::NZ;
+            const int n = w.rows(j);
+            if (!group_wait(full_y, b, 2, kGrpB, poll)) { failed = true; break; }
             uint32_t u[IT][4];
 #pragma unroll
             for (int i = 0; i < IT; ++i) lds128(sb + Ly::T_Y + col + swz(t0 + i * (kGrpB / PER), c & 7), u[i]);
@@ -595,20 +628,20 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
             for (int i = 0; i < IT; ++i) asm volatile("" : "+r"(u[i][0]), "+r"(u[i][1]), "+r"(u[i][2]), "+r"(u[i][3]));
             named_sync(2, kGrpB);
             if (bt == 0) mbar_arrive(y_read);
-            if (!group_wait(&g_full[b], (j >> 1) & 1, 2, kGrpB, poll) || (j > 0 && !group_wait(r_half, (j - 1) & 1, 2, kGrpB, poll)) ||
-                (n < C && !group_wait(&full_z[s], (j / Ly::NZ) & 1, 2, kGrpB, poll))) { failed = true; break; }
+            if (!group_wait(&g_full[b], (it >> 1) & 1, 2, kGrpB, poll) || (it > 0 && !group_wait(r_half, b ^ 1, 2, kGrpB, poll)) ||
+                (n < C && !group_wait(&full_z[s], (it / Ly::NZ) & 1, 2, kGrpB, poll))) { failed = true; break; }
             const GateBuf& g = gates[b];
             // two halves of 64 tokens, so that the products of one run while the other is formed
             auto half = [&](auto check, int h) {
                 constexpr int TS = kGrpB / PER, HI = IT / 2;     // tokens between two pieces, pieces of a half
-                float w[HI];       // read ahead of the stores, which the compiler moves no load across
+                float wt[HI];      // read ahead of the stores, which the compiler moves no load across
 #pragma unroll
-                for (int i = 0; i < HI; ++i) w[i] = g.cf[t0 + (h * HI + i) * TS] * g.ce[(h * HI + i) * TS / 32];
+                for (int i = 0; i < HI; ++i) wt[i] = g.cf[t0 + (h * HI + i) * TS] * g.ce[(h * HI + i) * TS / 32];
 #pragma unroll
                 for (int i = 0; i < HI; ++i) {
                     const int t = t0 + (h * HI + i) * TS;
                     const uint32_t off = col + swz(t, c & 7);
-                    scale16<check.value>(u[h * HI + i], w[i], t >= n, sb + Ly::T_YH + off, sb + Ly::T_YL + off);
+                    scale16<check.value>(u[h * HI + i], wt[i], t >= n, sb + Ly::T_YH + off, sb + Ly::T_YL + off);
                 }
             };
             if (n == C) half(std::false_type{}, 0);
@@ -617,7 +650,7 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
             fence_async_smem();
             named_sync(2, kGrpB);
             if (bt == 0) mbar_arrive(y_ready);
-            if (j > 0 && !group_wait(r_done, (j - 1) & 1, 2, kGrpB, poll)) { failed = true; break; }
+            if (it > 0 && !group_wait(r_done, b ^ 1, 2, kGrpB, poll)) { failed = true; break; }
             if (n == C) half(std::false_type{}, 1);
             else half(std::true_type{}, 1);
             fence_async_smem();
@@ -627,27 +660,31 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
         if (failed && bt == 0) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
     } else if (grp == 3) {
         // =================== C: P (thread = row) ===================
-        const int w = warp & 3;
-        const bool poll = w == 0;
-        const float sgn = rev ? 1.f : -1.f;
-        for (int j = 0; j < nchunk; ++j) {
-            const int b = j & 1, n = rows_of(j);
-            if (!group_wait(&g_full[b], (j >> 1) & 1, 3, kGrp, poll) || !group_wait(d_done, j & 1, 3, kGrp, poll)) { failed = true; break; }
+        const int rw = warp & 3;       // row block
+        const bool poll = rw == 0;
+        uint32_t it = 0;
+        HD_UNITS(w)
+        for (int j = 0; j < w.nchunk; ++j, ++it) {
+            const bool rev = w.rev;
+            const float sgn = rev ? 1.f : -1.f;
+            const uint32_t b = it & 1;
+            const int n = w.rows(j);
+            if (!group_wait(&g_full[b], (it >> 1) & 1, 3, kGrp, poll) || !group_wait(d_done, b, 3, kGrp, poll)) { failed = true; break; }
             const GateBuf& g = gates[b];
-            const float rc = g.rc[gt], row = ex2(rev ? g.bl[w] - rc : rc);
+            const float rc = g.rc[gt], row = ex2(rev ? g.bl[rw] - rc : rc);
             // blocks of 32 columns, each packed in place: hi in its first 16 columns, lo in the others. The loops over
             // blocks stay loops: unrolled, the roles' straight-line code outran the instruction cache (no_instruction
             // was the largest stall, a chunk took 11.4 K cycles).
 #pragma unroll 1
             for (int q = 0; q < 4; ++q) {
                 uint32_t h[16], l[16];
-                if (rev ? q < w : q > w) {
+                if (rev ? q < rw : q > rw) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) h[i] = l[i] = 0u;
                 } else {
                     float v[32];
                     tmem_ld32(tmem + TM_D + lane_off + 32 * q, v);
-                    if (q == w) {
+                    if (q == rw) {
                         const float2 s2 = make_float2(sgn, sgn), b2 = make_float2(-sgn * rc, -sgn * rc);
                         const float4* col = reinterpret_cast<const float4*>(g.rc + 32 * q);
 #pragma unroll
@@ -659,7 +696,7 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                             v[i] = vx.x; v[i + 1] = vx.y; v[i + 2] = vy.x; v[i + 3] = vy.y;
                         }
                     } else {
-                        const float rf = row * g.f[w][q];
+                        const float rf = row * g.f[rw][q];
                         const float2 r2 = make_float2(rf, rf);
                         const float4* col = reinterpret_cast<const float4*>(g.cf + 32 * q);
 #pragma unroll
@@ -671,8 +708,8 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                         }
                     }
                     // columns that this row sees: up to its own token, or from it to the chunk's last
-                    if (q == w || (rev && n < C)) {
-                        uint32_t seen = q == w ? (rev ? ~0u << lane : ~0u >> (31 - lane)) : ~0u;
+                    if (q == rw || (rev && n < C)) {
+                        uint32_t seen = q == rw ? (rev ? ~0u << lane : ~0u >> (31 - lane)) : ~0u;
                         if (rev && 32 * q + 31 >= n) seen &= 32 * q >= n ? 0u : ~0u >> (32 - (n - 32 * q));
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
@@ -695,20 +732,25 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
         if (failed && gt == 0) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
     } else {
         // =================== O: the outputs (thread = row) ===================
-        const int w = warp & 3;
-        const bool poll = w == 0;
+        const int rw = warp & 3;
+        const bool poll = rw == 0;
         bool storing = false;      // (thread 0) a store may still read the tile
-        for (int j = 0; j < nchunk; ++j) {
-            const int b = j & 1, n = rows_of(j);
-            if (!group_wait(&g_full[b], (j >> 1) & 1, 4, kGrp, poll)) { failed = true; break; }
+        uint32_t it = 0;
+        HD_UNITS(w) {
+        const Pass& p = *w.p;
+        const Segment& sg = w.sg;
+        for (int j = 0; j < w.nchunk; ++j, ++it) {
+            const uint32_t b = it & 1;
+            const int n = w.rows(j);
+            if (!group_wait(&g_full[b], (it >> 1) & 1, 4, kGrp, poll)) { failed = true; break; }
             const float rc = gates[b].rc[gt];
-            const float cx = ex2(rev ? gates[b].bl[w] - rc : rc) * gates[b].re[w];
+            const float cx = ex2(w.rev ? gates[b].bl[rw] - rc : rc) * gates[b].re[rw];
             if (storing) bulk_wait_read();
-            if (!group_wait(oi_done, j & 1, 4, kGrp, poll)) { failed = true; break; }
+            if (!group_wait(oi_done, b, 4, kGrp, poll)) { failed = true; break; }
             if (gt == 0) mbar_arrive(&g_free[b]);     // every thread of the group has read its gates
-            if (!group_wait(op_done, j & 1, 4, kGrp, poll)) { failed = true; break; }
+            if (!group_wait(op_done, b, 4, kGrp, poll)) { failed = true; break; }
             const bool staged = Ly::STAGED && n == C && !p.o_f32;
-            const int t0 = sg.t0 + chunk(j) * C;
+            const int t0 = sg.t0 + w.chunk(j) * C;
             const bool live = gt < n;
             const long long at = sg.b * p.ob + sg.h * p.oh + (long long)(t0 + gt) * p.ot;
             float dot = 0.f;
@@ -764,11 +806,12 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                 if (staged) {
 #pragma unroll
                     for (int x = 0; x < DZ / 64; ++x)
-                        tma_store_4d(&maps[3], 64 * x, t0, sg.h, sg.b, sb + Ly::T_O + x * kHalf);
+                        tma_store_4d(&w.maps[3], 64 * x, t0, sg.h, sg.b, sb + Ly::T_O + x * kHalf);
                     bulk_commit();
                     storing = true;
                 }
             }
+        }
         }
         if (storing) bulk_wait_all();
         if (failed && gt == 0) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
@@ -776,6 +819,7 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
     fence_before_sync();
     __syncthreads();
     if (warp == 0) tmem_dealloc(tmem, kTmemCols);
+#undef HD_UNITS
 }
 
 // A row sequence as [batch][head][token][feature]: boxes of 64 features x 128 tokens of one head.
@@ -784,20 +828,21 @@ bool map_rows(CUtensorMap* m, const View& v, int D, long long T, int heads, int 
 }
 
 template <int DX, int DZ, bool SPLIT, bool STATES>
-cudaError_t run(const Args& a, long long n, cudaStream_t s) {
+cudaError_t run(const Args& a, cudaStream_t s) {
     static std::atomic<uint64_t> set{0};
     constexpr int bytes = Layout<DX, DZ, SPLIT, STATES>::TOTAL;
     auto f = hd_tc_kernel<DX, DZ, SPLIT, STATES>;
     const cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(f), bytes, set);
     if (e != cudaSuccess) return e;
-    f<<<dim3((unsigned)n, (unsigned)a.l.npass), NT, bytes, s>>>(a);
+    const long long sms = sm_count();
+    f<<<(unsigned)(a.total < sms ? a.total : sms), NT, bytes, s>>>(a);
     return cudaGetLastError();
 }
 
 template <int DX, int DZ>
-cudaError_t run_kind(const Args& a, bool split, bool states, long long n, cudaStream_t s) {
-    if (states) return run<DX, DZ, false, true>(a, n, s);
-    return split ? run<DX, DZ, true, false>(a, n, s) : run<DX, DZ, false, false>(a, n, s);
+cudaError_t run_kind(const Args& a, bool split, bool states, cudaStream_t s) {
+    if (states) return run<DX, DZ, false, true>(a, s);
+    return split ? run<DX, DZ, true, false>(a, s) : run<DX, DZ, false, false>(a, s);
 }
 
 }  // namespace
@@ -834,12 +879,13 @@ cudaError_t launch_tc(const Launch& l, cudaStream_t s) {
                 !map_rows(&a.map[k][3], View{p.o, p.ob, p.oh, p.ot, 1}, p.DZ, T, H, l.B))
                 return cudaErrorInvalidValue;
         }
+        a.total = n * a.l.npass;
         const bool split = q.dots != nullptr, states = q.states_only != 0;
         cudaError_t e;
-        if (q.DX == 128 && q.DZ == 128) e = run_kind<128, 128>(a, split, states, n, s);
-        else if (q.DX == 128) e = run_kind<128, 64>(a, split, states, n, s);
-        else if (q.DZ == 128) e = run_kind<64, 128>(a, split, states, n, s);
-        else e = run_kind<64, 64>(a, split, states, n, s);
+        if (q.DX == 128 && q.DZ == 128) e = run_kind<128, 128>(a, split, states, s);
+        else if (q.DX == 128) e = run_kind<128, 64>(a, split, states, s);
+        else if (q.DZ == 128) e = run_kind<64, 128>(a, split, states, s);
+        else e = run_kind<64, 64>(a, split, states, s);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
