@@ -56,10 +56,10 @@ __host__ __device__ inline long long units(const Geometry& g, int B, int max_blo
 }
 
 // False: nothing to do (a block behind the last).
-__device__ __forceinline__ bool locate(const Geometry& g, long long unit, Segment& s) {
+__device__ __forceinline__ bool locate(const Geometry& g, int unit, Segment& s) {
     if (g.blocks) {
-        const int blk = (int)(unit / g.H);
-        s.h = (int)(unit % g.H);
+        const int blk = unit / g.H;
+        s.h = unit % g.H;
         const int4 e = *reinterpret_cast<const int4*>(g.blocks + 4 * (long long)blk);
         if (e.x < 0) return false;
         const int nb = g.block_starts[e.x + 1] - g.block_starts[e.x];
@@ -73,15 +73,14 @@ __device__ __forceinline__ bool locate(const Geometry& g, long long unit, Segmen
         s.step = g.H;
         return true;
     }
-    const long long bh = unit / g.nseg;
-    const int seg = (int)(unit % g.nseg);
-    s.b = (int)(bh / g.H); s.h = (int)(bh % g.H);
+    const int bh = unit / g.nseg, seg = unit % g.nseg;
+    s.b = bh / g.H; s.h = bh % g.H;
     s.t0 = seg * g.L;
     s.n = min(g.L, g.T - s.t0);
     s.alone = g.nseg == 1; s.first = seg == 0; s.last = seg == g.nseg - 1;
     s.fresh = false;
     s.ext = bh;
-    s.entry = bh * (g.nseg + 1) + seg;
+    s.entry = (long long)bh * (g.nseg + 1) + seg;
     s.step = 1;
     return true;
 }

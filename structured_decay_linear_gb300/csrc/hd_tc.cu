@@ -60,7 +60,7 @@ constexpr double kLog2e = 1.4426950408889634;
 struct alignas(128) Args {
     CUtensorMap map[3][4];    // [pass][x, y, z, o]
     Launch l;
-    long long total;          // units of work: segments times passes
+    int total;                // units of work: segments times passes
 };
 
 // Per-chunk gate values, double-buffered; A_i: cumulative gates at the start of block i of 32 tokens (log2 units).
@@ -81,7 +81,7 @@ struct Layout {
     static constexpr int XB = DX * 256, ZB = DZ * 256;        // bytes of a tile: D / 64 half tiles
     static constexpr int NZ = STATES ? 2 : 1;                 // z buffers
     static constexpr int NY = STATES ? 2 : 1;                 // y buffers (a states pass has no x)
-    static constexpr int RB = STATES ? 0 : DX * DZ * 2;       // R as bf16: DZ / 64 halves of DX rows of 128 bytes
+    static constexpr int RB = STATES ? DX * 128 : DX * DZ * 2;  // R as bf16: DZ / 64 halves of DX rows of 128 bytes
     static constexpr int T_X = 0;
     static constexpr int T_Y = T_X + (STATES ? 0 : XB);
     static constexpr int T_YH = T_Y + NY * XB;
@@ -197,22 +197,73 @@ __device__ __forceinline__ void clear_rows(uint32_t tz, int n, int tid, int nt) 
     }
 }
 
-// Row `row` of the state in tensor memory (this thread's lane) to an array of [DX][DZ] states.
+// States in memory. A thread holds a row of the state, a warp 32 rows; lane by lane, 16-byte accesses to rows 512 bytes
+// apart keep the SM's load path busy for 4 K cycles per state. So a warp moves 32 x 32 blocks with eight lanes to a row
+// and turns them in 4 KB of shared memory of its own (the rows of the R tile that it alone writes).
+__device__ __forceinline__ uint32_t turn_at(int row, int piece) { return (uint32_t)(row * 128 + ((piece ^ (row & 7)) << 4)); }
+
+// Columns c .. c + 31 of the warp's 32 rows (first row r0) of a state [DX][DZ], or `turned` of one [DZ][DX]: v = this
+// lane's row.
 template <int DX, int DZ>
-__device__ __forceinline__ void store_state(float* state, const Pass& p, int row, uint32_t taddr) {
-    float* dst = state + row * p.six;
+__device__ __forceinline__ void load_block(const float* state, bool turned, int r0, int c, uint32_t turn, float (&v)[32]) {
+    const int lane = threadIdx.x & 31;
+    if (!turned) {
+        const float* src = state + (r0 + (lane >> 3)) * DZ + c + 4 * (lane & 7);
+        float4 x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = __ldcs(reinterpret_cast<const float4*>(src + 4 * k * DZ));
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            sts128(turn + turn_at(4 * k + (lane >> 3), lane & 7), __float_as_uint(x[k].x), __float_as_uint(x[k].y),
+                   __float_as_uint(x[k].z), __float_as_uint(x[k].w));
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            uint32_t u[4];
+            lds128(turn + turn_at(lane, k), u);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[4 * k + e] = __uint_as_float(u[e]);
+        }
+        __syncwarp();
+    } else {        // transposed: a column's 32 rows lie together
+        const float* src = state + r0 + lane + c * DX;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = src[i * DX];
+    }
+}
+
+template <int DX, int DZ>
+__device__ __forceinline__ void store_block(float* state, bool turned, int r0, int c, uint32_t turn, const float (&v)[32]) {
+    const int lane = threadIdx.x & 31;
+    if (!turned) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            sts128(turn + turn_at(lane, k), __float_as_uint(v[4 * k]), __float_as_uint(v[4 * k + 1]), __float_as_uint(v[4 * k + 2]),
+                   __float_as_uint(v[4 * k + 3]));
+        __syncwarp();
+        float* dst = state + (r0 + (lane >> 3)) * DZ + c + 4 * (lane & 7);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            uint32_t u[4];
+            lds128(turn + turn_at(4 * k + (lane >> 3), lane & 7), u);
+            *reinterpret_cast<uint4*>(dst + 4 * k * DZ) = make_uint4(u[0], u[1], u[2], u[3]);
+        }
+        __syncwarp();
+    } else {
+        float* dst = state + r0 + lane + c * DX;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) dst[i * DX] = v[i];
+    }
+}
+
+// The warp's rows of the state in tensor memory to an array of [DX][DZ] states.
+template <int DX, int DZ>
+__device__ __forceinline__ void store_state(float* state, bool turned, int r0, uint32_t turn, uint32_t taddr) {
 #pragma unroll 1
     for (int c = 0; c < DZ; c += 32) {
         float v[32];
         tmem_ld32(taddr + c, v);
-        if (p.siz == 1) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 4)
-                *reinterpret_cast<float4*>(dst + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) dst[(c + i) * p.siz] = v[i];
-        }
+        store_block<DX, DZ>(state, turned, r0, c, turn, v);
     }
 }
 
@@ -230,8 +281,8 @@ struct Work {
 
 // False: nothing to do.
 template <bool STATES>
-__device__ __forceinline__ bool find_work(const Args& a, long long u, Work& w) {
-    const int pi = (int)(u % a.l.npass);      // the passes of a segment side by side: they read the same rows
+__device__ __forceinline__ bool find_work(const Args& a, int u, Work& w) {
+    const int pi = u % a.l.npass;      // the passes of a segment side by side: they read the same rows
     w.p = &a.l.pass[pi];
     w.maps = a.map[pi];
     if (!locate(a.l.geo, u / a.l.npass, w.sg)) return false;
@@ -241,6 +292,14 @@ __device__ __forceinline__ bool find_work(const Args& a, long long u, Work& w) {
     // chunk of step j: in the pass's direction; a states pass comes from the far end
     w.down = STATES ? !w.rev : w.rev;
     return w.nchunk > 0;
+}
+
+// The state a unit starts from (null: zero).
+template <int DX, int DZ>
+__device__ __forceinline__ const float* start_state(const Work& w) {
+    const Pass& p = *w.p;
+    if (p.bound && !w.sg.alone) return p.bound + (w.rev ? w.sg.entry + w.sg.step : w.sg.entry) * (long long)(DX * DZ);
+    return p.ext_in && !w.sg.fresh ? p.ext_in + w.sg.ext * (long long)(DX * DZ) : nullptr;
 }
 
 template <int DX, int DZ, bool SPLIT, bool STATES>
@@ -302,7 +361,7 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
 
     // units of this CTA; `it` numbers its chunks through
 #define HD_UNITS(w)                                                                        \
-    for (long long u_ = blockIdx.x; u_ < a.total && !failed; u_ += gridDim.x)              \
+    for (int u_ = blockIdx.x; u_ < a.total && !failed; u_ += gridDim.x)                    \
         if (Work w; find_work<STATES>(a, u_, w))
 
     if (warp == 20) {
@@ -313,6 +372,8 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                 const Pass& p = *w.p;
                 const Segment& sg = w.sg;
                 const int hx = sg.h / p.x.div, hy = sg.h / p.y.div, hz = sg.h / p.z.div;
+                if (const float* src = STATES ? nullptr : start_state<DX, DZ>(w))
+                    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" :: "l"(src), "r"(DX * DZ * 4) : "memory");
                 for (int j = 0; j < w.nchunk; ++j, ++it) {
                     const int t = sg.t0 + w.chunk(j) * C;
                     // Shared memory has room for one x and one y tile: the rows start on their way into L2 while the
@@ -443,12 +504,13 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
         HD_UNITS(w) {
         const Pass& p = *w.p;
         const bool rev = w.rev;
-        const float* gp = p.g + w.sg.b * p.gb + w.sg.h * p.gh;
+        const long long gstep = p.gt;     // (in registers: the loops below would read the pass from memory again and again)
+        const float* gp = p.g + w.sg.b * p.gb + w.sg.h * p.gh + w.sg.t0 * gstep;
         auto raw = [&](int j, float (&r)[4]) {
             const int n = w.rows(j);
-            const long long t0 = (long long)w.sg.t0 + w.chunk(j) * C;
+            const int t0 = w.chunk(j) * C + 4 * lane;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) r[i] = 4 * lane + i < n ? gp[(t0 + 4 * lane + i) * p.gt] : 0.f;
+            for (int i = 0; i < 4; ++i) r[i] = 4 * lane + i < n ? gp[(t0 + i) * gstep] : 0.f;
         };
         float cur[4], nxt[4];
         raw(0, cur);
@@ -530,9 +592,9 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                 if (tid == 0) { mbar_arrive(y_ready); mbar_arrive(&g_free[s]); }
             }
             if (failed || !group_wait(r_done, (it & 1) ^ 1, 1, N, warp == 0)) { failed = true; break; }
-            if (grp == 0 && (DX == 128 || warp < 2))
-                store_state<DX, DZ>(p.bound + (w.rev ? sg.entry : sg.entry + sg.step) * (long long)(DX * DZ), p, gt,
-                                    tmem + TM_R + lane_off);
+            if (grp == 0 && (DX == 128 || warp < 2))        // (the R tile's place is not used otherwise here)
+                store_state<DX, DZ>(p.bound + (w.rev ? sg.entry : sg.entry + sg.step) * (long long)(DX * DZ), p.siz != 1, 32 * warp,
+                                sb + Ly::T_R + 4096 * warp, tmem + TM_R + lane_off);
         }
         if (failed && tid == 0) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
     } else if (grp == 0) {
@@ -541,60 +603,68 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
         const uint32_t tr = sb + Ly::T_R;
         uint32_t it = 0;
         HD_UNITS(w) {
-        const Pass& p = *w.p;
-        const Segment& sg = w.sg;
-        const float* src = nullptr;
-        if (p.bound && !sg.alone) src = p.bound + (w.rev ? sg.entry + sg.step : sg.entry) * (long long)(DX * DZ);
-        else if (p.ext_in && !sg.fresh) src = p.ext_in + sg.ext * (long long)(DX * DZ);
+        const float* src = start_state<DX, DZ>(w);
+        float* out = w.p->ext_out && (w.rev ? w.sg.first : w.sg.last) ? w.p->ext_out + w.sg.ext * (long long)(DX * DZ) : nullptr;
+        const bool turned = w.p->siz != 1;
         for (int j = 0; j < w.nchunk; ++j, ++it) {
             const uint32_t b = it & 1;
             if (!group_wait(&g_full[b], (it >> 1) & 1, 1, kGrp, warp == 0) ||
                 (it > 0 && (!group_wait(oi_done, b ^ 1, 1, kGrp, warp == 0) ||
                             !group_wait(r_done, b ^ 1, 1, kGrp, warp == 0)))) { failed = true; break; }
             const float en = gates[b].en;
-            if (mine) {
+            const uint32_t turn = tr + 4096 * warp;      // rows 32 warp .. of the tile's first half
+            auto scale_out = [&](int c, float (&v)[32]) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                    const float2 x = __fmul2_rn(make_float2(v[i], v[i + 1]), make_float2(en, en));
+                    v[i] = x.x; v[i + 1] = x.y;
+                }
+                tmem_st32_nowait(tmem + TM_R + lane_off + c, v);
+            };
+            auto pack8 = [&](int c, const float* v) {    // eight columns of the row, c a multiple of 8
+                const uint32_t off = (uint32_t)(c >> 6) * (DX * 128) + swz(gt, (c & 63) >> 3);
+                uint32_t h[4], l[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (SPLIT) split2(v[2 * e], v[2 * e + 1], h[e], l[e]);
+                    else h[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+                }
+                sts128(tr + off, h[0], h[1], h[2], h[3]);
+                if (SPLIT) sts128(tr + Ly::RB + off, l[0], l[1], l[2], l[3]);
+            };
+            if (mine && j > 0) {
 #pragma unroll 1
                 for (int c = 0; c < DZ; c += 32) {
                     float v[32];
-                    if (j > 0) {
-                        tmem_ld32(tmem + TM_R + lane_off + c, v);
-                    } else if (src) {
-                        const float* s = src + gt * p.six + c * p.siz;
-                        if (p.siz == 1) {
+                    tmem_ld32(tmem + TM_R + lane_off + c, v);
 #pragma unroll
-                            for (int i = 0; i < 32; i += 4) {
-                                const float4 x = *reinterpret_cast<const float4*>(s + i);
-                                v[i] = x.x; v[i + 1] = x.y; v[i + 2] = x.z; v[i + 3] = x.w;
-                            }
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] = s[i * p.siz];
-                        }
+                    for (int i = 0; i < 32; i += 8) pack8(c + i, v + i);
+                    scale_out(c, v);
+                }
+            } else if (mine) {
+                // from memory to tensor memory first (the tile's place turns the blocks), then the tile from there
+#pragma unroll 1
+                for (int c = 0; c < DZ; c += 32) {
+                    float v[32];
+                    if (src) {
+                        load_block<DX, DZ>(src, turned, 32 * warp, c, turn, v);
                     } else {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = 0.f;
                     }
-#pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        const uint32_t off = (uint32_t)((c + i) >> 6) * (DX * 128) + swz(gt, ((c + i) & 63) >> 3);
-                        uint32_t h[4], l[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            if (SPLIT) split2(v[i + 2 * e], v[i + 2 * e + 1], h[e], l[e]);
-                            else h[e] = pack_bf16(v[i + 2 * e], v[i + 2 * e + 1]);
-                        }
-                        sts128(tr + off, h[0], h[1], h[2], h[3]);
-                        if (SPLIT) sts128(tr + Ly::RB + off, l[0], l[1], l[2], l[3]);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        const float2 x = __fmul2_rn(make_float2(v[i], v[i + 1]), make_float2(en, en));
-                        v[i] = x.x; v[i + 1] = x.y;
-                    }
                     tmem_st32_nowait(tmem + TM_R + lane_off + c, v);
                 }
                 tmem_wait_st();
+#pragma unroll 1
+                for (int c = 0; c < DZ; c += 32) {
+                    float v[32];
+                    tmem_ld32(tmem + TM_R + lane_off + c, v);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) pack8(c + i, v + i);
+                    scale_out(c, v);
+                }
             }
+            tmem_wait_st();
             fence_async_smem();
             fence_before_sync();
             named_sync(1, kGrp);
@@ -602,8 +672,13 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
         }
         // the state it ends with
         if (failed || !group_wait(r_done, (it & 1) ^ 1, 1, kGrp, warp == 0)) { failed = true; break; }
-        if (mine && p.ext_out && (w.rev ? sg.first : sg.last))
-            store_state<DX, DZ>(p.ext_out + sg.ext * (long long)(DX * DZ), p, gt, tmem + TM_R + lane_off);
+        if (out) {
+            if (!group_wait(oi_done, (it & 1) ^ 1, 1, kGrp, warp == 0)) { failed = true; break; }     // the tile is free
+            if (mine) {
+                store_state<DX, DZ>(out, turned, 32 * warp, tr + 4096 * warp, tmem + TM_R + lane_off);
+                fence_async_smem();
+            }
+        }
         }
         if (failed && gt == 0) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
     } else if (grp <= 2) {
@@ -739,6 +814,11 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
         HD_UNITS(w) {
         const Pass& p = *w.p;
         const Segment& sg = w.sg;
+        const bool f32 = p.o_f32;
+        const long long ostep = p.ot, wstep = p.w.st;
+        char* obase = static_cast<char*>(p.o) + (sg.b * p.ob + sg.h * p.oh) * (f32 ? 4 : 2);
+        const __nv_bfloat16* wbase = SPLIT ? static_cast<const __nv_bfloat16*>(p.w.p) + sg.b * p.w.sb + (sg.h / p.w.div) * p.w.sh : nullptr;
+        float* dots = SPLIT ? p.dots + ((long long)sg.b * a.l.geo.H + sg.h) * a.l.geo.T : nullptr;
         for (int j = 0; j < w.nchunk; ++j, ++it) {
             const uint32_t b = it & 1;
             const int n = w.rows(j);
@@ -749,10 +829,10 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
             if (!group_wait(oi_done, b, 4, kGrp, poll)) { failed = true; break; }
             if (gt == 0) mbar_arrive(&g_free[b]);     // every thread of the group has read its gates
             if (!group_wait(op_done, b, 4, kGrp, poll)) { failed = true; break; }
-            const bool staged = Ly::STAGED && n == C && !p.o_f32;
+            const bool staged = Ly::STAGED && n == C && !f32;
             const int t0 = sg.t0 + w.chunk(j) * C;
             const bool live = gt < n;
-            const long long at = sg.b * p.ob + sg.h * p.oh + (long long)(t0 + gt) * p.ot;
+            const long long at = (t0 + gt) * ostep;
             float dot = 0.f;
 #pragma unroll 1
             for (int c = 0; c < DZ; c += 32) {
@@ -771,8 +851,7 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                                pack_bf16(v[i + 6], v[i + 7]));
                 } else if (live) {
                     if (SPLIT) {
-                        const uint4* wp = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.w.p) + sg.b * p.w.sb +
-                                                                         (sg.h / p.w.div) * p.w.sh + (long long)(t0 + gt) * p.w.st + c);
+                        const uint4* wp = reinterpret_cast<const uint4*>(wbase + (t0 + gt) * wstep + c);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const uint4 x = wp[i];
@@ -784,12 +863,12 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                             }
                         }
                     }
-                    if (p.o_f32) {
-                        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.o) + at + c);
+                    if (f32) {
+                        float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(obase) + at + c);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
                     } else {
-                        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + at + c);
+                        uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(obase) + at + c);
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             dst[i] = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
@@ -797,7 +876,7 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                     }
                 }
             }
-            if (SPLIT && live) p.dots[((long long)sg.b * a.l.geo.H + sg.h) * a.l.geo.T + t0 + gt] = dot;
+            if (SPLIT && live) dots[t0 + gt] = dot;
             if (staged) fence_async_smem();
             fence_before_sync();
             named_sync(4, kGrp);
@@ -834,7 +913,7 @@ cudaError_t run(const Args& a, cudaStream_t s) {
     auto f = hd_tc_kernel<DX, DZ, SPLIT, STATES>;
     const cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(f), bytes, set);
     if (e != cudaSuccess) return e;
-    const long long sms = sm_count();
+    const int sms = sm_count();
     f<<<(unsigned)(a.total < sms ? a.total : sms), NT, bytes, s>>>(a);
     return cudaGetLastError();
 }
@@ -852,7 +931,7 @@ bool tc_supported(bool bf16, int dk, int dv) { return bf16 && (dk == 64 || dk ==
 cudaError_t launch_tc(const Launch& l, cudaStream_t s) {
     const long long n = units(l.geo, l.B, l.max_blocks);
     if (n == 0) return cudaSuccess;
-    if (n >= (1LL << 31)) return cudaErrorInvalidValue;
+    if (n >= (1LL << 29)) return cudaErrorInvalidValue;    // three passes and a grid's stride stay within 31 bits
     // passes of one size and kind go in one launch
     bool done[3] = {};
     for (int i = 0; i < l.npass; ++i) {
@@ -879,7 +958,7 @@ cudaError_t launch_tc(const Launch& l, cudaStream_t s) {
                 !map_rows(&a.map[k][3], View{p.o, p.ob, p.oh, p.ot, 1}, p.DZ, T, H, l.B))
                 return cudaErrorInvalidValue;
         }
-        a.total = n * a.l.npass;
+        a.total = (int)n * a.l.npass;
         const bool split = q.dots != nullptr, states = q.states_only != 0;
         cudaError_t e;
         if (q.DX == 128 && q.DZ == 128) e = run_kind<128, 128>(a, split, states, s);
