@@ -21,24 +21,25 @@
 // (forward: row to its block's start, that start to the column block's end, that end to the column), two of them per
 // token and one per pair of blocks: a quarter of the exponentials, and nothing overflows for any gate.
 //
-// Work split: groups of four warps (thread = lane of tensor memory; B has eight) and three single warps:
-//   A  the state: R to bf16 in shared memory, e^{G_n} R back        B  Y~ from Y
-//   C  P from D                                                     O  o from Oi and Op
+// Work split: groups of four warps (thread = lane of tensor memory) and three single warps:
+//   A   the state: R to bf16 in shared memory, e^{G_n} R back      B1, B2  Y~ from Y, of the chunk's two halves
+//   C   P from D                                                   O   o from Oi and Op
 //   copies (TMA), MMA issue, gates
-// The issuer's order within a chunk, D Oi R Op, leaves the CUDA-core phases of a chunk under the other products.
+// The gate warp also says for each chunk what the others need to know of it; they only follow. Warps of a group do not
+// wait for each other: each hands its part on by itself (a barrier of the group's threads took 300 cycles, several times
+// a chunk). The issuer's order within a chunk, D Oi R Op, leaves the CUDA-core phases of a chunk under the other products.
 // Each row sequence is read once by TMA in the 128-byte swizzle; the same tile serves K-major (D, Oi) and MN-major (Op,
 // R) operands. A full chunk's o leaves by TMA from a tile of its own (16-byte stores of rows by lanes took 3.2 K cycles
 // of the SM's store path); a ragged one, an fp32 one, and with SPLIT (whose second part of R takes the tile's place)
 // every one is stored from registers.
 //
 // A pass for states only (the segments' own contributions) walks the chunks from the far end, so that the weights
-// e^{(gates behind the token)} need no rescaling of R: its accumulator is touched by MMAs alone, and all four groups
-// form Y~.
+// e^{(gates behind the token)} need no rescaling of R: its accumulator is touched by MMAs alone, and all groups form
+// Y~.
 //
 // Bound: by the bytes of x, y, z and o (1 KB a token and head at 128 x 128): a chunk is 128 KB, 5.6 K cycles of its
 // share of HBM bandwidth on 152 SMs, against 2.6 K cycles of products and about 2.5 K of each group's work.
 #include <cstring>
-#include <type_traits>
 
 #include "hd_internal.h"
 #include "tc_common.cuh"
@@ -51,8 +52,8 @@ using namespace tc;
 
 constexpr int C = kChunk;                  // 128
 constexpr int kGrp = 128;
-constexpr int kGrpB = 2 * kGrp;            // group B has eight warps
-constexpr int NT = 5 * kGrp + 96;          // groups A, B, C, O; warps 20 (copies), 21 (MMA issue), 22 (gates)
+constexpr int kWorkers = 20;                // warps of the groups A (0-3), B1 (4-7), B2 (8-11), C (12-15), O (16-19)
+constexpr int NT = 32 * kWorkers + 96;     // and warps 20 (copies), 21 (MMA issue), 22 (gates)
 constexpr uint32_t kHalf = C * 128;        // bytes of a half tile: 128 rows of 64 bf16
 constexpr uint32_t TM_R = 0, TM_D = 128, TM_OI = 256, TM_OP = 384, kTmemCols = 512;
 constexpr double kLog2e = 1.4426950408889634;
@@ -63,8 +64,9 @@ struct alignas(128) Args {
     int total;                // units of work: segments times passes
 };
 
-// Per-chunk gate values, double-buffered; A_i: cumulative gates at the start of block i of 32 tokens (log2 units).
-struct GateBuf {
+// What the gate warp says of a chunk, double-buffered; A_i: cumulative gates at the start of block i of 32 tokens (log2
+// units).
+struct alignas(16) GateBuf {
     float rc[C];        // G_t minus its block's start
     float cf[C];        // forward e^{A_{i+1} - G_t}, backward e^{G_t - A_i}: a token as a column of P, and as a row of Y~
     float f[4][4];      // between row block i and column block j: forward e^{A_i - A_{j+1}}, backward e^{A_j - A_{i+1}}
@@ -72,8 +74,18 @@ struct GateBuf {
     float ce[4];        // Y~: times this. Forward e^{G_n - A_{i+1}}, backward e^{A_i} (a states pass: and the chunks between)
     float re[4];        // Oi: a row's factor times this. Forward e^{A_i}, backward e^{G_n - A_{i+1}}
     float en;           // e^{G_n}
-    float pad[3];
+    int n;              // tokens
+    int flags;          // kFirst .. kEnd
+    int t0, h, b;       // where its rows lie
+    int pass;
+    const float* src;   // first chunk: the state to start from (null: zero)
+    float* dst;         // last chunk: where the state goes (null: nowhere)
+    char* o;            // the head's first output row
+    const __nv_bfloat16* w;
+    float* dots;        // the head's
+    long long ostep, wstep;
 };
+enum : int { kFirst = 1, kLast = 2, kRev = 4, kTurned = 8, kOutF32 = 16, kEnd = 32 };
 static_assert(sizeof(GateBuf) % 16 == 0, "16-byte rows");
 
 template <int DX, int DZ, bool SPLIT, bool STATES>
@@ -92,7 +104,7 @@ struct Layout {
     static constexpr bool STAGED = !SPLIT && !STATES;
     static constexpr int GATES = T_O + (STAGED ? ZB : 0);
     static constexpr int BARS = GATES + 2 * (int)sizeof(GateBuf);
-    static constexpr int TOTAL = BARS + 256;   // 23 barriers, the address of the tensor memory
+    static constexpr int TOTAL = BARS + 192;   // 23 barriers, the address of the tensor memory
     static_assert(TOTAL <= 227 * 1024, "shared memory budget");
 };
 
@@ -148,9 +160,8 @@ __device__ __forceinline__ void tmem_st32_nowait(uint32_t taddr, const float (&v
     tmem_st16(taddr + 16, r + 16);
 }
 
-// Sixteen bytes of a y row times the row's weight, as hi + lo (zero if `off`, whatever they hold).
-template <bool CHECK>
-__device__ __forceinline__ void scale16(const uint32_t (&u)[4], float w, bool off, uint32_t th, uint32_t tl) {
+// Sixteen bytes of a y row times the row's weight, as hi + lo.
+__device__ __forceinline__ void scale16(const uint32_t (&u)[4], float w, uint32_t th, uint32_t tl) {
     const float2 w2 = make_float2(w, w);
     uint32_t h[4], l[4];
 #pragma unroll
@@ -160,10 +171,6 @@ __device__ __forceinline__ void scale16(const uint32_t (&u)[4], float w, bool of
         const float2 r = __ffma2_rn(make_float2(__uint_as_float(h[e] << 16), __uint_as_float(h[e] & 0xFFFF0000u)),
                                     make_float2(-1.f, -1.f), x);
         l[e] = pack_bf16(r.x, r.y);
-    }
-    if (CHECK && off) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) h[e] = l[e] = 0u;
     }
     sts128(th, h[0], h[1], h[2], h[3]);
     sts128(tl, l[0], l[1], l[2], l[3]);
@@ -183,15 +190,17 @@ __device__ __forceinline__ void scale_rows(uint32_t ty, uint32_t th, uint32_t tl
         const uint32_t off = (uint32_t)(c >> 3) * kHalf + swz(t, c & 7);
         uint32_t u[4];
         lds128(ty + off, u);
-        scale16<true>(u, g.cf[t] * g.ce[t >> 5], t >= n, th + off, tl + off);
+        float w = g.cf[t] * g.ce[t >> 5];
+        if (t >= n) u[0] = u[1] = u[2] = u[3] = 0u, w = 0.f;
+        scale16(u, w, th + off, tl + off);
     }
 }
 
-// Rows n .. 127 of a z tile become zero: they may belong to another request and hold anything.
+// Rows r0 .. r1 - 1 of a z tile become zero: they may belong to another request and hold anything.
 template <int DZ>
-__device__ __forceinline__ void clear_rows(uint32_t tz, int n, int tid, int nt) {
+__device__ __forceinline__ void clear_rows(uint32_t tz, int r0, int r1, int tid, int nt) {
     constexpr int PER = DZ / 8;
-    for (int i = n * PER + tid; i < C * PER; i += nt) {
+    for (int i = r0 * PER + tid; i < r1 * PER; i += nt) {
         const int t = i / PER, c = i % PER;
         sts128(tz + (uint32_t)(c >> 3) * kHalf + swz(t, c & 7), 0u, 0u, 0u, 0u);
     }
@@ -312,35 +321,43 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
         return;
     }
 
+    // completed copies and products (one arrival each); parts handed on by warps (one arrival per warp)
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Ly::BARS);
     uint64_t* full_x = bars + 0;
     uint64_t* full_y = bars + 1;     // [2]
     uint64_t* full_z = bars + 3;     // [2]
     uint64_t* free_z = bars + 5;     // [2] Op of the chunk that used the buffer
-    uint64_t* g_full = bars + 7;     // [2]
-    uint64_t* g_free = bars + 9;     // [2] one arrival per group
-    uint64_t* d_done = bars + 11;    // D
-    uint64_t* oi_done = bars + 12;   // Oi
-    uint64_t* r_done = bars + 13;    // R (all of its tokens)
-    uint64_t* op_done = bars + 14;   // Op
-    uint64_t* y_ready = bars + 15;   // B: Y~ of the first 64 tokens (and a cleared z); a states pass: all of it
-    uint64_t* r_ready = bars + 16;   // A: R scaled, its bf16 copy written
-    uint64_t* p_ready = bars + 17;   // C: P
-    uint64_t* o_free = bars + 18;    // C: Oi and Op read
-    uint64_t* drain = bars + 19;
-    uint64_t* y_read = bars + 20;    // B: the y tile is in its registers
-    uint64_t* y_rest = bars + 21;    // B: Y~ of the other 64 tokens
-    uint64_t* r_half = bars + 22;    // R from the first 64 tokens
+    uint64_t* d_done = bars + 7;     // D
+    uint64_t* oi_done = bars + 8;    // Oi
+    uint64_t* r_half = bars + 9;     // R from the first 64 tokens
+    uint64_t* r_done = bars + 10;    // R from all
+    uint64_t* op_done = bars + 11;   // Op
+    uint64_t* drain = bars + 12;
+    uint64_t* g_full = bars + 13;    // [2] gates, one arrival
+    uint64_t* g_free = bars + 15;    // [2] every worker warp and the issuer
+    uint64_t* r_ready = bars + 17;   // A: R scaled, its bf16 copy written
+    uint64_t* y_read = bars + 18;    // B1, B2: the y tile is in their registers
+    uint64_t* y_ready = bars + 19;   // B1: Y~ of the first 64 tokens (a states pass: of all, every worker)
+    uint64_t* y_rest = bars + 20;    // B2: of the others
+    uint64_t* p_ready = bars + 21;   // C: P
+    uint64_t* o_free = bars + 22;    // O: Oi and Op read
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 23);
     GateBuf* gates = reinterpret_cast<GateBuf*>(smem + Ly::GATES);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int grp = warp >> 2, gt = tid & (kGrp - 1);
-    const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const int rw = warp & 3, row = tid & (kGrp - 1);     // a worker's 32 lanes of tensor memory, and this thread's
+    const uint32_t lane_off = static_cast<uint32_t>(32 * rw) << 16;
     const long long wl = a.l.wait_cycles;
 
     if (tid == 0) {
-        for (int i = 0; i < 23; ++i) mbar_init(bars + i, i == 9 || i == 10 ? (STATES ? 1 : 4) : 1);
+        for (int i = 0; i < 23; ++i) {
+            uint32_t n = 1;
+            if (i == 15 || i == 16) n = kWorkers + 1;
+            else if (i == 17 || i >= 20) n = 4;
+            else if (i == 18) n = 8;
+            else if (i == 19) n = STATES ? kWorkers : 4;
+            mbar_init(bars + i, n);
+        }
         mbar_fence_init();
     }
     if (warp == 0) tmem_alloc(tmem_holder, kTmemCols);
@@ -350,62 +367,59 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
     const uint32_t tmem = *tmem_holder;
     bool failed = false;
 
-    // A bounded wait of `n` threads (named barrier `id`) on a phase: the first warp of them polls.
-    auto group_wait = [&](uint64_t* bar, uint32_t parity, uint32_t id, uint32_t n, bool polls) -> bool {
-        bool got = true;
-        if (polls) got = mbar_wait(bar, parity, wl);
-        const bool bad = named_sync_or(id, n, !got);
+    // A bounded wait of a warp. One that gives up leaves its loop; the others run into their own limits.
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, wl));
         fence_after_sync();
-        return !bad;
+        return ok;
     };
-
-    // units of this CTA; `it` numbers its chunks through
-#define HD_UNITS(w)                                                                        \
-    for (int u_ = blockIdx.x; u_ < a.total && !failed; u_ += gridDim.x)                    \
-        if (Work w; find_work<STATES>(a, u_, w))
+    // Hands on what the warp's lanes have written.
+    auto arrive = [&](uint64_t* bar) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+    };
 
     if (warp == 20) {
         // =================== copies ===================
         if (lane == 0) {
             uint32_t it = 0, nx = 0, ny = 0, nz = 0;    // chunks; copies started
-            HD_UNITS(w) {
-                const Pass& p = *w.p;
-                const Segment& sg = w.sg;
-                const int hx = sg.h / p.x.div, hy = sg.h / p.y.div, hz = sg.h / p.z.div;
+            for (int u = blockIdx.x; u < a.total && !failed; u += gridDim.x) {
+                Work w;
+                if (!find_work<STATES>(a, u, w)) continue;
+                const CUtensorMap* maps = w.maps;
+                const int hx = w.sg.h / w.p->x.div, hy = w.sg.h / w.p->y.div, hz = w.sg.h / w.p->z.div, bb = w.sg.b;
                 if (const float* src = STATES ? nullptr : start_state<DX, DZ>(w))
                     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" :: "l"(src), "r"(DX * DZ * 4) : "memory");
                 for (int j = 0; j < w.nchunk; ++j, ++it) {
-                    const int t = sg.t0 + w.chunk(j) * C;
-                    // Shared memory has room for one x and one y tile: the rows start on their way into L2 while the
-                    // buffers are still in use.
-                    for (int x = 0; x < DX / 64; ++x) {
-                        tma_prefetch_4d(&w.maps[1], 64 * x, t, hy, sg.b);
-                        if (!STATES) tma_prefetch_4d(&w.maps[0], 64 * x, t, hx, sg.b);
-                    }
-                    for (int x = 0; x < DZ / 64; ++x) tma_prefetch_4d(&w.maps[2], 64 * x, t, hz, sg.b);
+                    const int t = w.sg.t0 + w.chunk(j) * C;
+                    const uint32_t s = it % Ly::NZ;
                     auto load = [&](uint32_t dst, int which, int D, int h, uint64_t* bar) {
                         mbar_expect_tx(bar, D * 256);
-                        for (int x = 0; x < D / 64; ++x) tma_load_4d(dst + x * kHalf, &w.maps[which], 64 * x, t, h, sg.b, bar);
+                        for (int x = 0; x < D / 64; ++x) tma_load_4d(dst + x * kHalf, &maps[which], 64 * x, t, h, bb, bar);
                     };
-                    const int s = it % Ly::NZ;
                     if (STATES) {
                         if (it >= 2 && !mbar_wait(&free_z[s], ((it - 2) >> 1) & 1, wl)) { failed = true; break; }
                         load(sb + Ly::T_Y + s * Ly::XB, 1, DX, hy, &full_y[s]);
-                        load(sb + Ly::T_Z + s * Ly::ZB, 2, DZ, hz, &full_z[s]);
                     } else {
-                        // y once the D before is formed and its tile in B's registers, x once its Oi is, z once the Op
-                        // of its buffer is
+                        // Shared memory has room for one x, y and z tile: the rows start on their way into L2 while the
+                        // buffers are still in use.
+                        for (int x = 0; x < DX / 64; ++x) {
+                            tma_prefetch_4d(&maps[1], 64 * x, t, hy, bb);
+                            tma_prefetch_4d(&maps[0], 64 * x, t, hx, bb);
+                        }
+                        for (int x = 0; x < DZ / 64; ++x) tma_prefetch_4d(&maps[2], 64 * x, t, hz, bb);
+                        // y once the D before is formed and its tile in registers, x once its Oi is, z once its Op is
                         if (it >= 1 && (!mbar_wait(d_done, (it - 1) & 1, wl) || !mbar_wait(y_read, (it - 1) & 1, wl))) { failed = true; break; }
                         load(sb + Ly::T_Y, 1, DX, hy, full_y);
                         ++ny;
                         if (it >= 1 && !mbar_wait(oi_done, (it - 1) & 1, wl)) { failed = true; break; }
                         load(sb + Ly::T_X, 0, DX, hx, full_x);
                         ++nx;
-                        if (it >= Ly::NZ && !mbar_wait(&free_z[s], ((it - Ly::NZ) / Ly::NZ) & 1, wl)) { failed = true; break; }
-                        load(sb + Ly::T_Z + s * Ly::ZB, 2, DZ, hz, &full_z[s]);
-                        ++nz;
+                        if (it >= 1 && !mbar_wait(free_z, (it - 1) & 1, wl)) { failed = true; break; }
                     }
-                    if (STATES) { ++ny; ++nz; }
+                    if (STATES) ++ny;
+                    load(sb + Ly::T_Z + s * Ly::ZB, 2, DZ, hz, &full_z[s]);
+                    ++nz;
                 }
             }
             if (failed) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
@@ -430,65 +444,65 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
             const uint32_t idO = idesc_bf16(128, DZ, false, true);
             const uint32_t idR = idesc_bf16(128, DZ, true, true);
             auto mma_D = [&]() {
-#pragma unroll
+#pragma unroll 1
                 for (int h = 0; h < DX / 64; ++h)
                     mma_chain(tmem + TM_D, smem_desc_sw128(sb + Ly::T_X + h * kHalf, 16, 1024), 32,
                               smem_desc_sw128(sb + Ly::T_Y + h * kHalf, 16, 1024), 32, idD, 64, h > 0);
                 mma_commit(d_done);
             };
             auto mma_Oi = [&]() {
-#pragma unroll
-                for (int s = 0; s < (SPLIT ? 2 : 1); ++s)
-#pragma unroll
-                    for (int h = 0; h < DX / 64; ++h)
-                        mma_chain(tmem + TM_OI, smem_desc_sw128(sb + Ly::T_X + h * kHalf, 16, 1024), 32,
-                                  smem_desc_sw128(sb + Ly::T_R + s * Ly::RB + h * 64 * 128, DX * 128, 1024), 2048, idO, 64,
-                                  s > 0 || h > 0);
+#pragma unroll 1
+                for (int i = 0; i < (SPLIT ? 2 : 1) * (DX / 64); ++i) {
+                    const int h = i % (DX / 64), s = i / (DX / 64);
+                    mma_chain(tmem + TM_OI, smem_desc_sw128(sb + Ly::T_X + h * kHalf, 16, 1024), 32,
+                              smem_desc_sw128(sb + Ly::T_R + s * Ly::RB + h * 64 * 128, DX * 128, 1024), 2048, idO, 64, i > 0);
+                }
                 mma_commit(oi_done);
             };
             auto mma_R = [&](uint32_t tz, int half, bool acc) {      // 64 tokens: four slices of 2048 bytes
-#pragma unroll
+#pragma unroll 1
                 for (int s = 0; s < 2; ++s)
                     mma_chain(tmem + TM_R, smem_desc_sw128(sb + (s ? Ly::T_YL : Ly::T_YH) + 8192 * half, kHalf, 1024), 2048,
                               smem_desc_sw128(tz + 8192 * half, kHalf, 1024), 2048, idR, 64, acc || s > 0);
             };
             auto mma_Op = [&](uint32_t tz) {
                 const uint64_t dz = smem_desc_sw128(tz, kHalf, 1024);
-#pragma unroll
+#pragma unroll 1
                 for (int s = 0; s < (SPLIT ? 2 : 1); ++s)
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)     // 16 tokens: 8 columns of P
                         mma_bf16_tmem_a(tmem + TM_OP, tmem + TM_D + 32 * (ks >> 1) + 8 * (ks & 1) + 16 * s,
                                         dadd(dz, 2048 * ks), idO, (s > 0 || ks > 0) ? 1u : 0u);
             };
-            uint32_t it = 0;
-            HD_UNITS(w) {
-                for (int j = 0; j < w.nchunk; ++j, ++it) {
-                    const uint32_t par = it & 1, s = it % Ly::NZ, zpar = (it / Ly::NZ) & 1;
-                    const uint32_t tz = sb + Ly::T_Z + s * Ly::ZB;
-                    if (STATES) {
-                        if (!wait1(y_ready, par) || !wait1(&full_z[s], zpar)) { failed = true; break; }
-                        mma_R(tz, 0, j > 0);
-                        mma_R(tz, 1, true);
-                        mma_commit(&free_z[s]);
-                        mma_commit(r_done);
-                        continue;
-                    }
-                    if (!wait1(full_x, par) || !wait1(full_y, par)) { failed = true; break; }
-                    mma_D();
-                    if (!wait1(r_ready, par) || (it > 0 && !wait1(o_free, par ^ 1))) { failed = true; break; }
-                    mma_Oi();
+            for (uint32_t it = 0;; ++it) {
+                const uint32_t par = it & 1, s = it % Ly::NZ, zpar = (it / Ly::NZ) & 1;
+                const uint32_t tz = sb + Ly::T_Z + s * Ly::ZB;
+                if (!wait1(&g_full[par], (it >> 1) & 1)) { failed = true; break; }
+                const int flags = gates[par].flags;
+                mbar_arrive(&g_free[par]);
+                if (flags & kEnd) break;
+                if (STATES) {
                     if (!wait1(y_ready, par) || !wait1(&full_z[s], zpar)) { failed = true; break; }
-                    mma_R(tz, 0, true);
-                    mma_commit(r_half);
-                    if (!wait1(y_rest, par)) { failed = true; break; }
+                    mma_R(tz, 0, !(flags & kFirst));
                     mma_R(tz, 1, true);
-                    mma_commit(r_done);
-                    if (!wait1(p_ready, par)) { failed = true; break; }
-                    mma_Op(tz);
                     mma_commit(&free_z[s]);
-                    mma_commit(op_done);
+                    mma_commit(r_done);
+                    continue;
                 }
+                if (!wait1(full_x, par) || !wait1(full_y, par)) { failed = true; break; }
+                mma_D();
+                if (!wait1(r_ready, par) || (it > 0 && !wait1(o_free, par ^ 1))) { failed = true; break; }
+                mma_Oi();
+                if (!wait1(y_ready, par) || !wait1(&full_z[s], zpar)) { failed = true; break; }
+                mma_R(tz, 0, true);
+                mma_commit(r_half);
+                if (!wait1(y_rest, par)) { failed = true; break; }
+                mma_R(tz, 1, true);
+                mma_commit(r_done);
+                if (!wait1(p_ready, par)) { failed = true; break; }
+                mma_Op(tz);
+                mma_commit(&free_z[s]);
+                mma_commit(op_done);
             }
             if (failed) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
             mma_commit(drain);       // every MMA this thread issued: none may run on freed tensor memory
@@ -501,409 +515,378 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
         // which this warp took 6.6 K cycles a chunk and held up all others) a few integer instructions each.
         auto real = [](long long x) { return (float)x * 2.3283064365386963e-10f; };     // 2^-32
         uint32_t it = 0;
-        HD_UNITS(w) {
-        const Pass& p = *w.p;
-        const bool rev = w.rev;
-        const long long gstep = p.gt;     // (in registers: the loops below would read the pass from memory again and again)
-        const float* gp = p.g + w.sg.b * p.gb + w.sg.h * p.gh + w.sg.t0 * gstep;
-        auto raw = [&](int j, float (&r)[4]) {
-            const int n = w.rows(j);
-            const int t0 = w.chunk(j) * C + 4 * lane;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) r[i] = 4 * lane + i < n ? gp[(t0 + i) * gstep] : 0.f;
+        auto take = [&]() -> GateBuf* {       // the next buffer, once its chunk before the last is done with
+            const uint32_t b = it & 1;
+            if (it >= 2 && !wait(&g_free[b], ((it - 2) >> 1) & 1)) { failed = true; return nullptr; }
+            return gates + b;
         };
-        float cur[4], nxt[4];
-        raw(0, cur);
-        long long passed = 0;    // gates of the chunks before
-        float lost = 0.f;        // NaN once a gate was: it then reaches everything behind
-        for (int j = 0; j < w.nchunk; ++j, ++it) {
-            if (j + 1 < w.nchunk) raw(j + 1, nxt);
-            long long x[4];
-            bool nan = false;
+        for (int u = blockIdx.x; u < a.total && !failed; u += gridDim.x) {
+            Work w;
+            if (!find_work<STATES>(a, u, w)) continue;
+            const Pass& p = *w.p;
+            const bool rev = w.rev;
+            const long long gstep = p.gt;     // (in registers: the loops below would read the pass from memory again and again)
+            const float* gp = p.g + w.sg.b * p.gb + w.sg.h * p.gh + w.sg.t0 * gstep;
+            auto raw = [&](int j, float (&r)[4]) {
+                const int n = w.rows(j);
+                const int t0 = w.chunk(j) * C + 4 * lane;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                nan |= !(cur[i] <= 1e4f);        // (gates are not positive; one that large is no gate either)
-                const float g = cur[i] < kMinGate ? kMinGate : cur[i];
-                x[i] = __float2ll_rn(g * (float)kLog2e * 4294967296.f) + (i > 0 ? x[i - 1] : 0);
-            }
-            if (__any_sync(0xffffffffu, nan)) lost = __int_as_float(0x7fc00000);
-            long long s = x[3];
+                for (int i = 0; i < 4; ++i) r[i] = 4 * lane + i < n ? gp[(t0 + i) * gstep] : 0.f;
+            };
+            float cur[4], nxt[4];
+            raw(0, cur);
+            // what the others need to know of the unit
+            const float* src = STATES ? nullptr : start_state<DX, DZ>(w);
+            float* dst = nullptr;
+            if (STATES) dst = p.bound + (rev ? w.sg.entry : w.sg.entry + w.sg.step) * (long long)(DX * DZ);
+            else if (p.ext_out && (rev ? w.sg.first : w.sg.last)) dst = p.ext_out + w.sg.ext * (long long)(DX * DZ);
+            const long long ostep = p.ot, wstep = p.w.st;
+            char* o = static_cast<char*>(p.o) + (w.sg.b * p.ob + w.sg.h * p.oh) * (p.o_f32 ? 4 : 2);
+            const __nv_bfloat16* wv = SPLIT ? static_cast<const __nv_bfloat16*>(p.w.p) + w.sg.b * p.w.sb + (w.sg.h / p.w.div) * p.w.sh : nullptr;
+            float* dots = SPLIT ? p.dots + ((long long)w.sg.b * a.l.geo.H + w.sg.h) * a.l.geo.T : nullptr;
+            float* gsum = STATES && p.gsum ? p.gsum + w.sg.entry : nullptr;
+            const int kind = (rev ? kRev : 0) | (p.siz != 1 ? kTurned : 0) | (p.o_f32 ? kOutF32 : 0);
+            long long passed = 0;    // gates of the chunks before
+            float lost = 0.f;        // NaN once a gate was: it then reaches everything behind
+            for (int j = 0; j < w.nchunk; ++j, ++it) {
+                if (j + 1 < w.nchunk) raw(j + 1, nxt);
+                long long x[4];
+                bool nan = false;
 #pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const long long y = __shfl_up_sync(0xffffffffu, s, off);
-                if (lane >= off) s += y;
-            }
-            const long long all = __shfl_sync(0xffffffffu, s, 31);
-            const long long before = s - x[3];                                       // exclusive
-            // this lane's block: its start, its end
-            const long long start = __shfl_sync(0xffffffffu, before, lane & ~7), end = __shfl_sync(0xffffffffu, s, lane | 7);
-            // lanes 4 i + j of the first 16: blocks i and j
-            const int bi = (lane >> 2) & 3, bj = lane & 3;
-            const long long si = __shfl_sync(0xffffffffu, before, 8 * bi), sj = __shfl_sync(0xffffffffu, before, 8 * bj);
-            const long long ei = __shfl_sync(0xffffffffu, s, 8 * bi + 7), ej = __shfl_sync(0xffffffffu, s, 8 * bj + 7);
-            const int b = it & 1;
-            bool ok = true;
-            if (it >= 2) ok = mbar_wait(&g_free[b], ((it - 2) >> 1) & 1, wl);
-            if (!__all_sync(0xffffffffu, ok)) { failed = true; break; }
-            GateBuf& g = gates[b];
-            const long long far = STATES ? passed : 0;
-            float up[4], cf[4];
+                for (int i = 0; i < 4; ++i) {
+                    nan |= !(cur[i] <= 1e4f);        // (gates are not positive; one that large is no gate either)
+                    const float g = cur[i] < kMinGate ? kMinGate : cur[i];
+                    x[i] = __float2ll_rn(g * (float)kLog2e * 4294967296.f) + (i > 0 ? x[i - 1] : 0);
+                }
+                if (__any_sync(0xffffffffu, nan)) lost = __int_as_float(0x7fc00000);
+                long long s = x[3];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                up[i] = real(before - start + x[i]) + lost;
-                cf[i] = ex2(rev ? up[i] : real(end - before - x[i])) + lost;
-            }
-            *reinterpret_cast<float4*>(g.rc + 4 * lane) = make_float4(up[0], up[1], up[2], up[3]);
-            *reinterpret_cast<float4*>(g.cf + 4 * lane) = make_float4(cf[0], cf[1], cf[2], cf[3]);
-            if (lane < 16) g.f[bi][bj] = ex2(real(rev ? sj - ei : si - ej));
-            if (lane < 4) {
-                g.bl[lane] = real(ej - sj);
-                g.ce[lane] = ex2(real((rev ? sj : all - ej) + far));
-                g.re[lane] = ex2(real(rev ? all - ej : sj));
-            }
-            if (lane == 0) g.en = ex2(real(all)) + lost;
-            passed += all;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&g_full[b]);
+                for (int off = 1; off < 32; off <<= 1) {
+                    const long long y = __shfl_up_sync(0xffffffffu, s, off);
+                    if (lane >= off) s += y;
+                }
+                const long long all = __shfl_sync(0xffffffffu, s, 31);
+                const long long before = s - x[3];                                       // exclusive
+                // this lane's block: its start, its end
+                const long long start = __shfl_sync(0xffffffffu, before, lane & ~7), end = __shfl_sync(0xffffffffu, s, lane | 7);
+                // lanes 4 i + j of the first 16: blocks i and j
+                const int bi = (lane >> 2) & 3, bj = lane & 3;
+                const long long si = __shfl_sync(0xffffffffu, before, 8 * bi), sj = __shfl_sync(0xffffffffu, before, 8 * bj);
+                const long long ei = __shfl_sync(0xffffffffu, s, 8 * bi + 7), ej = __shfl_sync(0xffffffffu, s, 8 * bj + 7);
+                GateBuf* gb = take();
+                if (!gb) break;
+                GateBuf& g = *gb;
+                const long long far = STATES ? passed : 0;
+                float up[4], cf[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) cur[i] = nxt[i];
+                for (int i = 0; i < 4; ++i) {
+                    up[i] = real(before - start + x[i]) + lost;
+                    cf[i] = ex2(rev ? up[i] : real(end - before - x[i])) + lost;
+                }
+                *reinterpret_cast<float4*>(g.rc + 4 * lane) = make_float4(up[0], up[1], up[2], up[3]);
+                *reinterpret_cast<float4*>(g.cf + 4 * lane) = make_float4(cf[0], cf[1], cf[2], cf[3]);
+                if (lane < 16) g.f[bi][bj] = ex2(real(rev ? sj - ei : si - ej));
+                if (lane < 4) {
+                    g.bl[lane] = real(ej - sj);
+                    g.ce[lane] = ex2(real((rev ? sj : all - ej) + far));
+                    g.re[lane] = ex2(real(rev ? all - ej : sj));
+                }
+                if (lane == 0) {
+                    g.en = ex2(real(all)) + lost;
+                    g.n = w.rows(j);
+                    g.flags = kind | (j == 0 ? kFirst : 0) | (j == w.nchunk - 1 ? kLast : 0);
+                    g.t0 = w.sg.t0 + w.chunk(j) * C;
+                    g.h = w.sg.h;
+                    g.b = w.sg.b;
+                    g.pass = (int)(w.p - a.l.pass);
+                    g.src = src;
+                    g.dst = dst;
+                    g.o = o;
+                    g.w = wv;
+                    g.dots = dots;
+                    g.ostep = ostep;
+                    g.wstep = wstep;
+                }
+                passed += all;
+                arrive(&g_full[it & 1]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) cur[i] = nxt[i];
+            }
+            if (gsum && lane == 0 && !failed) *gsum = real(passed) * 0.6931471805599453f + lost;
         }
-        if (STATES && p.gsum && lane == 0 && !failed) p.gsum[w.sg.entry] = real(passed) * 0.6931471805599453f + lost;
+        if (!failed) {
+            if (GateBuf* g = take()) {
+                if (lane == 0) g->flags = kEnd;
+                arrive(&g_full[it & 1]);
+            }
         }
         if (failed && lane == 0) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
-    } else if (STATES) {
-        // =================== all groups: Y~; then the state ===================
-        constexpr uint32_t N = 5 * kGrp;
-        uint32_t it = 0;
-        HD_UNITS(w) {
-            const Pass& p = *w.p;
-            const Segment& sg = w.sg;
-            for (int j = 0; j < w.nchunk; ++j, ++it) {
-                const uint32_t s = it & 1, par = (it >> 1) & 1;
-                const int n = w.rows(j);
-                if (!group_wait(&g_full[s], par, 1, N, warp == 0) || !group_wait(&full_y[s], par, 1, N, warp == 0) ||
-                    (it > 0 && !group_wait(r_done, s ^ 1, 1, N, warp == 0)) ||
-                    (n < C && !group_wait(&full_z[s], par, 1, N, warp == 0))) { failed = true; break; }
-                scale_rows<DX>(sb + Ly::T_Y + s * Ly::XB, sb + Ly::T_YH, sb + Ly::T_YL, gates[s], n, tid, N);
-                if (n < C) clear_rows<DZ>(sb + Ly::T_Z + s * Ly::ZB, n, tid, N);
+    } else {
+        // =================== the groups ===================
+        const int grp = warp >> 2;
+        const uint32_t tr = sb + Ly::T_R, turn = tr + 4096 * rw;     // rows 32 rw .. of the R tile's first half: A's warp's own
+        bool storing = false;      // (O, lane 0) a store may still read the warp's rows of the o tile
+        for (uint32_t it = 0;; ++it) {
+            const uint32_t b = it & 1, s = it % Ly::NZ, zpar = (it / Ly::NZ) & 1;
+            const GateBuf& g = gates[b];
+            if (!STATES && (grp == 1 || grp == 2)) {
+                // ---- B1, B2: Y~ of 64 tokens
+                // Their part of the y tile goes into registers as soon as it has landed, so that the next one is on its
+                // way while this one's parts are formed and while the R of the chunk before still reads the parts of its own.
+                constexpr int PER = DX / 8, IT = C / 2 * PER / kGrp, TS = kGrp / PER;     // pieces of a row, of a thread; tokens between two
+                if (!wait(&g_full[b], (it >> 1) & 1)) { failed = true; break; }
+                if (g.flags & kEnd) break;
+                const int h = grp - 1, n = g.n, t0 = 64 * h + row / PER, c = row % PER;
+                const uint32_t col = (uint32_t)(c >> 3) * kHalf;
+                if (!wait(full_y, b)) { failed = true; break; }
+                uint32_t u[IT][4];
+#pragma unroll
+                for (int i = 0; i < IT; ++i) lds128(sb + Ly::T_Y + col + swz(t0 + i * TS, c & 7), u[i]);
+                // (the shared loads have completed when their values are used)
+#pragma unroll
+                for (int i = 0; i < IT; ++i) asm volatile("" : "+r"(u[i][0]), "+r"(u[i][1]), "+r"(u[i][2]), "+r"(u[i][3]));
+                arrive(y_read);
+                float wt[IT];      // read ahead of the stores, which the compiler moves no load across
+#pragma unroll
+                for (int i = 0; i < IT; ++i) wt[i] = g.cf[t0 + i * TS] * g.ce[2 * h + i * TS / 32];
+                if ((it > 0 && !wait(h ? r_done : r_half, b ^ 1)) || (n < C && !wait(&full_z[s], zpar))) { failed = true; break; }
+                if (n < C) {
+#pragma unroll
+                    for (int i = 0; i < IT; ++i)
+                        if (t0 + i * TS >= n) u[i][0] = u[i][1] = u[i][2] = u[i][3] = 0u, wt[i] = 0.f;
+                    clear_rows<DZ>(sb + Ly::T_Z + s * Ly::ZB, max(n, 64 * h), 64 * h + 64, row, kGrp);
+                }
+#pragma unroll
+                for (int i = 0; i < IT; ++i) {
+                    const uint32_t off = col + swz(t0 + i * TS, c & 7);
+                    scale16(u[i], wt[i], sb + Ly::T_YH + off, sb + Ly::T_YL + off);
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) { mbar_arrive(h ? y_rest : y_ready); mbar_arrive(&g_free[b]); }
+                continue;
+            }
+            if (!wait(&g_full[b], (it >> 1) & 1)) { failed = true; break; }
+            const int flags = g.flags, n = g.n;
+            if (flags & kEnd) break;
+            const bool rev = flags & kRev;
+            if (STATES) {
+                // ---- every worker: Y~; behind the last chunk A: the state
+                if (!wait(&full_y[s], zpar) || (it > 0 && !wait(r_done, b ^ 1)) || (n < C && !wait(&full_z[s], zpar))) { failed = true; break; }
+                scale_rows<DX>(sb + Ly::T_Y + s * Ly::XB, sb + Ly::T_YH, sb + Ly::T_YL, g, n, tid, 32 * kWorkers);
+                if (n < C) clear_rows<DZ>(sb + Ly::T_Z + s * Ly::ZB, n, C, tid, 32 * kWorkers);
+                float* dst = g.dst;
                 fence_async_smem();
                 fence_before_sync();      // (the state of the unit before has been read)
-                named_sync(1, N);
-                if (tid == 0) { mbar_arrive(y_ready); mbar_arrive(&g_free[s]); }
-            }
-            if (failed || !group_wait(r_done, (it & 1) ^ 1, 1, N, warp == 0)) { failed = true; break; }
-            if (grp == 0 && (DX == 128 || warp < 2))        // (the R tile's place is not used otherwise here)
-                store_state<DX, DZ>(p.bound + (w.rev ? sg.entry : sg.entry + sg.step) * (long long)(DX * DZ), p.siz != 1, 32 * warp,
-                                sb + Ly::T_R + 4096 * warp, tmem + TM_R + lane_off);
-        }
-        if (failed && tid == 0) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
-    } else if (grp == 0) {
-        // =================== A: the state (thread = row of R; with DX = 64 two warps only keep step) ===================
-        const bool mine = DX == 128 || warp < 2;
-        const uint32_t tr = sb + Ly::T_R;
-        uint32_t it = 0;
-        HD_UNITS(w) {
-        const float* src = start_state<DX, DZ>(w);
-        float* out = w.p->ext_out && (w.rev ? w.sg.first : w.sg.last) ? w.p->ext_out + w.sg.ext * (long long)(DX * DZ) : nullptr;
-        const bool turned = w.p->siz != 1;
-        for (int j = 0; j < w.nchunk; ++j, ++it) {
-            const uint32_t b = it & 1;
-            if (!group_wait(&g_full[b], (it >> 1) & 1, 1, kGrp, warp == 0) ||
-                (it > 0 && (!group_wait(oi_done, b ^ 1, 1, kGrp, warp == 0) ||
-                            !group_wait(r_done, b ^ 1, 1, kGrp, warp == 0)))) { failed = true; break; }
-            const float en = gates[b].en;
-            const uint32_t turn = tr + 4096 * warp;      // rows 32 warp .. of the tile's first half
-            auto scale_out = [&](int c, float (&v)[32]) {
-#pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                    const float2 x = __fmul2_rn(make_float2(v[i], v[i + 1]), make_float2(en, en));
-                    v[i] = x.x; v[i + 1] = x.y;
+                __syncwarp();
+                if (lane == 0) { mbar_arrive(y_ready); mbar_arrive(&g_free[b]); }
+                if ((flags & kLast) && grp == 0 && (DX == 128 || warp < 2)) {
+                    if (!wait(r_done, b)) { failed = true; break; }
+                    store_state<DX, DZ>(dst, flags & kTurned, 32 * warp, turn, tmem + TM_R + lane_off);
                 }
-                tmem_st32_nowait(tmem + TM_R + lane_off + c, v);
-            };
-            auto pack8 = [&](int c, const float* v) {    // eight columns of the row, c a multiple of 8
-                const uint32_t off = (uint32_t)(c >> 6) * (DX * 128) + swz(gt, (c & 63) >> 3);
-                uint32_t h[4], l[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (SPLIT) split2(v[2 * e], v[2 * e + 1], h[e], l[e]);
-                    else h[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
-                }
-                sts128(tr + off, h[0], h[1], h[2], h[3]);
-                if (SPLIT) sts128(tr + Ly::RB + off, l[0], l[1], l[2], l[3]);
-            };
-            if (mine && j > 0) {
+            } else if (grp == 0) {
+                // ---- A: the state (thread = row of R; with DX = 64 two warps only keep step)
+                const bool mine = DX == 128 || warp < 2;
+                if (it > 0 && (!wait(oi_done, b ^ 1) || !wait(r_done, b ^ 1))) { failed = true; break; }
+                const float en = g.en;
+                const float* src = g.src;
+                float* dst = g.dst;
+                const bool turned = flags & kTurned;
+                if (mine && (flags & kFirst)) {     // from memory to tensor memory (the tile's place turns the blocks)
 #pragma unroll 1
-                for (int c = 0; c < DZ; c += 32) {
-                    float v[32];
-                    tmem_ld32(tmem + TM_R + lane_off + c, v);
+                    for (int c = 0; c < DZ; c += 32) {
+                        float v[32];
+                        if (src) {
+                            load_block<DX, DZ>(src, turned, 32 * warp, c, turn, v);
+                        } else {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8) pack8(c + i, v + i);
-                    scale_out(c, v);
-                }
-            } else if (mine) {
-                // from memory to tensor memory first (the tile's place turns the blocks), then the tile from there
-#pragma unroll 1
-                for (int c = 0; c < DZ; c += 32) {
-                    float v[32];
-                    if (src) {
-                        load_block<DX, DZ>(src, turned, 32 * warp, c, turn, v);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = 0.f;
-                    }
-                    tmem_st32_nowait(tmem + TM_R + lane_off + c, v);
-                }
-                tmem_wait_st();
-#pragma unroll 1
-                for (int c = 0; c < DZ; c += 32) {
-                    float v[32];
-                    tmem_ld32(tmem + TM_R + lane_off + c, v);
-#pragma unroll
-                    for (int i = 0; i < 32; i += 8) pack8(c + i, v + i);
-                    scale_out(c, v);
-                }
-            }
-            tmem_wait_st();
-            fence_async_smem();
-            fence_before_sync();
-            named_sync(1, kGrp);
-            if (gt == 0) { mbar_arrive(r_ready); mbar_arrive(&g_free[b]); }
-        }
-        // the state it ends with
-        if (failed || !group_wait(r_done, (it & 1) ^ 1, 1, kGrp, warp == 0)) { failed = true; break; }
-        if (out) {
-            if (!group_wait(oi_done, (it & 1) ^ 1, 1, kGrp, warp == 0)) { failed = true; break; }     // the tile is free
-            if (mine) {
-                store_state<DX, DZ>(out, turned, 32 * warp, tr + 4096 * warp, tmem + TM_R + lane_off);
-                fence_async_smem();
-            }
-        }
-        }
-        if (failed && gt == 0) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
-    } else if (grp <= 2) {
-        // =================== B: Y~ ===================
-        // The whole y tile goes into registers as soon as it has landed, so that the next one is on its way while this
-        // one's parts are formed and while the R of the chunk before still reads the parts of its own.
-        constexpr int PER = DX / 8, IT = C * PER / kGrpB;    // 16-byte pieces of a row, pieces of a thread
-        const int bt = tid - kGrp, t0 = bt / PER, c = bt % PER;   // piece i: token t0 + i (kGrpB / PER), always column c
-        const uint32_t col = (uint32_t)(c >> 3) * kHalf;
-        const bool poll = warp == 4;
-        uint32_t it = 0;
-        HD_UNITS(w)
-        for (int j = 0; j < w.nchunk; ++j, ++it) {
-            const uint32_t b = it & 1, s = it % Ly::NZ;
-            const int n = w.rows(j);
-            if (!group_wait(full_y, b, 2, kGrpB, poll)) { failed = true; break; }
-            uint32_t u[IT][4];
-#pragma unroll
-            for (int i = 0; i < IT; ++i) lds128(sb + Ly::T_Y + col + swz(t0 + i * (kGrpB / PER), c & 7), u[i]);
-            // (the shared loads have completed when the barriers of the next waits are passed: their values are used behind)
-#pragma unroll
-            for (int i = 0; i < IT; ++i) asm volatile("" : "+r"(u[i][0]), "+r"(u[i][1]), "+r"(u[i][2]), "+r"(u[i][3]));
-            named_sync(2, kGrpB);
-            if (bt == 0) mbar_arrive(y_read);
-            if (!group_wait(&g_full[b], (it >> 1) & 1, 2, kGrpB, poll) || (it > 0 && !group_wait(r_half, b ^ 1, 2, kGrpB, poll)) ||
-                (n < C && !group_wait(&full_z[s], (it / Ly::NZ) & 1, 2, kGrpB, poll))) { failed = true; break; }
-            const GateBuf& g = gates[b];
-            // two halves of 64 tokens, so that the products of one run while the other is formed
-            auto half = [&](auto check, int h) {
-                constexpr int TS = kGrpB / PER, HI = IT / 2;     // tokens between two pieces, pieces of a half
-                float wt[HI];      // read ahead of the stores, which the compiler moves no load across
-#pragma unroll
-                for (int i = 0; i < HI; ++i) wt[i] = g.cf[t0 + (h * HI + i) * TS] * g.ce[(h * HI + i) * TS / 32];
-#pragma unroll
-                for (int i = 0; i < HI; ++i) {
-                    const int t = t0 + (h * HI + i) * TS;
-                    const uint32_t off = col + swz(t, c & 7);
-                    scale16<check.value>(u[h * HI + i], wt[i], t >= n, sb + Ly::T_YH + off, sb + Ly::T_YL + off);
-                }
-            };
-            if (n == C) half(std::false_type{}, 0);
-            else half(std::true_type{}, 0);
-            if (n < C) clear_rows<DZ>(sb + Ly::T_Z + s * Ly::ZB, n, bt, kGrpB);
-            fence_async_smem();
-            named_sync(2, kGrpB);
-            if (bt == 0) mbar_arrive(y_ready);
-            if (it > 0 && !group_wait(r_done, b ^ 1, 2, kGrpB, poll)) { failed = true; break; }
-            if (n == C) half(std::false_type{}, 1);
-            else half(std::true_type{}, 1);
-            fence_async_smem();
-            named_sync(2, kGrpB);
-            if (bt == 0) { mbar_arrive(y_rest); mbar_arrive(&g_free[b]); }
-        }
-        if (failed && bt == 0) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
-    } else if (grp == 3) {
-        // =================== C: P (thread = row) ===================
-        const int rw = warp & 3;       // row block
-        const bool poll = rw == 0;
-        uint32_t it = 0;
-        HD_UNITS(w)
-        for (int j = 0; j < w.nchunk; ++j, ++it) {
-            const bool rev = w.rev;
-            const float sgn = rev ? 1.f : -1.f;
-            const uint32_t b = it & 1;
-            const int n = w.rows(j);
-            if (!group_wait(&g_full[b], (it >> 1) & 1, 3, kGrp, poll) || !group_wait(d_done, b, 3, kGrp, poll)) { failed = true; break; }
-            const GateBuf& g = gates[b];
-            const float rc = g.rc[gt], row = ex2(rev ? g.bl[rw] - rc : rc);
-            // blocks of 32 columns, each packed in place: hi in its first 16 columns, lo in the others. The loops over
-            // blocks stay loops: unrolled, the roles' straight-line code outran the instruction cache (no_instruction
-            // was the largest stall, a chunk took 11.4 K cycles).
-#pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-                uint32_t h[16], l[16];
-                if (rev ? q < rw : q > rw) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) h[i] = l[i] = 0u;
-                } else {
-                    float v[32];
-                    tmem_ld32(tmem + TM_D + lane_off + 32 * q, v);
-                    if (q == rw) {
-                        const float2 s2 = make_float2(sgn, sgn), b2 = make_float2(-sgn * rc, -sgn * rc);
-                        const float4* col = reinterpret_cast<const float4*>(g.rc + 32 * q);
-#pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            const float4 cc = col[i >> 2];
-                            const float2 x = __ffma2_rn(make_float2(cc.x, cc.y), s2, b2), y = __ffma2_rn(make_float2(cc.z, cc.w), s2, b2);
-                            const float2 vx = __fmul2_rn(make_float2(v[i], v[i + 1]), make_float2(ex2(x.x), ex2(x.y)));
-                            const float2 vy = __fmul2_rn(make_float2(v[i + 2], v[i + 3]), make_float2(ex2(y.x), ex2(y.y)));
-                            v[i] = vx.x; v[i + 1] = vx.y; v[i + 2] = vy.x; v[i + 3] = vy.y;
+                            for (int i = 0; i < 32; ++i) v[i] = 0.f;
                         }
-                    } else {
-                        const float rf = row * g.f[rw][q];
-                        const float2 r2 = make_float2(rf, rf);
-                        const float4* col = reinterpret_cast<const float4*>(g.cf + 32 * q);
-#pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            const float4 cc = col[i >> 2];
-                            const float2 x = __fmul2_rn(make_float2(v[i], v[i + 1]), __fmul2_rn(make_float2(cc.x, cc.y), r2));
-                            const float2 y = __fmul2_rn(make_float2(v[i + 2], v[i + 3]), __fmul2_rn(make_float2(cc.z, cc.w), r2));
-                            v[i] = x.x; v[i + 1] = x.y; v[i + 2] = y.x; v[i + 3] = y.y;
-                        }
+                        tmem_st32_nowait(tmem + TM_R + lane_off + c, v);
                     }
-                    // columns that this row sees: up to its own token, or from it to the chunk's last
-                    if (q == rw || (rev && n < C)) {
-                        uint32_t seen = q == rw ? (rev ? ~0u << lane : ~0u >> (31 - lane)) : ~0u;
-                        if (rev && 32 * q + 31 >= n) seen &= 32 * q >= n ? 0u : ~0u >> (32 - (n - 32 * q));
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (!(seen & (1u << i))) v[i] = 0.f;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        if (SPLIT) split2(v[2 * i], v[2 * i + 1], h[i], l[i]);
-                        else h[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-                    }
+                    tmem_wait_st();
                 }
-                tmem_st16(tmem + TM_D + lane_off + 32 * q, h);
-                if (SPLIT) tmem_st16(tmem + TM_D + lane_off + 32 * q + 16, l);
-            }
-            tmem_wait_st();
-            fence_before_sync();
-            named_sync(3, kGrp);
-            if (gt == 0) { mbar_arrive(p_ready); mbar_arrive(&g_free[b]); }
-        }
-        if (failed && gt == 0) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
-    } else {
-        // =================== O: the outputs (thread = row) ===================
-        const int rw = warp & 3;
-        const bool poll = rw == 0;
-        bool storing = false;      // (thread 0) a store may still read the tile
-        uint32_t it = 0;
-        HD_UNITS(w) {
-        const Pass& p = *w.p;
-        const Segment& sg = w.sg;
-        const bool f32 = p.o_f32;
-        const long long ostep = p.ot, wstep = p.w.st;
-        char* obase = static_cast<char*>(p.o) + (sg.b * p.ob + sg.h * p.oh) * (f32 ? 4 : 2);
-        const __nv_bfloat16* wbase = SPLIT ? static_cast<const __nv_bfloat16*>(p.w.p) + sg.b * p.w.sb + (sg.h / p.w.div) * p.w.sh : nullptr;
-        float* dots = SPLIT ? p.dots + ((long long)sg.b * a.l.geo.H + sg.h) * a.l.geo.T : nullptr;
-        for (int j = 0; j < w.nchunk; ++j, ++it) {
-            const uint32_t b = it & 1;
-            const int n = w.rows(j);
-            if (!group_wait(&g_full[b], (it >> 1) & 1, 4, kGrp, poll)) { failed = true; break; }
-            const float rc = gates[b].rc[gt];
-            const float cx = ex2(w.rev ? gates[b].bl[rw] - rc : rc) * gates[b].re[rw];
-            if (storing) bulk_wait_read();
-            if (!group_wait(oi_done, b, 4, kGrp, poll)) { failed = true; break; }
-            if (gt == 0) mbar_arrive(&g_free[b]);     // every thread of the group has read its gates
-            if (!group_wait(op_done, b, 4, kGrp, poll)) { failed = true; break; }
-            const bool staged = Ly::STAGED && n == C && !f32;
-            const int t0 = sg.t0 + w.chunk(j) * C;
-            const bool live = gt < n;
-            const long long at = (t0 + gt) * ostep;
-            float dot = 0.f;
+                if (mine) {
 #pragma unroll 1
-            for (int c = 0; c < DZ; c += 32) {
-                float u[32], v[32];
-                tmem_ld32_pair(tmem + TM_OI + lane_off + c, tmem + TM_OP + lane_off + c, u, v);
+                    for (int c = 0; c < DZ; c += 32) {
+                        float v[32];
+                        tmem_ld32(tmem + TM_R + lane_off + c, v);
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                    const float2 x = __ffma2_rn(make_float2(u[i], u[i + 1]), make_float2(cx, cx), make_float2(v[i], v[i + 1]));
-                    v[i] = x.x; v[i + 1] = x.y;
-                }
-                if (staged) {
-#pragma unroll
-                    for (int i = 0; i < 32; i += 8)
-                        sts128(sb + Ly::T_O + (uint32_t)((c + i) >> 6) * kHalf + swz(gt, ((c + i) & 63) >> 3),
-                               pack_bf16(v[i], v[i + 1]), pack_bf16(v[i + 2], v[i + 3]), pack_bf16(v[i + 4], v[i + 5]),
-                               pack_bf16(v[i + 6], v[i + 7]));
-                } else if (live) {
-                    if (SPLIT) {
-                        const uint4* wp = reinterpret_cast<const uint4*>(wbase + (t0 + gt) * wstep + c);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint4 x = wp[i];
-                            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+                        for (int i = 0; i < 32; i += 8) {
+                            const uint32_t off = (uint32_t)((c + i) >> 6) * (DX * 128) + swz(row, ((c + i) & 63) >> 3);
+                            uint32_t h[4], l[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                dot = fmaf(__uint_as_float(xs[e] << 16), v[8 * i + 2 * e], dot);
-                                dot = fmaf(__uint_as_float(xs[e] & 0xFFFF0000u), v[8 * i + 2 * e + 1], dot);
+                                if (SPLIT) split2(v[i + 2 * e], v[i + 2 * e + 1], h[e], l[e]);
+                                else h[e] = pack_bf16(v[i + 2 * e], v[i + 2 * e + 1]);
+                            }
+                            sts128(tr + off, h[0], h[1], h[2], h[3]);
+                            if (SPLIT) sts128(tr + Ly::RB + off, l[0], l[1], l[2], l[3]);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            const float2 x = __fmul2_rn(make_float2(v[i], v[i + 1]), make_float2(en, en));
+                            v[i] = x.x; v[i + 1] = x.y;
+                        }
+                        tmem_st32_nowait(tmem + TM_R + lane_off + c, v);
+                    }
+                    tmem_wait_st();
+                }
+                fence_async_smem();
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) { mbar_arrive(r_ready); mbar_arrive(&g_free[b]); }
+                if ((flags & kLast) && dst) {       // the state it ends with
+                    if (!wait(oi_done, b) || !wait(r_done, b)) { failed = true; break; }
+                    if (mine) store_state<DX, DZ>(dst, turned, 32 * warp, turn, tmem + TM_R + lane_off);
+                }
+            } else if (grp == 3) {
+                // ---- C: P (thread = row)
+                if (!wait(d_done, b)) { failed = true; break; }
+                const float sgn = rev ? 1.f : -1.f;
+                const float rc = g.rc[row], rfac = ex2(rev ? g.bl[rw] - rc : rc);
+                // blocks of 32 columns, each packed in place: hi in its first 16 columns, lo in the others. The loops over
+                // blocks stay loops: unrolled, the roles' straight-line code outran the instruction cache (no_instruction
+                // was the largest stall, a chunk took 11.4 K cycles).
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t h[16], l[16];
+                    if (rev ? q < rw : q > rw) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) h[i] = l[i] = 0u;
+                    } else {
+                        float v[32];
+                        tmem_ld32(tmem + TM_D + lane_off + 32 * q, v);
+                        if (q == rw) {
+                            const float2 s2 = make_float2(sgn, sgn), b2 = make_float2(-sgn * rc, -sgn * rc);
+                            const float4* col = reinterpret_cast<const float4*>(g.rc + 32 * q);
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4) {
+                                const float4 cc = col[i >> 2];
+                                const float2 x = __ffma2_rn(make_float2(cc.x, cc.y), s2, b2), y = __ffma2_rn(make_float2(cc.z, cc.w), s2, b2);
+                                const float2 vx = __fmul2_rn(make_float2(v[i], v[i + 1]), make_float2(ex2(x.x), ex2(x.y)));
+                                const float2 vy = __fmul2_rn(make_float2(v[i + 2], v[i + 3]), make_float2(ex2(y.x), ex2(y.y)));
+                                v[i] = vx.x; v[i + 1] = vx.y; v[i + 2] = vy.x; v[i + 3] = vy.y;
+                            }
+                        } else {
+                            const float rf = rfac * g.f[rw][q];
+                            const float2 r2 = make_float2(rf, rf);
+                            const float4* col = reinterpret_cast<const float4*>(g.cf + 32 * q);
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4) {
+                                const float4 cc = col[i >> 2];
+                                const float2 x = __fmul2_rn(make_float2(v[i], v[i + 1]), __fmul2_rn(make_float2(cc.x, cc.y), r2));
+                                const float2 y = __fmul2_rn(make_float2(v[i + 2], v[i + 3]), __fmul2_rn(make_float2(cc.z, cc.w), r2));
+                                v[i] = x.x; v[i + 1] = x.y; v[i + 2] = y.x; v[i + 3] = y.y;
                             }
                         }
+                        // columns that this row sees: up to its own token, or from it to the chunk's last
+                        if (q == rw || (rev && n < C)) {
+                            uint32_t seen = q == rw ? (rev ? ~0u << lane : ~0u >> (31 - lane)) : ~0u;
+                            if (rev && 32 * q + 31 >= n) seen &= 32 * q >= n ? 0u : ~0u >> (32 - (n - 32 * q));
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (!(seen & (1u << i))) v[i] = 0.f;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            if (SPLIT) split2(v[2 * i], v[2 * i + 1], h[i], l[i]);
+                            else h[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+                        }
                     }
-                    if (f32) {
-                        float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(obase) + at + c);
+                    tmem_st16(tmem + TM_D + lane_off + 32 * q, h);
+                    if (SPLIT) tmem_st16(tmem + TM_D + lane_off + 32 * q + 16, l);
+                }
+                tmem_wait_st();
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) { mbar_arrive(p_ready); mbar_arrive(&g_free[b]); }
+            } else {
+                // ---- O: the outputs (thread = row)
+                const float rc = g.rc[row];
+                const float cx = ex2(rev ? g.bl[rw] - rc : rc) * g.re[rw];
+                const bool f32 = flags & kOutF32, staged = Ly::STAGED && n == C && !f32, live = row < n;
+                const int t0 = g.t0, hh = g.h, bb = g.b, pi = g.pass;
+                const long long at = (t0 + row) * g.ostep, wat = (t0 + row) * g.wstep;
+                char* obase = g.o;
+                const __nv_bfloat16* wv = g.w;
+                float* dots = g.dots;
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&g_free[b]);
+                    if (storing) bulk_wait_read();
+                }
+                if (!wait(oi_done, b) || !wait(op_done, b)) { failed = true; break; }
+                float dot = 0.f;
+#pragma unroll 1
+                for (int c = 0; c < DZ; c += 32) {
+                    float u[32], v[32];
+                    tmem_ld32_pair(tmem + TM_OI + lane_off + c, tmem + TM_OP + lane_off + c, u, v);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                    } else {
-                        uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(obase) + at + c);
+                    for (int i = 0; i < 32; i += 2) {
+                        const float2 x = __ffma2_rn(make_float2(u[i], u[i + 1]), make_float2(cx, cx), make_float2(v[i], v[i + 1]));
+                        v[i] = x.x; v[i + 1] = x.y;
+                    }
+                    if (staged) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            dst[i] = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
-                                                pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+                        for (int i = 0; i < 32; i += 8)
+                            sts128(sb + Ly::T_O + (uint32_t)((c + i) >> 6) * kHalf + swz(row, ((c + i) & 63) >> 3),
+                                   pack_bf16(v[i], v[i + 1]), pack_bf16(v[i + 2], v[i + 3]), pack_bf16(v[i + 4], v[i + 5]),
+                                   pack_bf16(v[i + 6], v[i + 7]));
+                    } else if (live) {
+                        if (SPLIT) {
+                            const uint4* wp = reinterpret_cast<const uint4*>(wv + wat + c);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint4 x = wp[i];
+                                const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    dot = fmaf(__uint_as_float(xs[e] << 16), v[8 * i + 2 * e], dot);
+                                    dot = fmaf(__uint_as_float(xs[e] & 0xFFFF0000u), v[8 * i + 2 * e + 1], dot);
+                                }
+                            }
+                        }
+                        if (f32) {
+                            float4* d = reinterpret_cast<float4*>(reinterpret_cast<float*>(obase) + at + c);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) d[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                        } else {
+                            uint4* d = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(obase) + at + c);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                d[i] = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                                                  pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+                        }
+                    }
+                }
+                if (SPLIT && live) dots[t0 + row] = dot;
+                if (staged) fence_async_smem();
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(o_free);
+                    if (staged) {     // the warp's 32 rows
+#pragma unroll
+                        for (int x = 0; x < DZ / 64; ++x)
+                            tma_store_4d(&a.map[pi][3], 64 * x, t0 + 32 * rw, hh, bb, sb + Ly::T_O + x * kHalf + 4096 * rw);
+                        bulk_commit();
+                        storing = true;
                     }
                 }
             }
-            if (SPLIT && live) dots[t0 + gt] = dot;
-            if (staged) fence_async_smem();
-            fence_before_sync();
-            named_sync(4, kGrp);
-            if (gt == 0) {
-                mbar_arrive(o_free);
-                if (staged) {
-#pragma unroll
-                    for (int x = 0; x < DZ / 64; ++x)
-                        tma_store_4d(&w.maps[3], 64 * x, t0, sg.h, sg.b, sb + Ly::T_O + x * kHalf);
-                    bulk_commit();
-                    storing = true;
-                }
-            }
-        }
         }
         if (storing) bulk_wait_all();
-        if (failed && gt == 0) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
+        if (failed && lane == 0) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
     }
     fence_before_sync();
     __syncthreads();
     if (warp == 0) tmem_dealloc(tmem, kTmemCols);
-#undef HD_UNITS
 }
 
-// A row sequence as [batch][head][token][feature]: boxes of 64 features x 128 tokens of one head.
-bool map_rows(CUtensorMap* m, const View& v, int D, long long T, int heads, int B) {
-    return tensor_map_rows(m, v.p, D, T, heads, B, v.st, v.sh, v.sb, C);
+// A row sequence as [batch][head][token][feature]: boxes of 64 features x `rows` tokens of one head.
+bool map_rows(CUtensorMap* m, const View& v, int D, long long T, int heads, int B, int rows = C) {
+    return tensor_map_rows(m, v.p, D, T, heads, B, v.st, v.sh, v.sb, rows);
 }
 
 template <int DX, int DZ, bool SPLIT, bool STATES>
@@ -955,7 +938,7 @@ cudaError_t launch_tc(const Launch& l, cudaStream_t s) {
             if (!map_rows(&a.map[k][1], p.y, p.DX, T, H / p.y.div, l.B)) return cudaErrorInvalidValue;
             if (!map_rows(&a.map[k][2], p.z, p.DZ, T, H / p.z.div, l.B)) return cudaErrorInvalidValue;
             if (!p.states_only && !p.o_f32 &&
-                !map_rows(&a.map[k][3], View{p.o, p.ob, p.oh, p.ot, 1}, p.DZ, T, H, l.B))
+                !map_rows(&a.map[k][3], View{p.o, p.ob, p.oh, p.ot, 1}, p.DZ, T, H, l.B, 32))
                 return cudaErrorInvalidValue;
         }
         a.total = (int)n * a.l.npass;
