@@ -132,24 +132,34 @@ __device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, int c0, int
 }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// 32 columns of two accumulators, both loads in flight at once.
-__device__ __forceinline__ void tmem_ld32_pair(uint32_t ta, uint32_t tb, float (&x)[32], float (&y)[32]) {
-    uint32_t r[64];
+// 16 columns of two accumulators, both loads in flight at once.
+__device__ __forceinline__ void tmem_ld16_pair(uint32_t ta, uint32_t tb, float (&x)[16], float (&y)[16]) {
+    uint32_t r[32];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
         uint32_t* q = r + 16 * i;
         asm volatile(
             "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
             : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3]), "=r"(q[4]), "=r"(q[5]), "=r"(q[6]), "=r"(q[7]), "=r"(q[8]),
               "=r"(q[9]), "=r"(q[10]), "=r"(q[11]), "=r"(q[12]), "=r"(q[13]), "=r"(q[14]), "=r"(q[15])
-            : "r"((i < 2 ? ta : tb) + 16 * (i & 1)));
+            : "r"(i ? tb : ta));
     }
-    // the wait takes the registers as operands, so that no use of them moves in front of it
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    // no use of the values moves in front of the wait
 #pragma unroll
-    for (int i = 0; i < 64; ++i) asm volatile("" : "+r"(r[i]));
+    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
 #pragma unroll
-    for (int i = 0; i < 32; ++i) { x[i] = __uint_as_float(r[i]); y[i] = __uint_as_float(r[32 + i]); }
+    for (int i = 0; i < 16; ++i) { x[i] = __uint_as_float(r[i]); y[i] = __uint_as_float(r[16 + i]); }
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory");
+}
+__device__ __forceinline__ void tmem_st16_nowait(uint32_t taddr, const float (&v)[16]) {
+    uint32_t r[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i]);
+    tmem_st16(taddr, r);
 }
 
 __device__ __forceinline__ void tmem_st32_nowait(uint32_t taddr, const float (&v)[32]) {
@@ -344,7 +354,9 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 23);
     GateBuf* gates = reinterpret_cast<GateBuf*>(smem + Ly::GATES);
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // (what is the same for a warp goes through a shuffle, which tells the compiler so: branches on it then cost no
+    // re-convergence, 100 cycles and more in a loop of a few hundred)
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int rw = warp & 3, row = tid & (kGrp - 1);     // a worker's 32 lanes of tensor memory, and this thread's
     const uint32_t lane_off = static_cast<uint32_t>(32 * rw) << 16;
     const long long wl = a.l.wait_cycles;
@@ -631,43 +643,42 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
             const GateBuf& g = gates[b];
             if (!STATES && (grp == 1 || grp == 2)) {
                 // ---- B1, B2: Y~ of 64 tokens
-                // Their part of the y tile goes into registers as soon as it has landed, so that the next one is on its
-                // way while this one's parts are formed and while the R of the chunk before still reads the parts of its own.
                 constexpr int PER = DX / 8, IT = C / 2 * PER / kGrp, TS = kGrp / PER;     // pieces of a row, of a thread; tokens between two
                 if (!wait(&g_full[b], (it >> 1) & 1)) { failed = true; break; }
-                if (g.flags & kEnd) break;
-                const int h = grp - 1, n = g.n, t0 = 64 * h + row / PER, c = row % PER;
-                const uint32_t col = (uint32_t)(c >> 3) * kHalf;
+                if (__shfl_sync(0xffffffffu, g.flags, 0) & kEnd) break;
+                const int h = grp - 1, n = __shfl_sync(0xffffffffu, g.n, 0), t0 = 64 * h + row / PER, c = row % PER;
+                const uint32_t off = (uint32_t)(c >> 3) * kHalf + swz(t0, c & 7);      // TS is a multiple of 8: the swizzle stays
+                // Their part of the y tile goes into registers as soon as it has landed, so that the next one is on its
+                // way while this one's parts are formed and while the R of the chunk before still reads the parts of its own.
                 if (!wait(full_y, b)) { failed = true; break; }
                 uint32_t u[IT][4];
 #pragma unroll
-                for (int i = 0; i < IT; ++i) lds128(sb + Ly::T_Y + col + swz(t0 + i * TS, c & 7), u[i]);
+                for (int i = 0; i < IT; ++i) lds128(sb + Ly::T_Y + off + i * TS * 128, u[i]);
+                float wt[IT];      // read ahead of the stores, which the compiler moves no load across
+#pragma unroll
+                for (int i = 0; i < IT; ++i) wt[i] = g.cf[t0 + i * TS] * g.ce[2 * h + i * TS / 32];
                 // (the shared loads have completed when their values are used)
 #pragma unroll
                 for (int i = 0; i < IT; ++i) asm volatile("" : "+r"(u[i][0]), "+r"(u[i][1]), "+r"(u[i][2]), "+r"(u[i][3]));
                 arrive(y_read);
-                float wt[IT];      // read ahead of the stores, which the compiler moves no load across
-#pragma unroll
-                for (int i = 0; i < IT; ++i) wt[i] = g.cf[t0 + i * TS] * g.ce[2 * h + i * TS / 32];
-                if ((it > 0 && !wait(h ? r_done : r_half, b ^ 1)) || (n < C && !wait(&full_z[s], zpar))) { failed = true; break; }
+                if (it > 0 && !wait(h ? r_done : r_half, b ^ 1)) { failed = true; break; }
                 if (n < C) {
+                    if (!wait(&full_z[s], zpar)) { failed = true; break; }
+                    clear_rows<DZ>(sb + Ly::T_Z + s * Ly::ZB, max(n, 64 * h), 64 * h + 64, row, kGrp);
 #pragma unroll
                     for (int i = 0; i < IT; ++i)
                         if (t0 + i * TS >= n) u[i][0] = u[i][1] = u[i][2] = u[i][3] = 0u, wt[i] = 0.f;
-                    clear_rows<DZ>(sb + Ly::T_Z + s * Ly::ZB, max(n, 64 * h), 64 * h + 64, row, kGrp);
                 }
 #pragma unroll
-                for (int i = 0; i < IT; ++i) {
-                    const uint32_t off = col + swz(t0 + i * TS, c & 7);
-                    scale16(u[i], wt[i], sb + Ly::T_YH + off, sb + Ly::T_YL + off);
-                }
+                for (int i = 0; i < IT; ++i)
+                    scale16(u[i], wt[i], sb + Ly::T_YH + off + i * TS * 128, sb + Ly::T_YL + off + i * TS * 128);
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) { mbar_arrive(h ? y_rest : y_ready); mbar_arrive(&g_free[b]); }
                 continue;
             }
             if (!wait(&g_full[b], (it >> 1) & 1)) { failed = true; break; }
-            const int flags = g.flags, n = g.n;
+            const int flags = __shfl_sync(0xffffffffu, g.flags, 0), n = __shfl_sync(0xffffffffu, g.n, 0);
             if (flags & kEnd) break;
             const bool rev = flags & kRev;
             if (STATES) {
@@ -707,12 +718,12 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                     tmem_wait_st();
                 }
                 if (mine) {
-#pragma unroll 1
-                    for (int c = 0; c < DZ; c += 32) {
-                        float v[32];
-                        tmem_ld32(tmem + TM_R + lane_off + c, v);
+#pragma unroll 2
+                    for (int c = 0; c < DZ; c += 16) {
+                        float v[16];
+                        tmem_ld16(tmem + TM_R + lane_off + c, v);
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8) {
+                        for (int i = 0; i < 16; i += 8) {
                             const uint32_t off = (uint32_t)((c + i) >> 6) * (DX * 128) + swz(row, ((c + i) & 63) >> 3);
                             uint32_t h[4], l[4];
 #pragma unroll
@@ -724,11 +735,11 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                             if (SPLIT) sts128(tr + Ly::RB + off, l[0], l[1], l[2], l[3]);
                         }
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
+                        for (int i = 0; i < 16; i += 2) {
                             const float2 x = __fmul2_rn(make_float2(v[i], v[i + 1]), make_float2(en, en));
                             v[i] = x.x; v[i + 1] = x.y;
                         }
-                        tmem_st32_nowait(tmem + TM_R + lane_off + c, v);
+                        tmem_st16_nowait(tmem + TM_R + lane_off + c, v);
                     }
                     tmem_wait_st();
                 }
@@ -745,57 +756,83 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                 if (!wait(d_done, b)) { failed = true; break; }
                 const float sgn = rev ? 1.f : -1.f;
                 const float rc = g.rc[row], rfac = ex2(rev ? g.bl[rw] - rc : rc);
-                // blocks of 32 columns, each packed in place: hi in its first 16 columns, lo in the others. The loops over
-                // blocks stay loops: unrolled, the roles' straight-line code outran the instruction cache (no_instruction
-                // was the largest stall, a chunk took 11.4 K cycles).
-#pragma unroll 1
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t h[16], l[16];
-                    if (rev ? q < rw : q > rw) {
+                // pieces of W columns, each block of 32 columns packed in place: hi in its first 16 columns, lo in the others
+                constexpr int W = SPLIT ? 32 : 16;
+                auto load = [&](int c0, float (&v)[W]) {
+                    if constexpr (SPLIT) tmem_ld32(tmem + TM_D + lane_off + c0, v);
+                    else tmem_ld16(tmem + TM_D + lane_off + c0, v);
+                };
+                auto store = [&](int c0, const float (&v)[W]) {
+                    uint32_t h[W / 2], l[W / 2];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) h[i] = l[i] = 0u;
-                    } else {
-                        float v[32];
-                        tmem_ld32(tmem + TM_D + lane_off + 32 * q, v);
-                        if (q == rw) {
-                            const float2 s2 = make_float2(sgn, sgn), b2 = make_float2(-sgn * rc, -sgn * rc);
-                            const float4* col = reinterpret_cast<const float4*>(g.rc + 32 * q);
-#pragma unroll
-                            for (int i = 0; i < 32; i += 4) {
-                                const float4 cc = col[i >> 2];
-                                const float2 x = __ffma2_rn(make_float2(cc.x, cc.y), s2, b2), y = __ffma2_rn(make_float2(cc.z, cc.w), s2, b2);
-                                const float2 vx = __fmul2_rn(make_float2(v[i], v[i + 1]), make_float2(ex2(x.x), ex2(x.y)));
-                                const float2 vy = __fmul2_rn(make_float2(v[i + 2], v[i + 3]), make_float2(ex2(y.x), ex2(y.y)));
-                                v[i] = vx.x; v[i + 1] = vx.y; v[i + 2] = vy.x; v[i + 3] = vy.y;
-                            }
-                        } else {
-                            const float rf = rfac * g.f[rw][q];
-                            const float2 r2 = make_float2(rf, rf);
-                            const float4* col = reinterpret_cast<const float4*>(g.cf + 32 * q);
-#pragma unroll
-                            for (int i = 0; i < 32; i += 4) {
-                                const float4 cc = col[i >> 2];
-                                const float2 x = __fmul2_rn(make_float2(v[i], v[i + 1]), __fmul2_rn(make_float2(cc.x, cc.y), r2));
-                                const float2 y = __fmul2_rn(make_float2(v[i + 2], v[i + 3]), __fmul2_rn(make_float2(cc.z, cc.w), r2));
-                                v[i] = x.x; v[i + 1] = x.y; v[i + 2] = y.x; v[i + 3] = y.y;
-                            }
-                        }
-                        // columns that this row sees: up to its own token, or from it to the chunk's last
-                        if (q == rw || (rev && n < C)) {
-                            uint32_t seen = q == rw ? (rev ? ~0u << lane : ~0u >> (31 - lane)) : ~0u;
-                            if (rev && 32 * q + 31 >= n) seen &= 32 * q >= n ? 0u : ~0u >> (32 - (n - 32 * q));
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (!(seen & (1u << i))) v[i] = 0.f;
-                        }
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            if (SPLIT) split2(v[2 * i], v[2 * i + 1], h[i], l[i]);
-                            else h[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-                        }
+                    for (int i = 0; i < W / 2; ++i) {
+                        if (SPLIT) split2(v[2 * i], v[2 * i + 1], h[i], l[i]);
+                        else h[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
                     }
-                    tmem_st16(tmem + TM_D + lane_off + 32 * q, h);
-                    if (SPLIT) tmem_st16(tmem + TM_D + lane_off + 32 * q + 16, l);
+                    const uint32_t at = tmem + TM_D + lane_off + (c0 & ~31);
+                    if constexpr (SPLIT) {
+                        tmem_st16(at, h);
+                        tmem_st16(at + 16, l);
+                    } else {
+                        tmem_st8(at + ((c0 & 16) >> 1), h);
+                    }
+                };
+                // of `seen` bits, one per column of the block, the others become zero
+                auto mask = [&](int c0, uint32_t seen, float (&v)[W]) {
+                    seen >>= c0 & 31;
+#pragma unroll
+                    for (int i = 0; i < W; ++i)
+                        if (!(seen & (1u << i))) v[i] = 0.f;
+                };
+                const int here = 32 * rw;
+                // blocks that the rows see whole
+#pragma unroll 1
+                for (int c0 = rev ? here + 32 : 0; c0 < (rev ? C : here); c0 += W) {
+                    const float rf = rfac * g.f[rw][c0 >> 5];
+                    const float2 r2 = make_float2(rf, rf);
+                    const float4* col = reinterpret_cast<const float4*>(g.cf + c0);
+                    float v[W];
+                    load(c0, v);
+#pragma unroll
+                    for (int i = 0; i < W; i += 4) {
+                        const float4 cc = col[i >> 2];
+                        const float2 x = __fmul2_rn(make_float2(v[i], v[i + 1]), __fmul2_rn(make_float2(cc.x, cc.y), r2));
+                        const float2 y = __fmul2_rn(make_float2(v[i + 2], v[i + 3]), __fmul2_rn(make_float2(cc.z, cc.w), r2));
+                        v[i] = x.x; v[i + 1] = x.y; v[i + 2] = y.x; v[i + 3] = y.y;
+                    }
+                    if (rev && n < C) {     // up to the chunk's last token
+                        const int left = n - (c0 & ~31);
+                        mask(c0, left <= 0 ? 0u : left >= 32 ? ~0u : ~0u >> (32 - left), v);
+                    }
+                    store(c0, v);
+                }
+                // their own block: up to their own token, or from it to the chunk's last
+#pragma unroll 1
+                for (int c0 = here; c0 < here + 32; c0 += W) {
+                    const float2 s2 = make_float2(sgn, sgn), b2 = make_float2(-sgn * rc, -sgn * rc);
+                    const float4* col = reinterpret_cast<const float4*>(g.rc + c0);
+                    float v[W];
+                    load(c0, v);
+#pragma unroll
+                    for (int i = 0; i < W; i += 4) {
+                        const float4 cc = col[i >> 2];
+                        const float2 x = __ffma2_rn(make_float2(cc.x, cc.y), s2, b2), y = __ffma2_rn(make_float2(cc.z, cc.w), s2, b2);
+                        const float2 vx = __fmul2_rn(make_float2(v[i], v[i + 1]), make_float2(ex2(x.x), ex2(x.y)));
+                        const float2 vy = __fmul2_rn(make_float2(v[i + 2], v[i + 3]), make_float2(ex2(y.x), ex2(y.y)));
+                        v[i] = vx.x; v[i + 1] = vx.y; v[i + 2] = vy.x; v[i + 3] = vy.y;
+                    }
+                    uint32_t seen = rev ? ~0u << lane : ~0u >> (31 - lane);
+                    if (rev && n - here < 32) seen &= n <= here ? 0u : ~0u >> (32 - (n - here));
+                    mask(c0, seen, v);
+                    store(c0, v);
+                }
+                // and blocks that they do not see
+#pragma unroll 1
+                for (int c0 = rev ? 0 : here + 32; c0 < (rev ? here : C); c0 += W) {
+                    float v[W];
+#pragma unroll
+                    for (int i = 0; i < W; ++i) v[i] = 0.f;
+                    store(c0, v);
                 }
                 tmem_wait_st();
                 fence_before_sync();
@@ -817,27 +854,37 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                     if (storing) bulk_wait_read();
                 }
                 if (!wait(oi_done, b) || !wait(op_done, b)) { failed = true; break; }
-                float dot = 0.f;
-#pragma unroll 1
-                for (int c = 0; c < DZ; c += 32) {
-                    float u[32], v[32];
-                    tmem_ld32_pair(tmem + TM_OI + lane_off + c, tmem + TM_OP + lane_off + c, u, v);
+                auto values = [&](int c, float (&v)[16]) {       // columns c .. c + 15 of o
+                    float u[16];
+                    tmem_ld16_pair(tmem + TM_OI + lane_off + c, tmem + TM_OP + lane_off + c, u, v);
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
+                    for (int i = 0; i < 16; i += 2) {
                         const float2 x = __ffma2_rn(make_float2(u[i], u[i + 1]), make_float2(cx, cx), make_float2(v[i], v[i + 1]));
                         v[i] = x.x; v[i + 1] = x.y;
                     }
-                    if (staged) {
+                };
+                if (staged) {
+#pragma unroll 2
+                    for (int c = 0; c < DZ; c += 16) {
+                        float v[16];
+                        values(c, v);
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8)
+                        for (int i = 0; i < 16; i += 8)
                             sts128(sb + Ly::T_O + (uint32_t)((c + i) >> 6) * kHalf + swz(row, ((c + i) & 63) >> 3),
                                    pack_bf16(v[i], v[i + 1]), pack_bf16(v[i + 2], v[i + 3]), pack_bf16(v[i + 4], v[i + 5]),
                                    pack_bf16(v[i + 6], v[i + 7]));
-                    } else if (live) {
+                    }
+                } else {
+                    float dot = 0.f;
+#pragma unroll 1
+                    for (int c = 0; c < DZ; c += 16) {
+                        float v[16];
+                        values(c, v);
+                        if (!live) continue;
                         if (SPLIT) {
                             const uint4* wp = reinterpret_cast<const uint4*>(wv + wat + c);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
+                            for (int i = 0; i < 2; ++i) {
                                 const uint4 x = wp[i];
                                 const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -850,17 +897,17 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                         if (f32) {
                             float4* d = reinterpret_cast<float4*>(reinterpret_cast<float*>(obase) + at + c);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) d[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                            for (int i = 0; i < 4; ++i) d[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
                         } else {
                             uint4* d = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(obase) + at + c);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
+                            for (int i = 0; i < 2; ++i)
                                 d[i] = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
                                                   pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
                         }
                     }
+                    if (SPLIT && live) dots[t0 + row] = dot;
                 }
-                if (SPLIT && live) dots[t0 + row] = dot;
                 if (staged) fence_async_smem();
                 fence_before_sync();
                 __syncwarp();
