@@ -20,18 +20,16 @@ constexpr int TH = 256;   // threads
 constexpr int C = 32;     // tokens of a chunk
 constexpr int LDP = C + 4;
 
-template <class T> struct Vec;
+template <class T> struct Vec;     // 16 bytes of a type
 template <> struct Vec<float> {
     static constexpr int N = 4;
-    static __device__ __forceinline__ void load(const float* p, float* d) {
-        const float4 v = *reinterpret_cast<const float4*>(p);
-        d[0] = v.x; d[1] = v.y; d[2] = v.z; d[3] = v.w;
+    static __device__ __forceinline__ void unpack(uint4 v, float* d) {
+        d[0] = __uint_as_float(v.x); d[1] = __uint_as_float(v.y); d[2] = __uint_as_float(v.z); d[3] = __uint_as_float(v.w);
     }
 };
 template <> struct Vec<__nv_bfloat16> {
     static constexpr int N = 8;
-    static __device__ __forceinline__ void load(const __nv_bfloat16* p, float* d) {
-        const uint4 v = *reinterpret_cast<const uint4*>(p);
+    static __device__ __forceinline__ void unpack(uint4 v, float* d) {
         const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -43,25 +41,33 @@ template <> struct Vec<__nv_bfloat16> {
 
 __device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
-// Rows t0 .. t0 + C - 1 of a row sequence (features c0 .. c0 + D - 1) as fp32 into shared memory; rows from n on are 0.
+// C rows of a row sequence (D features) on their way through registers: 16 bytes a piece, pieces spread over the threads.
+// take() starts the loads of the rows t .. t + n - 1 (the others are zero), put() writes them as fp32 to shared memory.
 template <class IT, int D, int LD>
-__device__ __forceinline__ void load_rows(float* dst, const View& v, int b, int h, long long t0, int n, int c0) {
-    constexpr int N = Vec<IT>::N, PER = D / N;
-    const IT* base = static_cast<const IT*>(v.p) + b * v.sb + (h / v.div) * v.sh + t0 * v.st + c0;
-    for (int i = threadIdx.x; i < C * PER; i += TH) {
-        const int r = i / PER, c = (i % PER) * N;
-        float d[N];
-        if (r < n) {
-            Vec<IT>::load(base + r * v.st + c, d);
-        } else {
+struct Rows {
+    static constexpr int N = Vec<IT>::N, PER = D / N, M = (C * PER + TH - 1) / TH;
+    uint4 r[M];
+    __device__ __forceinline__ void take(const IT* base, long long step, long long t, int n) {
 #pragma unroll
-            for (int e = 0; e < N; ++e) d[e] = 0.f;
+        for (int m = 0; m < M; ++m) {
+            const int i = threadIdx.x + m * TH, row = i / PER;
+            r[m] = make_uint4(0u, 0u, 0u, 0u);
+            if (row < n) r[m] = *reinterpret_cast<const uint4*>(base + (t + row) * step + (i % PER) * N);
         }
-#pragma unroll
-        for (int e = 0; e < N; e += 4)
-            *reinterpret_cast<float4*>(dst + r * LD + c + e) = make_float4(d[e], d[e + 1], d[e + 2], d[e + 3]);
     }
-}
+    __device__ __forceinline__ void put(float* dst) const {
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            const int i = threadIdx.x + m * TH, row = i / PER, c = (i % PER) * N;
+            if (C * PER % TH != 0 && row >= C) break;
+            float d[N];
+            Vec<IT>::unpack(r[m], d);
+#pragma unroll
+            for (int e = 0; e < N; e += 4)
+                *reinterpret_cast<float4*>(dst + row * LD + c + e) = make_float4(d[e], d[e + 1], d[e + 2], d[e + 3]);
+        }
+    }
+};
 
 template <class IT>
 __device__ __forceinline__ void store4(void* p, long long at, const float (&v)[4], bool f32) {
@@ -109,17 +115,35 @@ __device__ __forceinline__ void segment_pass(const Pass& p, const Geometry& geo,
     float gsum = 0.f;
     const float* gp = p.g + sg.b * p.gb + sg.h * p.gh;
     const int nchunk = (sg.n + C - 1) / C;
+    // the next chunk's rows and gates are on their way while one is computed
+    auto head = [&](const View& v) { return static_cast<const IT*>(v.p) + sg.b * v.sb + (sg.h / v.div) * v.sh; };
+    const IT *xp = so ? nullptr : head(p.x), *yp = head(p.y), *zp = head(p.z) + z0;
+    const long long xs = p.x.st, ys = p.y.st, zs = p.z.st, gs = p.gt;
+    Rows<IT, DX, LDX> xr, yr;
+    Rows<IT, NZ, LDZ> zr;
+    float gr = 0.f;
+    auto take = [&](int jj) {
+        const int j = rev ? nchunk - 1 - jj : jj;
+        const long long t = (long long)sg.t0 + j * C;
+        const int n = min(C, sg.n - j * C);
+        if (!so) xr.take(xp, xs, t, n);
+        yr.take(yp, ys, t, n);
+        zr.take(zp, zs, t, n);
+        gr = tid < n ? gp[(t + tid) * gs] : 0.f;      // (n <= 32)
+    };
+    take(0);
     for (int jj = 0; jj < nchunk; ++jj) {
         const int j = rev ? nchunk - 1 - jj : jj;
         const long long t0 = (long long)sg.t0 + j * C;
         const int n = min(C, sg.n - j * C);
         __syncthreads();
-        if (!so) load_rows<IT, DX, LDX>(X, p.x, sg.b, sg.h, t0, n, 0);
-        load_rows<IT, DX, LDX>(Y, p.y, sg.b, sg.h, t0, n, 0);
-        load_rows<IT, NZ, LDZ>(Z, p.z, sg.b, sg.h, t0, n, z0);
+        if (!so) xr.put(X);
+        yr.put(Y);
+        zr.put(Z);
+        const float graw = gr;
+        if (jj + 1 < nchunk) take(jj + 1);
         if (tid < 32) {
-            float g0 = tid < n ? gp[(t0 + tid) * p.gt] : 0.f;
-            g0 = g0 < kMinGate ? kMinGate : g0;
+            const float g0 = graw < kMinGate ? kMinGate : graw;
             double g = g0;      // sums in 64 bits: after a gate of -100 those between later tokens still count
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
@@ -186,18 +210,35 @@ __device__ __forceinline__ void segment_pass(const Pass& p, const Geometry& geo,
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[q][e] *= cx;
             }
+            // tokens that a row does not see may hold anything: they are left out, not multiplied by zero. First those that
+            // all of the thread's rows see, then the few between its rows.
+            {
+                const int lo = rev ? OR * rg + OR - 1 : 0, hi = rev ? C : OR * rg + 1;
+                const float* Pr = P + OR * rg * LDP;
 #pragma unroll 4
-            for (int u = 0; u < C; ++u) {
-                const float4 z = ld4(Z + u * LDZ + c0);
+                for (int u = lo; u < hi; ++u) {
+                    const float4 z = ld4(Z + u * LDZ + c0);
 #pragma unroll
-                for (int q = 0; q < OR; ++q) {
-                    const int rr = OR * rg + q;
-                    if (rev ? u >= rr : u <= rr) {      // a token that is not seen may hold anything
-                        const float w = P[rr * LDP + u];
+                    for (int q = 0; q < OR; ++q) {
+                        const float w = Pr[q * LDP + u];
                         o[q][0] = fmaf(w, z.x, o[q][0]);
                         o[q][1] = fmaf(w, z.y, o[q][1]);
                         o[q][2] = fmaf(w, z.z, o[q][2]);
                         o[q][3] = fmaf(w, z.w, o[q][3]);
+                    }
+                }
+#pragma unroll
+                for (int k = 1; k < OR; ++k) {        // forward: token OR rg + k, seen by rows k ..; backward: token
+                    const int u = rev ? OR * rg + OR - 1 - k : OR * rg + k;      // OR rg + OR - 1 - k, by rows 0 .. OR - 1 - k
+                    const float4 z = ld4(Z + u * LDZ + c0);
+#pragma unroll
+                    for (int q = 0; q < OR; ++q) {
+                        const bool in = rev ? q <= OR - 1 - k : q >= k;
+                        const float w = Pr[q * LDP + u];
+                        o[q][0] = in ? fmaf(w, z.x, o[q][0]) : o[q][0];
+                        o[q][1] = in ? fmaf(w, z.y, o[q][1]) : o[q][1];
+                        o[q][2] = in ? fmaf(w, z.z, o[q][2]) : o[q][2];
+                        o[q][3] = in ? fmaf(w, z.w, o[q][3]) : o[q][3];
                     }
                 }
             }
@@ -230,17 +271,28 @@ __device__ __forceinline__ void segment_pass(const Pass& p, const Geometry& geo,
                 const float4 s = ld4(S + (SR * rg + q) * LDZ + c0);
                 a[q][0] = e * s.x; a[q][1] = e * s.y; a[q][2] = e * s.z; a[q][3] = e * s.w;
             }
-            for (int u = 0; u < n; ++u) {
+#pragma unroll 4
+            for (int u = 0; u < C; ++u) {      // (rows behind the last token are zero)
                 const float w = W[u];
                 float4 z = ld4(Z + u * LDZ + c0);
                 z.x *= w; z.y *= w; z.z *= w; z.w *= w;
+                float y[SR];
+                if constexpr (SR % 4 == 0) {
+#pragma unroll
+                    for (int q = 0; q < SR; q += 4) {
+                        const float4 v = ld4(Y + u * LDX + SR * rg + q);
+                        y[q] = v.x; y[q + 1] = v.y; y[q + 2] = v.z; y[q + 3] = v.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int q = 0; q < SR; ++q) y[q] = Y[u * LDX + SR * rg + q];
+                }
 #pragma unroll
                 for (int q = 0; q < SR; ++q) {
-                    const float y = Y[u * LDX + SR * rg + q];
-                    a[q][0] = fmaf(y, z.x, a[q][0]);
-                    a[q][1] = fmaf(y, z.y, a[q][1]);
-                    a[q][2] = fmaf(y, z.z, a[q][2]);
-                    a[q][3] = fmaf(y, z.w, a[q][3]);
+                    a[q][0] = fmaf(y[q], z.x, a[q][0]);
+                    a[q][1] = fmaf(y[q], z.y, a[q][1]);
+                    a[q][2] = fmaf(y[q], z.z, a[q][2]);
+                    a[q][3] = fmaf(y[q], z.w, a[q][3]);
                 }
             }
 #pragma unroll
