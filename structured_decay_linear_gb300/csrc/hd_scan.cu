@@ -13,18 +13,15 @@ namespace {
 // of the contributions do not depend on the chain, so four are in flight at a time.
 constexpr int kAhead = 4;
 
-__global__ void __launch_bounds__(256) hd_scan_kernel(const __grid_constant__ Scan a) {
+__device__ __forceinline__ void scan_row(const Scan& a, int row, int at, bool back) {
     const long long size = (long long)a.dk * a.dv;
-    const int at = (blockIdx.y * 256 + threadIdx.x) * 4;
-    if (at >= size) return;
-    const bool back = a.fwd == nullptr || blockIdx.z == 1;
     float* W = back ? a.bwd : a.fwd;
     const float* ext = back ? a.bwd_ext : a.fwd_ext;
     long long base, step, eidx;
     int nseg;
     bool fresh = false;
     if (a.geo.blocks) {
-        const int r = blockIdx.x / a.geo.H, h = blockIdx.x % a.geo.H;
+        const int r = row / a.geo.H, h = row % a.geo.H;
         const int b0 = a.geo.block_starts[r];
         nseg = a.geo.block_starts[r + 1] - b0;
         if (nseg < 2) return;
@@ -36,9 +33,9 @@ __global__ void __launch_bounds__(256) hd_scan_kernel(const __grid_constant__ Sc
         fresh = a.geo.context[r] == 0;
     } else {
         nseg = a.geo.nseg;
-        base = (long long)blockIdx.x * (nseg + 1);
+        base = (long long)row * (nseg + 1);
         step = 1;
-        eidx = blockIdx.x;
+        eidx = row;
     }
     float4 cur = make_float4(0.f, 0.f, 0.f, 0.f);
     if (ext && !fresh) cur = *reinterpret_cast<const float4*>(ext + eidx * size + at);
@@ -69,6 +66,12 @@ __global__ void __launch_bounds__(256) hd_scan_kernel(const __grid_constant__ Sc
     }
 }
 
+__global__ void __launch_bounds__(256) hd_scan_kernel(const __grid_constant__ Scan a, int rows) {
+    const int at = (blockIdx.y * 256 + threadIdx.x) * 4;
+    if (at >= a.dk * a.dv) return;
+    for (int row = blockIdx.x; row < rows; row += gridDim.x) scan_row(a, row, at, a.fwd == nullptr || blockIdx.z == 1);
+}
+
 // ---- the gradient of the log-gates: one CTA per segment of one (batch, head)
 __global__ void __launch_bounds__(256) hd_gate_grad_kernel(const __grid_constant__ GateGrad a) {
     __shared__ double part[8];
@@ -79,8 +82,9 @@ __global__ void __launch_bounds__(256) hd_gate_grad_kernel(const __grid_constant
     const int t0 = seg * a.L, n = min(a.L, a.T - t0);
     const long long size = (long long)a.dk * a.dv, all = (long long)a.B * a.H * a.T;
     const bool last = seg == a.nseg - 1;
-    // <S, dS> at the segment's end
-    double d = 0.0;
+    // <S, dS> at the segment's end: fp32 over a thread's products and a warp, 64 bits across warps (fp64 throughout took
+    // three times as long as the bytes)
+    float d = 0.f;
     if (!last || a.last_end) {
         const float *S, *R;
         if (a.fwd) {
@@ -90,10 +94,14 @@ __global__ void __launch_bounds__(256) hd_gate_grad_kernel(const __grid_constant
             S = a.S_T + bh * size;
             R = a.dST + bh * size;
         }
+        float e[4] = {};
+#pragma unroll 4
         for (int i = 4 * tid; i < size; i += 1024) {
             const float4 x = *reinterpret_cast<const float4*>(S + i), y = *reinterpret_cast<const float4*>(R + i);
-            d += (double)(x.x * y.x + x.y * y.y) + (double)(x.z * y.z + x.w * y.w);
+            e[0] = fmaf(x.x, y.x, e[0]); e[1] = fmaf(x.y, y.y, e[1]);
+            e[2] = fmaf(x.z, y.z, e[2]); e[3] = fmaf(x.w, y.w, e[3]);
         }
+        d = (e[0] + e[1]) + (e[2] + e[3]);
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
@@ -106,27 +114,28 @@ __global__ void __launch_bounds__(256) hd_gate_grad_kernel(const __grid_constant
     double total = 0.0;
     for (int hi = n; hi > 0; hi -= 256) {
         const int i = hi - 1 - tid;            // thread 0 takes the last token
-        double x = 0.0;
+        float x = 0.f;
         const long long t = bh * a.T + t0 + i;
         if (i >= 0) {
-            for (int z = 0; z < a.nq; ++z) x += (double)a.dq_dots[z * all + t];
-            for (int z = 0; z < a.nk; ++z) x -= (double)a.dk_dots[z * all + t];
+            for (int z = 0; z < a.nq; ++z) x += a.dq_dots[z * all + t];
+            for (int z = 0; z < a.nk; ++z) x -= a.dk_dots[z * all + t];
         }
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const double y = __shfl_up_sync(0xffffffffu, x, off);
+            const float y = __shfl_up_sync(0xffffffffu, x, off);
             if (lane >= off) x += y;
         }
         __syncthreads();
         if (lane == 31) part[warp] = x;
         __syncthreads();
-        for (int w = 0; w < warp; ++w) x += part[w];
-        x += carry;
+        double before = carry;
+        for (int w = 0; w < warp; ++w) before += part[w];
+        const double sum = before + (double)x;
         if (i >= 0) {
-            if (a.dg_token) a.dg_token[t] = (float)x;
-            total += x;
+            if (a.dg_token) a.dg_token[t] = (float)sum;
+            total += sum;
         }
-        if (tid == 255) carry_s = x;
+        if (tid == 255) carry_s = sum;
         __syncthreads();
         carry = carry_s;
     }
@@ -186,7 +195,10 @@ cudaError_t launch_scan(const Scan& a, cudaStream_t s) {
     const long long rows = a.geo.blocks ? (long long)a.R * a.geo.H : (long long)a.B * a.geo.H;
     if (rows == 0) return cudaSuccess;
     const unsigned gy = (unsigned)((a.dk * a.dv / 4 + 255) / 256), gz = a.fwd && a.bwd ? 2 : 1;
-    hd_scan_kernel<<<dim3((unsigned)rows, gy, gz), 256, 0, s>>>(a);
+    // a ragged batch's rows are mostly of one block, with nothing to do: few CTAs walk them (1600 rows of which none had
+    // anything to do took 16 us as CTAs of their own)
+    const long long most = a.geo.blocks ? 64 : rows;
+    hd_scan_kernel<<<dim3((unsigned)(rows < most ? rows : most), gy, gz), 256, 0, s>>>(a, (int)rows);
     return cudaGetLastError();
 }
 

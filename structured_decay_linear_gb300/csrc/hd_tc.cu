@@ -385,6 +385,13 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
         fence_after_sync();
         return ok;
     };
+    // Gives back a buffer that the warp's lanes have read: `seen` is formed from all that each lane loaded. Shared loads and
+    // barrier arrivals take different ways, so an arrival issued behind a load may be seen before the load has read; the
+    // vote waits for every lane's values, and which lane arrives depends on it.
+    auto give_back = [&](uint64_t* bar, uint32_t seen) {
+        const int who = __any_sync(0xffffffffu, seen == 0x9e3779b9u) ? 1 : 0;
+        if (lane == who) mbar_arrive(bar);
+    };
     // Hands on what the warp's lanes have written.
     auto arrive = [&](uint64_t* bar) {
         __syncwarp();
@@ -491,8 +498,8 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                 const uint32_t tz = sb + Ly::T_Z + s * Ly::ZB;
                 if (!wait1(&g_full[par], (it >> 1) & 1)) { failed = true; break; }
                 const int flags = gates[par].flags;
-                mbar_arrive(&g_free[par]);
                 if (flags & kEnd) break;
+                mbar_arrive(&g_free[par]);       // (behind the branch: the load has returned)
                 if (STATES) {
                     if (!wait1(y_ready, par) || !wait1(&full_z[s], zpar)) { failed = true; break; }
                     mma_R(tz, 0, !(flags & kFirst));
@@ -657,10 +664,10 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                 float wt[IT];      // read ahead of the stores, which the compiler moves no load across
 #pragma unroll
                 for (int i = 0; i < IT; ++i) wt[i] = g.cf[t0 + i * TS] * g.ce[2 * h + i * TS / 32];
-                // (the shared loads have completed when their values are used)
+                uint32_t seen = 0;
 #pragma unroll
-                for (int i = 0; i < IT; ++i) asm volatile("" : "+r"(u[i][0]), "+r"(u[i][1]), "+r"(u[i][2]), "+r"(u[i][3]));
-                arrive(y_read);
+                for (int i = 0; i < IT; ++i) seen ^= (u[i][0] ^ u[i][1]) ^ (u[i][2] ^ u[i][3]);
+                give_back(y_read, seen);
                 if (it > 0 && !wait(h ? r_done : r_half, b ^ 1)) { failed = true; break; }
                 if (n < C) {
                     if (!wait(&full_z[s], zpar)) { failed = true; break; }
@@ -689,8 +696,8 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                 float* dst = g.dst;
                 fence_async_smem();
                 fence_before_sync();      // (the state of the unit before has been read)
-                __syncwarp();
-                if (lane == 0) { mbar_arrive(y_ready); mbar_arrive(&g_free[b]); }
+                arrive(y_ready);
+                give_back(&g_free[b], (uint32_t)(uintptr_t)dst);
                 if ((flags & kLast) && grp == 0 && (DX == 128 || warp < 2)) {
                     if (!wait(r_done, b)) { failed = true; break; }
                     store_state<DX, DZ>(dst, flags & kTurned, 32 * warp, turn, tmem + TM_R + lane_off);
@@ -745,8 +752,8 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                 }
                 fence_async_smem();
                 fence_before_sync();
-                __syncwarp();
-                if (lane == 0) { mbar_arrive(r_ready); mbar_arrive(&g_free[b]); }
+                arrive(r_ready);
+                give_back(&g_free[b], (uint32_t)(uintptr_t)dst);
                 if ((flags & kLast) && dst) {       // the state it ends with
                     if (!wait(oi_done, b) || !wait(r_done, b)) { failed = true; break; }
                     if (mine) store_state<DX, DZ>(dst, turned, 32 * warp, turn, tmem + TM_R + lane_off);
@@ -848,14 +855,22 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                 char* obase = g.o;
                 const __nv_bfloat16* wv = g.w;
                 float* dots = g.dots;
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&g_free[b]);
-                    if (storing) bulk_wait_read();
+                give_back(&g_free[b], __float_as_uint(cx) ^ (uint32_t)t0 ^ (uint32_t)hh ^ (uint32_t)bb ^ (uint32_t)pi ^ (uint32_t)at ^
+                                          (uint32_t)wat ^ (uint32_t)(uintptr_t)obase ^ (uint32_t)(uintptr_t)wv ^
+                                          (uint32_t)(uintptr_t)dots);
+                if (lane == 0 && storing) bulk_wait_read();
+                // the rows of the dots, kWAhead pieces of 16 columns ahead (waited for one by one they took 8 K cycles a chunk)
+                constexpr int kWAhead = 3;
+                const uint4* wp = reinterpret_cast<const uint4*>(wv + wat);
+                uint4 wq[2 * kWAhead];
+                if (SPLIT && live) {
+#pragma unroll
+                    for (int i = 0; i < 2 * kWAhead; ++i) wq[i] = wp[i];
                 }
                 if (!wait(oi_done, b) || !wait(op_done, b)) { failed = true; break; }
                 auto values = [&](int c, float (&v)[16]) {       // columns c .. c + 15 of o
                     float u[16];
+                    __syncwarp();        // (dead rows come from another way: these loads are the whole warp's)
                     tmem_ld16_pair(tmem + TM_OI + lane_off + c, tmem + TM_OP + lane_off + c, u, v);
 #pragma unroll
                     for (int i = 0; i < 16; i += 2) {
@@ -876,17 +891,17 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                     }
                 } else {
                     float dot = 0.f;
-#pragma unroll 1
+#pragma unroll (SPLIT ? DZ / 16 : 1)
                     for (int c = 0; c < DZ; c += 16) {
                         float v[16];
                         values(c, v);
                         if (!live) continue;
-                        if (SPLIT) {
-                            const uint4* wp = reinterpret_cast<const uint4*>(wv + wat + c);
+                        if constexpr (SPLIT) {
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
-                                const uint4 x = wp[i];
-                                const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+                                const int k = (c / 16 % kWAhead) * 2 + i;
+                                const uint32_t xs[4] = {wq[k].x, wq[k].y, wq[k].z, wq[k].w};
+                                if (c + 16 * kWAhead < DZ) wq[k] = wp[c / 8 + 2 * kWAhead + i];
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) {
                                     dot = fmaf(__uint_as_float(xs[e] << 16), v[8 * i + 2 * e], dot);
