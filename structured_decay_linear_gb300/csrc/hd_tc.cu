@@ -85,7 +85,7 @@ struct alignas(16) GateBuf {
     float* dots;        // the head's
     long long ostep, wstep;
 };
-enum : int { kFirst = 1, kLast = 2, kRev = 4, kTurned = 8, kOutF32 = 16, kEnd = 32 };
+enum : int { kFirst = 1, kLast = 2, kRev = 4, kTurned = 8, kOutF32 = 16, kEnd = 32, kWide = 64 };   // kWide: rows of o and w on 32 bytes
 static_assert(sizeof(GateBuf) % 16 == 0, "16-byte rows");
 
 template <int DX, int DZ, bool SPLIT, bool STATES>
@@ -150,6 +150,15 @@ __device__ __forceinline__ void tmem_ld16_pair(uint32_t ta, uint32_t tb, float (
     for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
 #pragma unroll
     for (int i = 0; i < 16; ++i) { x[i] = __uint_as_float(r[i]); y[i] = __uint_as_float(r[16 + i]); }
+}
+// 32 bytes at once (addresses on 32 bytes): rows apart, a lane's access is then a whole sector.
+__device__ __forceinline__ void ldg256(const void* p, uint4& x, uint4& y) {
+    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w), "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w) : "l"(p));
+}
+__device__ __forceinline__ void stg256(void* p, uint4 x, uint4 y) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 :: "l"(p), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w) : "memory");
 }
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
@@ -564,7 +573,8 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
             const __nv_bfloat16* wv = SPLIT ? static_cast<const __nv_bfloat16*>(p.w.p) + w.sg.b * p.w.sb + (w.sg.h / p.w.div) * p.w.sh : nullptr;
             float* dots = SPLIT ? p.dots + ((long long)w.sg.b * a.l.geo.H + w.sg.h) * a.l.geo.T : nullptr;
             float* gsum = STATES && p.gsum ? p.gsum + w.sg.entry : nullptr;
-            const int kind = (rev ? kRev : 0) | (p.siz != 1 ? kTurned : 0) | (p.o_f32 ? kOutF32 : 0);
+            const int kind = (rev ? kRev : 0) | (p.siz != 1 ? kTurned : 0) | (p.o_f32 ? kOutF32 : 0) |
+                             (((reinterpret_cast<uintptr_t>(o) | reinterpret_cast<uintptr_t>(wv)) & 31) == 0 && ((ostep | wstep) & 15) == 0 ? kWide : 0);
             long long passed = 0;    // gates of the chunks before
             float lost = 0.f;        // NaN once a gate was: it then reaches everything behind
             for (int j = 0; j < w.nchunk; ++j, ++it) {
@@ -862,10 +872,15 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                 // the rows of the dots, kWAhead pieces of 16 columns ahead (waited for one by one they took 8 K cycles a chunk)
                 constexpr int kWAhead = 3;
                 const uint4* wp = reinterpret_cast<const uint4*>(wv + wat);
+                const bool wide = flags & kWide;
                 uint4 wq[2 * kWAhead];
+                auto dot_rows = [&](int piece, uint4& x, uint4& y) {
+                    if (wide) ldg256(wp + 2 * piece, x, y);
+                    else { x = wp[2 * piece]; y = wp[2 * piece + 1]; }
+                };
                 if (SPLIT && live) {
 #pragma unroll
-                    for (int i = 0; i < 2 * kWAhead; ++i) wq[i] = wp[i];
+                    for (int i = 0; i < kWAhead; ++i) dot_rows(i, wq[2 * i], wq[2 * i + 1]);
                 }
                 if (!wait(oi_done, b) || !wait(op_done, b)) { failed = true; break; }
                 auto values = [&](int c, float (&v)[16]) {       // columns c .. c + 15 of o
@@ -890,24 +905,21 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                                    pack_bf16(v[i + 6], v[i + 7]));
                     }
                 } else {
-                    float dot = 0.f;
+                    float dot = 0.f, dot2 = 0.f;
 #pragma unroll (SPLIT ? DZ / 16 : 1)
                     for (int c = 0; c < DZ; c += 16) {
                         float v[16];
                         values(c, v);
                         if (!live) continue;
                         if constexpr (SPLIT) {
+                            const int k = (c / 16 % kWAhead) * 2;
+                            const uint32_t xs[8] = {wq[k].x, wq[k].y, wq[k].z, wq[k].w, wq[k + 1].x, wq[k + 1].y, wq[k + 1].z, wq[k + 1].w};
 #pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const int k = (c / 16 % kWAhead) * 2 + i;
-                                const uint32_t xs[4] = {wq[k].x, wq[k].y, wq[k].z, wq[k].w};
-                                if (c + 16 * kWAhead < DZ) wq[k] = wp[c / 8 + 2 * kWAhead + i];
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    dot = fmaf(__uint_as_float(xs[e] << 16), v[8 * i + 2 * e], dot);
-                                    dot = fmaf(__uint_as_float(xs[e] & 0xFFFF0000u), v[8 * i + 2 * e + 1], dot);
-                                }
+                            for (int e = 0; e < 8; ++e) {
+                                dot = fmaf(__uint_as_float(xs[e] << 16), v[2 * e], dot);
+                                dot2 = fmaf(__uint_as_float(xs[e] & 0xFFFF0000u), v[2 * e + 1], dot2);
                             }
+                            if (c + 16 * kWAhead < DZ) dot_rows(c / 16 + kWAhead, wq[k], wq[k + 1]);
                         }
                         if (f32) {
                             float4* d = reinterpret_cast<float4*>(reinterpret_cast<float*>(obase) + at + c);
@@ -915,13 +927,16 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                             for (int i = 0; i < 4; ++i) d[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
                         } else {
                             uint4* d = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(obase) + at + c);
+                            uint4 x[2];
 #pragma unroll
                             for (int i = 0; i < 2; ++i)
-                                d[i] = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                                x[i] = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
                                                   pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+                            if (wide) stg256(d, x[0], x[1]);
+                            else { d[0] = x[0]; d[1] = x[1]; }
                         }
                     }
-                    if (SPLIT && live) dots[t0 + row] = dot;
+                    if (SPLIT && live) dots[t0 + row] = dot + dot2;
                 }
                 if (staged) fence_async_smem();
                 fence_before_sync();
