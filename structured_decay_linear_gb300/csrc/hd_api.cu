@@ -166,12 +166,12 @@ Geometry dense(const dplr_hd_desc* d, const Cut& c) {
     return g;
 }
 
-Pass base_pass(const Gates& g, int dv, int DX, int DZ, bool transposed) {
+Pass base_pass(const Gates& g, int DX, int DZ, bool ext_turned, bool bound_turned) {
     Pass p{};
     p.g = g.p; p.gb = g.sb; p.gh = g.sh; p.gt = g.st;
     p.DX = DX; p.DZ = DZ;
-    p.six = transposed ? 1 : dv;
-    p.siz = transposed ? dv : 1;
+    p.ext_turned = ext_turned;
+    p.bound_turned = bound_turned;
     return p;
 }
 
@@ -235,7 +235,7 @@ dplr_status dplr_hd_forward(const dplr_hd_desc* desc, const dplr_hd_tensor* q, c
     a.status = static_cast<int*>(workspace);
     a.wait_cycles = wait_limit();
     Pass& p = a.pass[0];
-    p = base_pass(g, desc->dv, desc->dk, desc->dv, false);
+    p = base_pass(g, desc->dk, desc->dv, false, false);
     p.x = vq; p.y = vk; p.z = vv;
     if (pl.c.nseg > 1) {
         p.bound = reinterpret_cast<float*>(ws + pl.bound);
@@ -296,19 +296,20 @@ dplr_status dplr_hd_backward(const dplr_hd_desc* desc, const dplr_hd_tensor* q, 
     const int K = desc->dk, V = desc->dv;
     if (many) {
         a.npass = 2;
+        // boundary states as S^T and dS^T [dv][dk], the way dq and dk start from them (dv turns them)
         Pass& f = a.pass[0];
-        f = base_pass(g, V, K, V, false);
-        f.y = vk; f.z = vv; f.bound = at(pl.fwd); f.gsum = at(pl.gsum);
+        f = base_pass(g, V, K, false, false);
+        f.y = vv; f.z = vk; f.bound = at(pl.fwd); f.gsum = at(pl.gsum);
         f.states_only = 2;          // the last segment's too: its gates, and S_T
         Pass& b = a.pass[1];
-        b = base_pass(g, V, K, V, false);
-        b.y = vq; b.z = vdo; b.reverse = 1; b.bound = at(pl.bwd);
+        b = base_pass(g, V, K, false, false);
+        b.y = vdo; b.z = vq; b.reverse = 1; b.bound = at(pl.bwd);
         b.states_only = 1;
         HD_CUDA(launch(a, on_tensor_cores(desc), s));
         Scan sc{};
         sc.geo = a.geo; sc.B = desc->B; sc.dk = K; sc.dv = V;
         sc.fwd = at(pl.fwd); sc.fwd_ext = S0; sc.upto_end = 1;
-        sc.bwd = at(pl.bwd); sc.bwd_ext = dST; sc.gsum = at(pl.gsum);
+        sc.bwd = at(pl.bwd); sc.bwd_ext = dST; sc.gsum = at(pl.gsum); sc.turned = 1;
         HD_CUDA(launch_scan(sc, s));
     }
     const bool shared = desc->H != desc->Hq;
@@ -318,16 +319,16 @@ dplr_status dplr_hd_backward(const dplr_hd_desc* desc, const dplr_hd_tensor* q, 
     };
     a.npass = 3;
     Pass& pq = a.pass[0];
-    pq = base_pass(g, V, V, K, true);
+    pq = base_pass(g, V, K, true, false);
     pq.x = vdo; pq.y = vv; pq.z = vk;
     pq.ext_in = S0; pq.bound = many ? at(pl.fwd) : nullptr;
     if (!many && ddecay && dST) pq.ext_out = at(pl.fwd);
     Pass& pk = a.pass[1];
-    pk = base_pass(g, V, V, K, true);
+    pk = base_pass(g, V, K, true, false);
     pk.x = vv; pk.y = vdo; pk.z = vq; pk.reverse = 1;
     pk.ext_in = dST; pk.bound = many ? at(pl.bwd) : nullptr;
     Pass& pv = a.pass[2];
-    pv = base_pass(g, V, K, V, false);
+    pv = base_pass(g, K, V, false, true);
     pv.x = vk; pv.y = vq; pv.z = vdo; pv.reverse = 1;
     pv.ext_in = dST; pv.bound = pk.bound; pv.ext_out = dS0;
     output(pq, vdq);
@@ -406,7 +407,7 @@ dplr_status dplr_hd_forward_packed(const dplr_hd_desc* desc, int32_t R, int32_t 
     a.status = static_cast<int*>(workspace);
     a.wait_cycles = wait_limit();
     Pass& p = a.pass[0];
-    p = base_pass(g, desc->dv, desc->dk, desc->dv, false);
+    p = base_pass(g, desc->dk, desc->dv, false, false);
     p.x = vq; p.y = vk; p.z = vv;
     if (desc->T > block) {
         const size_t n = (size_t)max_blocks * desc->H;

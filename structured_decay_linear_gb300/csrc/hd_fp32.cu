@@ -102,14 +102,20 @@ __device__ __forceinline__ void segment_pass(const Pass& p, const Geometry& geo,
     // ---- the starting state
     {
         const float* src = nullptr;
+        bool turned = false;
         if (!so) {
-            if (p.bound && !sg.alone) src = p.bound + (rev ? sg.entry + sg.step : sg.entry) * (long long)DX * p.DZ;
-            else if (p.ext_in && !sg.fresh) src = p.ext_in + sg.ext * (long long)DX * p.DZ;
+            if (p.bound && !sg.alone) {
+                src = p.bound + (rev ? sg.entry + sg.step : sg.entry) * (long long)DX * p.DZ;
+                turned = p.bound_turned;
+            } else if (p.ext_in && !sg.fresh) {
+                src = p.ext_in + sg.ext * (long long)DX * p.DZ;
+                turned = p.ext_turned;
+            }
         }
         for (int i = tid; i < DX * NZ; i += TH) {
             // walk the state along its contiguous axis
-            const int r = p.siz == 1 ? i / NZ : i % DX, c = p.siz == 1 ? i % NZ : i / DX;
-            S[r * LDZ + c] = src ? src[r * p.six + (z0 + c) * p.siz] : 0.f;
+            const int r = turned ? i % DX : i / NZ, c = turned ? i / DX : i % NZ;
+            S[r * LDZ + c] = src ? src[turned ? (z0 + c) * DX + r : r * p.DZ + z0 + c] : 0.f;
         }
     }
     float gsum = 0.f;
@@ -305,10 +311,11 @@ __device__ __forceinline__ void segment_pass(const Pass& p, const Geometry& geo,
     float* dst = nullptr;
     if (so) dst = p.bound + (rev ? sg.entry : sg.entry + sg.step) * (long long)DX * p.DZ;
     else if (p.ext_out && (rev ? sg.first : sg.last)) dst = p.ext_out + sg.ext * (long long)DX * p.DZ;
+    const bool turned = so ? p.bound_turned : p.ext_turned;
     if (dst)
         for (int i = tid; i < DX * NZ; i += TH) {
-            const int r = i / NZ, c = i % NZ;
-            dst[r * p.six + (z0 + c) * p.siz] = S[r * LDZ + c];
+            const int r = turned ? i % DX : i / NZ, c = turned ? i / DX : i % NZ;
+            dst[turned ? (z0 + c) * DX + r : r * p.DZ + z0 + c] = S[r * LDZ + c];
         }
     if (so && p.gsum && zb == 0 && tid == 0) p.gsum[sg.entry] = gsum;
 }

@@ -85,16 +85,16 @@ __device__ __forceinline__ bool locate(const Geometry& g, int unit, Segment& s) 
     return true;
 }
 
-// One pass over the segments. States are [DX][DZ] of the pass: element (i, j) of the state with index e of an array of
-// [dk][dv] states at e * dk * dv + i * six + j * siz (six, siz = dv, 1 or, for a pass on transposed states, 1, dv).
+// One pass over the segments. Its state is [DX][DZ]; the caller's states (ext) and the boundary states (bound) are arrays of
+// such matrices, or `turned` of their transposes [DZ][DX].
 struct Pass {
     View x, y, z;
     const float* g; long long gb, gh, gt;   // log-gates (0 strides: one per head)
     int reverse;
     int DX, DZ;
-    long long six, siz;
+    int ext_turned, bound_turned;
     const float* ext_in;     // the caller's initial (backward in time: final) states, nullable
-    float* ext_out;          // outputs pass: where the last segment leaves its state (plain orientation), nullable
+    float* ext_out;          // outputs pass: where the last segment leaves its state, nullable
     float* bound;            // boundary states (null: every sequence has one segment)
     float* gsum;             // states pass: sum of the segment's gates, at the segment's entry
     // outputs
@@ -134,6 +134,7 @@ struct Scan {
     int B, R, dk, dv;
     float* fwd; const float* fwd_ext; int upto_end;
     float* bwd; const float* bwd_ext;
+    int turned;              // the boundary states are [dv][dk], the ext states [dk][dv]
     const float* gsum;
 };
 cudaError_t launch_scan(const Scan& a, cudaStream_t s);

@@ -38,7 +38,14 @@ __device__ __forceinline__ void scan_row(const Scan& a, int row, int at, bool ba
         eidx = row;
     }
     float4 cur = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (ext && !fresh) cur = *reinterpret_cast<const float4*>(ext + eidx * size + at);
+    if (ext && !fresh) {
+        if (a.turned) {       // element (j, i) of [dv][dk] is (i, j) of [dk][dv]
+            const float* e = ext + eidx * size + (at % a.dk) * (long long)a.dv + at / a.dk;
+            cur = make_float4(e[0], e[a.dv], e[2 * a.dv], e[3 * a.dv]);
+        } else {
+            cur = *reinterpret_cast<const float4*>(ext + eidx * size + at);
+        }
+    }
     // step i (0 ..): the contribution lies at boundary first + i dir, its gates at segment gfirst + i dir
     const int n = back ? nseg - 1 : (a.upto_end ? nseg : nseg - 1);
     const long long dir = back ? -step : step;

@@ -85,7 +85,8 @@ struct alignas(16) GateBuf {
     float* dots;        // the head's
     long long ostep, wstep;
 };
-enum : int { kFirst = 1, kLast = 2, kRev = 4, kTurned = 8, kOutF32 = 16, kEnd = 32, kWide = 64 };   // kWide: rows of o and w on 32 bytes
+enum : int { kFirst = 1, kLast = 2, kRev = 4, kTurned = 8, kOutF32 = 16, kEnd = 32, kWide = 64, kOutTurned = 128 };   // kTurned: src;
+                                                            // kOutTurned: dst; kWide: rows of o and w on 32 bytes
 static_assert(sizeof(GateBuf) % 16 == 0, "16-byte rows");
 
 template <int DX, int DZ, bool SPLIT, bool STATES>
@@ -230,33 +231,37 @@ __device__ __forceinline__ void clear_rows(uint32_t tz, int r0, int r1, int tid,
 // and turns them in 4 KB of shared memory of its own (the rows of the R tile that it alone writes).
 __device__ __forceinline__ uint32_t turn_at(int row, int piece) { return (uint32_t)(row * 128 + ((piece ^ (row & 7)) << 4)); }
 
-// Columns c .. c + 31 of the warp's 32 rows (first row r0) of a state [DX][DZ], or `turned` of one [DZ][DX]: v = this
-// lane's row.
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Starts columns c .. c + 31 of the warp's 32 rows (first row r0) of a state [DX][DZ], or `turned` of one [DZ][DX], on
+// their way to the 4 KB at `turn`; after copies_done() and a __syncwarp(), block_row() gives this lane's row.
 template <int DX, int DZ>
-__device__ __forceinline__ void load_block(const float* state, bool turned, int r0, int c, uint32_t turn, float (&v)[32]) {
+__device__ __forceinline__ void start_block(const float* state, bool turned, int r0, int c, uint32_t turn) {
     const int lane = threadIdx.x & 31;
     if (!turned) {
         const float* src = state + (r0 + (lane >> 3)) * DZ + c + 4 * (lane & 7);
-        float4 x[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = __ldcs(reinterpret_cast<const float4*>(src + 4 * k * DZ));
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            sts128(turn + turn_at(4 * k + (lane >> 3), lane & 7), __float_as_uint(x[k].x), __float_as_uint(x[k].y),
-                   __float_as_uint(x[k].z), __float_as_uint(x[k].w));
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            uint32_t u[4];
-            lds128(turn + turn_at(lane, k), u);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[4 * k + e] = __uint_as_float(u[e]);
-        }
-        __syncwarp();
-    } else {        // transposed: a column's 32 rows lie together
+        for (int k = 0; k < 8; ++k) copy_async16(turn + turn_at(4 * k + (lane >> 3), lane & 7), src + 4 * k * DZ);
+    } else {        // a column's 32 rows lie together
         const float* src = state + r0 + lane + c * DX;
+#pragma unroll 8
+        for (int i = 0; i < 32; ++i) copy_async4(turn + turn_at(lane, i >> 2) + 4 * (i & 3), src + i * DX);
+    }
+}
+__device__ __forceinline__ void block_row(uint32_t turn, float (&v)[32]) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = src[i * DX];
+    for (int k = 0; k < 8; ++k) {
+        uint32_t u[4];
+        lds128(turn + turn_at(lane, k), u);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[4 * k + e] = __uint_as_float(u[e]);
     }
 }
 
@@ -573,7 +578,8 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
             const __nv_bfloat16* wv = SPLIT ? static_cast<const __nv_bfloat16*>(p.w.p) + w.sg.b * p.w.sb + (w.sg.h / p.w.div) * p.w.sh : nullptr;
             float* dots = SPLIT ? p.dots + ((long long)w.sg.b * a.l.geo.H + w.sg.h) * a.l.geo.T : nullptr;
             float* gsum = STATES && p.gsum ? p.gsum + w.sg.entry : nullptr;
-            const int kind = (rev ? kRev : 0) | (p.siz != 1 ? kTurned : 0) | (p.o_f32 ? kOutF32 : 0) |
+            const int kind = (rev ? kRev : 0) | ((p.bound && !w.sg.alone ? p.bound_turned : p.ext_turned) ? kTurned : 0) |
+                             ((STATES ? p.bound_turned : p.ext_turned) ? kOutTurned : 0) | (p.o_f32 ? kOutF32 : 0) |
                              (((reinterpret_cast<uintptr_t>(o) | reinterpret_cast<uintptr_t>(wv)) & 31) == 0 && ((ostep | wstep) & 15) == 0 ? kWide : 0);
             long long passed = 0;    // gates of the chunks before
             float lost = 0.f;        // NaN once a gate was: it then reaches everything behind
@@ -710,7 +716,7 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                 give_back(&g_free[b], (uint32_t)(uintptr_t)dst);
                 if ((flags & kLast) && grp == 0 && (DX == 128 || warp < 2)) {
                     if (!wait(r_done, b)) { failed = true; break; }
-                    store_state<DX, DZ>(dst, flags & kTurned, 32 * warp, turn, tmem + TM_R + lane_off);
+                    store_state<DX, DZ>(dst, flags & kOutTurned, 32 * warp, turn, tmem + TM_R + lane_off);
                 }
             } else if (grp == 0) {
                 // ---- A: the state (thread = row of R; with DX = 64 two warps only keep step)
@@ -720,17 +726,31 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                 const float* src = g.src;
                 float* dst = g.dst;
                 const bool turned = flags & kTurned;
-                if (mine && (flags & kFirst)) {     // from memory to tensor memory (the tile's place turns the blocks)
+                if (mine && (flags & kFirst)) {
+                    // From memory to tensor memory, through the places of the tile's rows that only this warp writes: as many
+                    // blocks at once as those hold (one by one, each waited for the memory's latency: 10 K cycles a state).
+                    constexpr int HB = DZ / 64, NB = DZ / 32, AT = (SPLIT ? 2 : 1) * HB;
+                    auto place = [&](int i) { return turn + (uint32_t)(i % HB) * (DX * 128) + (uint32_t)(i / HB) * Ly::RB; };
 #pragma unroll 1
-                    for (int c = 0; c < DZ; c += 32) {
-                        float v[32];
+                    for (int g0 = 0; g0 < NB; g0 += AT) {
                         if (src) {
-                            load_block<DX, DZ>(src, turned, 32 * warp, c, turn, v);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] = 0.f;
+#pragma unroll 1
+                            for (int i = 0; i < AT; ++i) start_block<DX, DZ>(src, turned, 32 * warp, 32 * (g0 + i), place(i));
+                            copies_done();
+                            __syncwarp();
                         }
-                        tmem_st32_nowait(tmem + TM_R + lane_off + c, v);
+#pragma unroll 1
+                        for (int i = 0; i < AT; ++i) {
+                            float v[32];
+                            if (src) {
+                                block_row(place(i), v);
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) v[e] = 0.f;
+                            }
+                            tmem_st32_nowait(tmem + TM_R + lane_off + 32 * (g0 + i), v);
+                        }
+                        __syncwarp();
                     }
                     tmem_wait_st();
                 }
@@ -766,7 +786,7 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                 give_back(&g_free[b], (uint32_t)(uintptr_t)dst);
                 if ((flags & kLast) && dst) {       // the state it ends with
                     if (!wait(oi_done, b) || !wait(r_done, b)) { failed = true; break; }
-                    if (mine) store_state<DX, DZ>(dst, turned, 32 * warp, turn, tmem + TM_R + lane_off);
+                    if (mine) store_state<DX, DZ>(dst, flags & kOutTurned, 32 * warp, turn, tmem + TM_R + lane_off);
                 }
             } else if (grp == 3) {
                 // ---- C: P (thread = row)
