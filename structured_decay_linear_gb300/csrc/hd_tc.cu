@@ -40,6 +40,7 @@
 // Bound: by the bytes of x, y, z and o (1 KB a token and head at 128 x 128): a chunk is 128 KB, 5.6 K cycles of its
 // share of HBM bandwidth on 152 SMs, against 2.6 K cycles of products and about 2.5 K of each group's work.
 #include <cstring>
+#include <type_traits>
 
 #include "hd_internal.h"
 #include "tc_common.cuh"
@@ -53,7 +54,7 @@ using namespace tc;
 constexpr int C = kChunk;                  // 128
 constexpr int kGrp = 128;
 constexpr int kWorkers = 20;                // warps of the groups A (0-3), B1 (4-7), B2 (8-11), C (12-15), O (16-19)
-constexpr int NT = 32 * kWorkers + 96;     // and warps 20 (copies), 21 (MMA issue), 22 (gates)
+constexpr int NT = 32 * kWorkers + 128;    // and warps 20 (copies), 21 (MMA issue), 22 (gates), 23 (none)
 constexpr uint32_t kHalf = C * 128;        // bytes of a half tile: 128 rows of 64 bf16
 constexpr uint32_t TM_R = 0, TM_D = 128, TM_OI = 256, TM_OP = 384, kTmemCols = 512;
 constexpr double kLog2e = 1.4426950408889634;
@@ -108,6 +109,14 @@ struct Layout {
     static constexpr int TOTAL = BARS + 192;   // 23 barriers, the address of the tensor memory
     static_assert(TOTAL <= 227 * 1024, "shared memory budget");
 };
+
+// Registers of a group's threads. The block is launched with 80 a thread (65536 / 768); B gives some up for C and O. With
+// what is left of the L1 cache beside the tiles, a spilled register is read back from L2: 32 of them a chunk had doubled
+// the time of the gradient passes.
+template <int N> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N)); }
+template <int N> __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N)); }
+constexpr int kRegsLaunch = 80, kRegsB = 64, kRegsC = 88, kRegsO = 104;
+static_assert(2 * kRegsB + kRegsC + kRegsO <= 4 * kRegsLaunch, "the groups' shares come out of the launch's registers");
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -656,15 +665,17 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
             }
         }
         if (failed && lane == 0) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
-    } else {
+    } else if (warp < kWorkers) {
         // =================== the groups ===================
         const int grp = warp >> 2;
         const uint32_t tr = sb + Ly::T_R, turn = tr + 4096 * rw;     // rows 32 rw .. of the R tile's first half: A's warp's own
         bool storing = false;      // (O, lane 0) a store may still read the warp's rows of the o tile
+        auto work = [&](auto role_) {      // one loop for each role: 0 A, 1 B1 and B2, 3 C, 4 O (a states pass: all the same)
+        constexpr int role = decltype(role_)::value;
         for (uint32_t it = 0;; ++it) {
             const uint32_t b = it & 1, s = it % Ly::NZ, zpar = (it / Ly::NZ) & 1;
             const GateBuf& g = gates[b];
-            if (!STATES && (grp == 1 || grp == 2)) {
+            if constexpr (!STATES && role == 1) {
                 // ---- B1, B2: Y~ of 64 tokens
                 constexpr int PER = DX / 8, IT = C / 2 * PER / kGrp, TS = kGrp / PER;     // pieces of a row, of a thread; tokens between two
                 if (!wait(&g_full[b], (it >> 1) & 1)) { failed = true; break; }
@@ -698,13 +709,12 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) { mbar_arrive(h ? y_rest : y_ready); mbar_arrive(&g_free[b]); }
-                continue;
-            }
+            } else {
             if (!wait(&g_full[b], (it >> 1) & 1)) { failed = true; break; }
             const int flags = __shfl_sync(0xffffffffu, g.flags, 0), n = __shfl_sync(0xffffffffu, g.n, 0);
             if (flags & kEnd) break;
-            const bool rev = flags & kRev;
-            if (STATES) {
+            [[maybe_unused]] const bool rev = flags & kRev;
+            if constexpr (STATES) {
                 // ---- every worker: Y~; behind the last chunk A: the state
                 if (!wait(&full_y[s], zpar) || (it > 0 && !wait(r_done, b ^ 1)) || (n < C && !wait(&full_z[s], zpar))) { failed = true; break; }
                 scale_rows<DX>(sb + Ly::T_Y + s * Ly::XB, sb + Ly::T_YH, sb + Ly::T_YL, g, n, tid, 32 * kWorkers);
@@ -718,7 +728,7 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                     if (!wait(r_done, b)) { failed = true; break; }
                     store_state<DX, DZ>(dst, flags & kOutTurned, 32 * warp, turn, tmem + TM_R + lane_off);
                 }
-            } else if (grp == 0) {
+            } else if constexpr (role == 0) {
                 // ---- A: the state (thread = row of R; with DX = 64 two warps only keep step)
                 const bool mine = DX == 128 || warp < 2;
                 if (it > 0 && (!wait(oi_done, b ^ 1) || !wait(r_done, b ^ 1))) { failed = true; break; }
@@ -788,7 +798,7 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                     if (!wait(oi_done, b) || !wait(r_done, b)) { failed = true; break; }
                     if (mine) store_state<DX, DZ>(dst, flags & kOutTurned, 32 * warp, turn, tmem + TM_R + lane_off);
                 }
-            } else if (grp == 3) {
+            } else if constexpr (role == 3) {
                 // ---- C: P (thread = row)
                 if (!wait(d_done, b)) { failed = true; break; }
                 const float sgn = rev ? 1.f : -1.f;
@@ -972,6 +982,22 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                     }
                 }
             }
+            }
+        }
+        };
+        if constexpr (STATES) {
+            work(std::integral_constant<int, 0>{});
+        } else if (grp == 0) {
+            work(std::integral_constant<int, 0>{});
+        } else if (grp <= 2) {
+            fewer_registers<kRegsB>();
+            work(std::integral_constant<int, 1>{});
+        } else if (grp == 3) {
+            more_registers<kRegsC>();
+            work(std::integral_constant<int, 3>{});
+        } else {
+            more_registers<kRegsO>();
+            work(std::integral_constant<int, 4>{});
         }
         if (storing) bulk_wait_all();
         if (failed && lane == 0) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
