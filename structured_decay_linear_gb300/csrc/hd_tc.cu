@@ -536,15 +536,22 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                 if (!wait1(r_ready, par) || (it > 0 && !wait1(o_free, par ^ 1))) { failed = true; break; }
                 mma_Oi();
                 if (!wait1(y_ready, par) || !wait1(&full_z[s], zpar)) { failed = true; break; }
+                if (SPLIT) {      // O takes longest here: Op before R (z has been cleared once both halves of Y~ are there)
+                    if (!wait1(y_rest, par) || !wait1(p_ready, par)) { failed = true; break; }
+                    mma_Op(tz);
+                    mma_commit(op_done);
+                }
                 mma_R(tz, 0, true);
                 mma_commit(r_half);
-                if (!wait1(y_rest, par)) { failed = true; break; }
+                if (!SPLIT && !wait1(y_rest, par)) { failed = true; break; }
                 mma_R(tz, 1, true);
                 mma_commit(r_done);
-                if (!wait1(p_ready, par)) { failed = true; break; }
-                mma_Op(tz);
+                if (!SPLIT) {
+                    if (!wait1(p_ready, par)) { failed = true; break; }
+                    mma_Op(tz);
+                }
                 mma_commit(&free_z[s]);
-                mma_commit(op_done);
+                if (!SPLIT) mma_commit(op_done);
             }
             if (failed) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
             mma_commit(drain);       // every MMA this thread issued: none may run on freed tensor memory
