@@ -402,7 +402,7 @@ dplr_status dplr_hd_forward_packed(const dplr_hd_desc* desc, int32_t R, int32_t 
     Launch a{};
     a.geo.H = desc->H; a.geo.T = desc->T;
     a.geo.blocks = blocks; a.geo.block_starts = block_starts; a.geo.slots = slots; a.geo.context = context;
-    a.geo.n_slots = n_slots;
+    a.geo.n_slots = n_slots; a.geo.R = R;
     a.B = 1; a.bf16 = desc->in_dtype == DPLR_BF16; a.max_blocks = (int)max_blocks; a.npass = 1;
     a.status = static_cast<int*>(workspace);
     a.wait_cycles = wait_limit();

@@ -35,7 +35,8 @@ struct Geometry {
     int T;                  // tokens of a sequence (dense)
     int nseg, L;            // dense: segments of a sequence, tokens of a segment
     const int* blocks;      // packed: [.][4] request, first row, rows, index in the request; null: dense
-    const int* block_starts;
+    const int* block_starts;   // [R + 1]
+    int R;
     const int* slots;
     const int* context;
     int n_slots;

@@ -75,6 +75,11 @@ __device__ __forceinline__ void scan_row(const Scan& a, int row, int at, bool ba
 
 __global__ void __launch_bounds__(256) hd_scan_kernel(const __grid_constant__ Scan a, int rows) {
     const int at = (blockIdx.y * 256 + threadIdx.x) * 4;
+    if (a.geo.blocks) {     // a ragged batch may have no request of two blocks: then there is nothing to do
+        bool any = false;
+        for (int r = threadIdx.x; r < a.R; r += 256) any |= a.geo.block_starts[r + 1] - a.geo.block_starts[r] > 1;
+        if (!__syncthreads_or(any)) return;
+    }
     if (at >= a.dk * a.dv) return;
     for (int row = blockIdx.x; row < rows; row += gridDim.x) scan_row(a, row, at, a.fwd == nullptr || blockIdx.z == 1);
 }
@@ -204,7 +209,7 @@ cudaError_t launch_scan(const Scan& a, cudaStream_t s) {
     const unsigned gy = (unsigned)((a.dk * a.dv / 4 + 255) / 256), gz = a.fwd && a.bwd ? 2 : 1;
     // a ragged batch's rows are mostly of one block, with nothing to do: few CTAs walk them (1600 rows of which none had
     // anything to do took 16 us as CTAs of their own)
-    const long long most = a.geo.blocks ? 64 : rows;
+    const long long most = a.geo.blocks ? 256 : rows;
     hd_scan_kernel<<<dim3((unsigned)(rows < most ? rows : most), gy, gz), 256, 0, s>>>(a, (int)rows);
     return cudaGetLastError();
 }

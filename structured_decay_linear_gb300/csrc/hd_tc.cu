@@ -63,6 +63,7 @@ struct alignas(128) Args {
     CUtensorMap map[3][4];    // [pass][x, y, z, o]
     Launch l;
     int total;                // units of work: segments times passes
+    int* counter;             // null: units u = blockIdx.x, + gridDim.x, ..; else all but a CTA's first come from here (0 at first)
 };
 
 // What the gate warp says of a chunk, double-buffered; A_i: cumulative gates at the start of block i of 32 tokens (log2
@@ -98,15 +99,15 @@ struct Layout {
     static constexpr int RB = STATES ? DX * 128 : DX * DZ * 2;  // R as bf16: DZ / 64 halves of DX rows of 128 bytes
     static constexpr int T_X = 0;
     static constexpr int T_Y = T_X + (STATES ? 0 : XB);
-    static constexpr int T_YH = T_Y + NY * XB;
-    static constexpr int T_YL = T_YH + XB;
-    static constexpr int T_Z = T_YL + XB;                     // (a 64-feature Y~ read as M = 128 runs into what follows)
+    static constexpr int T_YH = STATES ? T_Y : T_Y + NY * XB; // a states pass, which has no D, writes hi over y
+    static constexpr int T_YL = T_YH + NY * XB;
+    static constexpr int T_Z = T_YL + NY * XB;                // (a 64-feature Y~ read as M = 128 runs into what follows)
     static constexpr int T_R = T_Z + NZ * ZB;
     static constexpr int T_O = T_R + RB * (SPLIT ? 2 : 1);    // o on its way out
     static constexpr bool STAGED = !SPLIT && !STATES;
     static constexpr int GATES = T_O + (STAGED ? ZB : 0);
     static constexpr int BARS = GATES + 2 * (int)sizeof(GateBuf);
-    static constexpr int TOTAL = BARS + 192;   // 23 barriers, the address of the tensor memory
+    static constexpr int TOTAL = BARS + 256;   // 25 barriers, the address of the tensor memory, a unit's number
     static_assert(TOTAL <= 227 * 1024, "shared memory budget");
 };
 
@@ -309,8 +310,8 @@ __device__ __forceinline__ void store_state(float* state, bool turned, int r0, u
     }
 }
 
-// One unit of work: a segment in a pass. Every role of a CTA walks the same units, u = blockIdx.x, + gridDim.x, ..; its
-// chunks are numbered through, so that copies, gates and products of a unit run into those of the one before.
+// One unit of work: a segment in a pass. The gate warp finds a CTA's units and names them to the copy warp; a CTA's chunks
+// are numbered through, so that copies, gates and products of a unit run into those of the one before.
 struct Work {
     const Pass* p;
     const CUtensorMap* maps;
@@ -374,7 +375,10 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
     uint64_t* y_rest = bars + 20;    // B2: of the others
     uint64_t* p_ready = bars + 21;   // C: P
     uint64_t* o_free = bars + 22;    // O: Oi and Op read
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 23);
+    uint64_t* u_full = bars + 23;    // gates: the next unit's number (-1: none)
+    uint64_t* u_free = bars + 24;    // copies: taken
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 25);
+    volatile int* next_unit = reinterpret_cast<volatile int*>(bars + 25) + 1;
     GateBuf* gates = reinterpret_cast<GateBuf*>(smem + Ly::GATES);
 
     // (what is the same for a warp goes through a shuffle, which tells the compiler so: branches on it then cost no
@@ -385,10 +389,10 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
     const long long wl = a.l.wait_cycles;
 
     if (tid == 0) {
-        for (int i = 0; i < 23; ++i) {
+        for (int i = 0; i < 25; ++i) {
             uint32_t n = 1;
             if (i == 15 || i == 16) n = kWorkers + 1;
-            else if (i == 17 || i >= 20) n = 4;
+            else if (i == 17 || (i >= 20 && i <= 22)) n = 4;
             else if (i == 18) n = 8;
             else if (i == 19) n = STATES ? kWorkers : 4;
             mbar_init(bars + i, n);
@@ -425,9 +429,18 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
         // =================== copies ===================
         if (lane == 0) {
             uint32_t it = 0, nx = 0, ny = 0, nz = 0;    // chunks; copies started
-            for (int u = blockIdx.x; u < a.total && !failed; u += gridDim.x) {
+            // the first unit is the CTA's own number's, if there is something to do; the gate warp names the others
+            int u = blockIdx.x;
+            for (uint32_t named = 0; !failed; u = -1) {
                 Work w;
-                if (!find_work<STATES>(a, u, w)) continue;
+                if (u < 0 || !find_work<STATES>(a, u, w)) {
+                    if (!mbar_wait(u_full, named & 1, wl)) { failed = true; break; }
+                    u = *next_unit;
+                    if (u < 0) break;
+                    mbar_arrive(u_free);       // (behind the branch: the load has returned)
+                    ++named;
+                    find_work<STATES>(a, u, w);
+                }
                 const CUtensorMap* maps = w.maps;
                 const int hx = w.sg.h / w.p->x.div, hy = w.sg.h / w.p->y.div, hz = w.sg.h / w.p->z.div, bb = w.sg.b;
                 if (const float* src = STATES ? nullptr : start_state<DX, DZ>(w))
@@ -501,10 +514,10 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                 }
                 mma_commit(oi_done);
             };
-            auto mma_R = [&](uint32_t tz, int half, bool acc) {      // 64 tokens: four slices of 2048 bytes
+            auto mma_R = [&](uint32_t buf, uint32_t tz, int half, bool acc) {      // 64 tokens: four slices of 2048 bytes
 #pragma unroll 1
                 for (int s = 0; s < 2; ++s)
-                    mma_chain(tmem + TM_R, smem_desc_sw128(sb + (s ? Ly::T_YL : Ly::T_YH) + 8192 * half, kHalf, 1024), 2048,
+                    mma_chain(tmem + TM_R, smem_desc_sw128(sb + (s ? Ly::T_YL : Ly::T_YH) + buf * Ly::XB + 8192 * half, kHalf, 1024), 2048,
                               smem_desc_sw128(tz + 8192 * half, kHalf, 1024), 2048, idR, 64, acc || s > 0);
             };
             auto mma_Op = [&](uint32_t tz) {
@@ -525,8 +538,8 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                 mbar_arrive(&g_free[par]);       // (behind the branch: the load has returned)
                 if (STATES) {
                     if (!wait1(y_ready, par) || !wait1(&full_z[s], zpar)) { failed = true; break; }
-                    mma_R(tz, 0, !(flags & kFirst));
-                    mma_R(tz, 1, true);
+                    mma_R(s, tz, 0, !(flags & kFirst));
+                    mma_R(s, tz, 1, true);
                     mma_commit(&free_z[s]);
                     mma_commit(r_done);
                     continue;
@@ -541,10 +554,10 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                     mma_Op(tz);
                     mma_commit(op_done);
                 }
-                mma_R(tz, 0, true);
+                mma_R(0, tz, 0, true);
                 mma_commit(r_half);
                 if (!SPLIT && !wait1(y_rest, par)) { failed = true; break; }
-                mma_R(tz, 1, true);
+                mma_R(0, tz, 1, true);
                 mma_commit(r_done);
                 if (!SPLIT) {
                     if (!wait1(p_ready, par)) { failed = true; break; }
@@ -569,9 +582,38 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
             if (it >= 2 && !wait(&g_free[b], ((it - 2) >> 1) & 1)) { failed = true; return nullptr; }
             return gates + b;
         };
-        for (int u = blockIdx.x; u < a.total && !failed; u += gridDim.x) {
+        // a ragged batch's blocks end before its table does
+        int total = a.total;
+        if (a.l.geo.blocks) total = min(total, a.l.geo.block_starts[a.l.geo.R] * a.l.geo.H * a.l.npass);
+        uint32_t named = 0;
+        auto name = [&](int u) {          // tells the copy warp of a unit
+            if (named > 0 && !wait(u_free, (named - 1) & 1)) { failed = true; return; }
+            if (lane == 0) *next_unit = u;
+            arrive(u_full);
+            ++named;
+        };
+        int unit = blockIdx.x, after = 0;
+        for (bool begun = false; unit < total && !failed; unit = after, begun = true) {
             Work w;
-            if (!find_work<STATES>(a, u, w)) continue;
+            if (STATES && a.l.geo.blocks) {      // most of a ragged batch's requests have one block and no boundary: 32 at a time
+                Work v;
+                const int mine = unit + lane * (int)gridDim.x;
+                const uint32_t some = __ballot_sync(0xffffffffu, mine < total && find_work<STATES>(a, mine, v));
+                if (some == 0) {
+                    after = unit + 32 * (int)gridDim.x;
+                    continue;
+                }
+                const int skip = __ffs(some) - 1;
+                unit += skip * (int)gridDim.x;
+                begun |= skip > 0;
+            }
+            after = unit + (int)gridDim.x;
+            if (!STATES && a.counter && lane == 0) after = (int)gridDim.x + atomicAdd(a.counter, 1);
+            // An outputs pass has no unit without work: the next one is named as soon as this one's first chunk is out. In a
+            // states pass a unit is named when it has been found to have some.
+            const bool some = find_work<STATES>(a, unit, w);
+            if (STATES && some && begun) name(unit);
+            if (!some || failed) continue;
             const Pass& p = *w.p;
             const bool rev = w.rev;
             const long long gstep = p.gt;     // (in registers: the loops below would read the pass from memory again and again)
@@ -584,19 +626,8 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
             };
             float cur[4], nxt[4];
             raw(0, cur);
-            // what the others need to know of the unit
-            const float* src = STATES ? nullptr : start_state<DX, DZ>(w);
-            float* dst = nullptr;
-            if (STATES) dst = p.bound + (rev ? w.sg.entry : w.sg.entry + w.sg.step) * (long long)(DX * DZ);
-            else if (p.ext_out && (rev ? w.sg.first : w.sg.last)) dst = p.ext_out + w.sg.ext * (long long)(DX * DZ);
-            const long long ostep = p.ot, wstep = p.w.st;
-            char* o = static_cast<char*>(p.o) + (w.sg.b * p.ob + w.sg.h * p.oh) * (p.o_f32 ? 4 : 2);
-            const __nv_bfloat16* wv = SPLIT ? static_cast<const __nv_bfloat16*>(p.w.p) + w.sg.b * p.w.sb + (w.sg.h / p.w.div) * p.w.sh : nullptr;
-            float* dots = SPLIT ? p.dots + ((long long)w.sg.b * a.l.geo.H + w.sg.h) * a.l.geo.T : nullptr;
             float* gsum = STATES && p.gsum ? p.gsum + w.sg.entry : nullptr;
-            const int kind = (rev ? kRev : 0) | ((p.bound && !w.sg.alone ? p.bound_turned : p.ext_turned) ? kTurned : 0) |
-                             ((STATES ? p.bound_turned : p.ext_turned) ? kOutTurned : 0) | (p.o_f32 ? kOutF32 : 0) |
-                             (((reinterpret_cast<uintptr_t>(o) | reinterpret_cast<uintptr_t>(wv)) & 31) == 0 && ((ostep | wstep) & 15) == 0 ? kWide : 0);
+            int kind = 0;
             long long passed = 0;    // gates of the chunks before
             float lost = 0.f;        // NaN once a gate was: it then reaches everything behind
             for (int j = 0; j < w.nchunk; ++j, ++it) {
@@ -643,28 +674,47 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                     g.re[lane] = ex2(real(rev ? all - ej : sj));
                 }
                 if (lane == 0) {
+                    // what the others need to know: of the unit, in either buffer once (not kept in registers: they spilled)
+                    if (j < 2) {
+                        const long long ostep = p.ot, wstep = p.w.st;
+                        char* o = static_cast<char*>(p.o) + (w.sg.b * p.ob + w.sg.h * p.oh) * (p.o_f32 ? 4 : 2);
+                        const __nv_bfloat16* wv = SPLIT ? static_cast<const __nv_bfloat16*>(p.w.p) + w.sg.b * p.w.sb +
+                                                              (w.sg.h / p.w.div) * p.w.sh : nullptr;
+                        kind = (rev ? kRev : 0) | ((p.bound && !w.sg.alone ? p.bound_turned : p.ext_turned) ? kTurned : 0) |
+                               ((STATES ? p.bound_turned : p.ext_turned) ? kOutTurned : 0) | (p.o_f32 ? kOutF32 : 0) |
+                               (((reinterpret_cast<uintptr_t>(o) | reinterpret_cast<uintptr_t>(wv)) & 31) == 0 &&
+                                ((ostep | wstep) & 15) == 0 ? kWide : 0);
+                        g.h = w.sg.h;
+                        g.b = w.sg.b;
+                        g.pass = (int)(w.p - a.l.pass);
+                        g.src = STATES ? nullptr : start_state<DX, DZ>(w);
+                        g.dst = nullptr;
+                        if (STATES) g.dst = p.bound + (rev ? w.sg.entry : w.sg.entry + w.sg.step) * (long long)(DX * DZ);
+                        else if (p.ext_out && (rev ? w.sg.first : w.sg.last)) g.dst = p.ext_out + w.sg.ext * (long long)(DX * DZ);
+                        g.o = o;
+                        g.w = wv;
+                        g.dots = SPLIT ? p.dots + ((long long)w.sg.b * a.l.geo.H + w.sg.h) * a.l.geo.T : nullptr;
+                        g.ostep = ostep;
+                        g.wstep = wstep;
+                    }
                     g.en = ex2(real(all)) + lost;
                     g.n = w.rows(j);
                     g.flags = kind | (j == 0 ? kFirst : 0) | (j == w.nchunk - 1 ? kLast : 0);
                     g.t0 = w.sg.t0 + w.chunk(j) * C;
-                    g.h = w.sg.h;
-                    g.b = w.sg.b;
-                    g.pass = (int)(w.p - a.l.pass);
-                    g.src = src;
-                    g.dst = dst;
-                    g.o = o;
-                    g.w = wv;
-                    g.dots = dots;
-                    g.ostep = ostep;
-                    g.wstep = wstep;
                 }
                 passed += all;
                 arrive(&g_full[it & 1]);
+                if (!STATES && j == 0) {
+                    after = __shfl_sync(0xffffffffu, after, 0);
+                    if (after < total) name(after);
+                    if (failed) break;
+                }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) cur[i] = nxt[i];
             }
             if (gsum && lane == 0 && !failed) *gsum = real(passed) * 0.6931471805599453f + lost;
         }
+        if (!failed) name(-1);
         if (!failed) {
             if (GateBuf* g = take()) {
                 if (lane == 0) g->flags = kEnd;
@@ -695,9 +745,6 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                 uint32_t u[IT][4];
 #pragma unroll
                 for (int i = 0; i < IT; ++i) lds128(sb + Ly::T_Y + off + i * TS * 128, u[i]);
-                float wt[IT];      // read ahead of the stores, which the compiler moves no load across
-#pragma unroll
-                for (int i = 0; i < IT; ++i) wt[i] = g.cf[t0 + i * TS] * g.ce[2 * h + i * TS / 32];
                 uint32_t seen = 0;
 #pragma unroll
                 for (int i = 0; i < IT; ++i) seen ^= (u[i][0] ^ u[i][1]) ^ (u[i][2] ^ u[i][3]);
@@ -708,11 +755,22 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                     clear_rows<DZ>(sb + Ly::T_Z + s * Ly::ZB, max(n, 64 * h), 64 * h + 64, row, kGrp);
 #pragma unroll
                     for (int i = 0; i < IT; ++i)
-                        if (t0 + i * TS >= n) u[i][0] = u[i][1] = u[i][2] = u[i][3] = 0u, wt[i] = 0.f;
+                        if (t0 + i * TS >= n) u[i][0] = u[i][1] = u[i][2] = u[i][3] = 0u;
                 }
 #pragma unroll
-                for (int i = 0; i < IT; ++i)
-                    scale16(u[i], wt[i], sb + Ly::T_YH + off + i * TS * 128, sb + Ly::T_YL + off + i * TS * 128);
+                for (int i0 = 0; i0 < IT; i0 += 4) {
+                    float wt[4];      // read ahead of the stores, which the compiler moves no load across
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) wt[i] = g.cf[t0 + (i0 + i) * TS] * g.ce[2 * h + (i0 + i) * TS / 32];
+                    if (n < C) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (t0 + (i0 + i) * TS >= n) wt[i] = 0.f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        scale16(u[i0 + i], wt[i], sb + Ly::T_YH + off + (i0 + i) * TS * 128, sb + Ly::T_YL + off + (i0 + i) * TS * 128);
+                }
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) { mbar_arrive(h ? y_rest : y_ready); mbar_arrive(&g_free[b]); }
@@ -723,8 +781,9 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
             [[maybe_unused]] const bool rev = flags & kRev;
             if constexpr (STATES) {
                 // ---- every worker: Y~; behind the last chunk A: the state
-                if (!wait(&full_y[s], zpar) || (it > 0 && !wait(r_done, b ^ 1)) || (n < C && !wait(&full_z[s], zpar))) { failed = true; break; }
-                scale_rows<DX>(sb + Ly::T_Y + s * Ly::XB, sb + Ly::T_YH, sb + Ly::T_YL, g, n, tid, 32 * kWorkers);
+                // (lo's buffer too is free once y has landed in its own: the copy waited for the product that read both)
+                if (!wait(&full_y[s], zpar) || (n < C && !wait(&full_z[s], zpar))) { failed = true; break; }
+                scale_rows<DX>(sb + Ly::T_Y + s * Ly::XB, sb + Ly::T_YH + s * Ly::XB, sb + Ly::T_YL + s * Ly::XB, g, n, tid, 32 * kWorkers);
                 if (n < C) clear_rows<DZ>(sb + Ly::T_Z + s * Ly::ZB, n, C, tid, 32 * kWorkers);
                 float* dst = g.dst;
                 fence_async_smem();
@@ -1072,6 +1131,13 @@ cudaError_t launch_tc(const Launch& l, cudaStream_t s) {
                 return cudaErrorInvalidValue;
         }
         a.total = (int)n * a.l.npass;
+        // Lengths of a ragged batch differ: CTAs take their units as they get done with others. Which one takes a unit does
+        // not touch its result.
+        if (l.geo.blocks && !q.states_only) {
+            a.counter = l.status + 16;
+            const cudaError_t e = cudaMemsetAsync(a.counter, 0, sizeof(int), s);
+            if (e != cudaSuccess) return e;
+        }
         const bool split = q.dots != nullptr, states = q.states_only != 0;
         cudaError_t e;
         if (q.DX == 128 && q.DZ == 128) e = run_kind<128, 128>(a, split, states, s);

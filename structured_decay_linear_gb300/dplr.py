@@ -973,9 +973,10 @@ class HeadDecayPacked(_HeadDecayBase):
 
 
 def default_block(desc: dplr_hd_desc, requests: int) -> int:
-    """Tokens per block of a ragged batch: long enough that few requests need the extra pass over their keys and values
-    which every block but a request's last costs."""
-    return 1024
+    """Tokens per block of a ragged batch. Every block but a request's last costs an extra pass over its keys and values,
+    so blocks are long where the requests alone keep the GPU busy (two per SM and more), and short where a long request
+    has to be spread."""
+    return 2048 if requests * desc.H >= 304 else 512
 
 
 class HeadDecayDecode(_HeadDecayBase):
