@@ -247,6 +247,7 @@ dplr_status dplr_hd_forward(const dplr_hd_desc* desc, const dplr_hd_tensor* q, c
         sc.fwd = p.bound; sc.fwd_ext = S0; sc.gsum = p.gsum;
         HD_CUDA(launch_scan(sc, s));
         p.states_only = 0;
+        a.follows = 1;
     }
     p.ext_in = S0; p.ext_out = S_T;
     output(p, vo);
@@ -311,6 +312,7 @@ dplr_status dplr_hd_backward(const dplr_hd_desc* desc, const dplr_hd_tensor* q, 
         sc.fwd = at(pl.fwd); sc.fwd_ext = S0; sc.upto_end = 1;
         sc.bwd = at(pl.bwd); sc.bwd_ext = dST; sc.gsum = at(pl.gsum); sc.turned = 1;
         HD_CUDA(launch_scan(sc, s));
+        a.follows = 1;
     }
     const bool shared = desc->H != desc->Hq;
     auto partial = [&](Pass& p, size_t off) {      // shared heads: fp32 [B,H,T,dk], summed afterwards
@@ -406,6 +408,7 @@ dplr_status dplr_hd_forward_packed(const dplr_hd_desc* desc, int32_t R, int32_t 
     a.B = 1; a.bf16 = desc->in_dtype == DPLR_BF16; a.max_blocks = (int)max_blocks; a.npass = 1;
     a.status = static_cast<int*>(workspace);
     a.wait_cycles = wait_limit();
+    if (on_tensor_cores(desc)) HD_CUDA(cudaMemsetAsync(a.status + 16, 0, sizeof(int), s));     // the unit counter
     Pass& p = a.pass[0];
     p = base_pass(g, desc->dk, desc->dv, false, false);
     p.x = vq; p.y = vk; p.z = vv;
@@ -420,6 +423,7 @@ dplr_status dplr_hd_forward_packed(const dplr_hd_desc* desc, int32_t R, int32_t 
         sc.fwd = p.bound; sc.fwd_ext = S; sc.gsum = p.gsum;
         HD_CUDA(launch_scan(sc, s));
         p.states_only = 0;
+        a.follows = 1;
     }
     p.ext_in = S; p.ext_out = S;
     output(p, vo);

@@ -330,6 +330,8 @@ __device__ __forceinline__ void pass_nz(const Pass& p, const Geometry& geo, cons
 template <class IT>
 __global__ void __launch_bounds__(TH) hd_fp32_kernel(const __grid_constant__ Launch a, int zmax, long long bh) {
     extern __shared__ __align__(16) float sm[];
+    let_next_kernel_begin();
+    wait_for_kernel_before();
     const Pass& p = a.pass[blockIdx.y];
     const int zb = blockIdx.x % zmax;
     if (zb * (p.DZ == 32 ? 32 : 64) >= p.DZ) return;
@@ -368,9 +370,7 @@ cudaError_t launch_fp32(const Launch& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)n, (unsigned)a.npass);
     const long long bh = (long long)a.B * a.geo.H;
-    if (a.bf16) hd_fp32_kernel<__nv_bfloat16><<<grid, TH, bytes, s>>>(a, zmax, bh);
-    else hd_fp32_kernel<float><<<grid, TH, bytes, s>>>(a, zmax, bh);
-    return cudaGetLastError();
+    return launch_kernel(a.bf16 ? hd_fp32_kernel<__nv_bfloat16> : hd_fp32_kernel<float>, grid, TH, bytes, s, a.follows != 0, a, zmax, bh);
 }
 
 }  // namespace hd

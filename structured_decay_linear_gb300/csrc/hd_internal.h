@@ -22,6 +22,28 @@ namespace hd {
 constexpr int kChunk = 128;           // tokens that the tensor-core kernels compute together
 constexpr float kMinGate = -128.f;    // log-gates below this act like it: e^-128 is zero in fp32
 
+// Kernels of one call are launched so that the next begins while the one before still runs (programmatic dependent launch):
+// it sets itself up and reads the caller's inputs, and calls wait_for_kernel_before() in front of the first access to
+// anything that an earlier kernel of the call writes or reads for the last time. The first kernel of a call is an ordinary
+// launch. (Between two kernels of a call there were 5 us.)
+__device__ __forceinline__ void wait_for_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_kernel_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <class... P, class... A>
+cudaError_t launch_kernel(void (*f)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t s, bool follows, A&&... args) {
+    cudaLaunchConfig_t c = {};
+    c.gridDim = grid;
+    c.blockDim = dim3(block);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = at;
+    c.numAttrs = follows ? 1 : 0;
+    return cudaLaunchKernelEx(&c, f, static_cast<P>(args)...);
+}
+
 // One row sequence: element (b, h, t, i) at p + b sb + (h / div) sh + t st + i.
 struct View {
     const void* p;
@@ -111,8 +133,9 @@ struct Launch {
     int max_blocks;          // packed
     int npass;
     Pass pass[3];
-    int* status;
+    int* status;             // the workspace's status word; the word 16 behind it counts a ragged batch's units
     long long wait_cycles;
+    int follows;             // another kernel of the call goes before
 };
 
 cudaError_t launch_decode(const View& q, const View& k, const View& v, const float* g, long long gb, long long gh,
@@ -138,7 +161,7 @@ struct Scan {
     int turned;              // the boundary states are [dv][dk], the ext states [dk][dv]
     const float* gsum;
 };
-cudaError_t launch_scan(const Scan& a, cudaStream_t s);
+cudaError_t launch_scan(const Scan& a, cudaStream_t s);      // (follows the states pass)
 
 // ddecay from the per-token dots and the boundary states: with a_t = q_t . dq_t - k_t . dk_t and e the end of t's segment,
 //   ddecay_t = sum_{s=t..e} a_s + <S_e, dS_e>

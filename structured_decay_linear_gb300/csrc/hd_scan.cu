@@ -75,6 +75,8 @@ __device__ __forceinline__ void scan_row(const Scan& a, int row, int at, bool ba
 
 __global__ void __launch_bounds__(256) hd_scan_kernel(const __grid_constant__ Scan a, int rows) {
     const int at = (blockIdx.y * 256 + threadIdx.x) * 4;
+    let_next_kernel_begin();
+    wait_for_kernel_before();
     if (a.geo.blocks) {     // a ragged batch may have no request of two blocks: then there is nothing to do
         bool any = false;
         for (int r = threadIdx.x; r < a.R; r += 256) any |= a.geo.block_starts[r + 1] - a.geo.block_starts[r] > 1;
@@ -89,6 +91,8 @@ __global__ void __launch_bounds__(256) hd_gate_grad_kernel(const __grid_constant
     __shared__ double part[8];
     __shared__ double carry_s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    let_next_kernel_begin();
+    wait_for_kernel_before();
     const long long bh = blockIdx.x / a.nseg;
     const int seg = blockIdx.x % a.nseg;
     const int t0 = seg * a.L, n = min(a.L, a.T - t0);
@@ -168,6 +172,8 @@ __global__ void __launch_bounds__(256) hd_gate_grad_kernel(const __grid_constant
 // one warp per head: the sum of its segments, batch by batch
 __global__ void __launch_bounds__(32) hd_head_grad_kernel(const __grid_constant__ GateGrad a) {
     const int h = blockIdx.x, lane = threadIdx.x;
+    let_next_kernel_begin();
+    wait_for_kernel_before();
     double s = 0.0;
     for (int i = lane; i < a.B * a.nseg; i += 32)
         s += a.seg_sum[((long long)(i / a.nseg) * a.H + h) * a.nseg + i % a.nseg];
@@ -179,6 +185,8 @@ __global__ void __launch_bounds__(32) hd_head_grad_kernel(const __grid_constant_
 template <bool BF>
 __global__ void __launch_bounds__(256) hd_group_sum_kernel(const __grid_constant__ GroupSum a) {
     const int per = a.D / 4, group = a.H / a.Hq;
+    let_next_kernel_begin();
+    wait_for_kernel_before();
     const long long n = (long long)a.B * a.Hq * a.T * per;
     for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
         const int c = (int)(i % per) * 4;
@@ -210,16 +218,15 @@ cudaError_t launch_scan(const Scan& a, cudaStream_t s) {
     // a ragged batch's rows are mostly of one block, with nothing to do: few CTAs walk them (1600 rows of which none had
     // anything to do took 16 us as CTAs of their own)
     const long long most = a.geo.blocks ? 256 : rows;
-    hd_scan_kernel<<<dim3((unsigned)(rows < most ? rows : most), gy, gz), 256, 0, s>>>(a, (int)rows);
-    return cudaGetLastError();
+    return launch_kernel(hd_scan_kernel, dim3((unsigned)(rows < most ? rows : most), gy, gz), 256, 0, s, true, a, (int)rows);
 }
 
 cudaError_t launch_gate_grad(const GateGrad& a, cudaStream_t s) {
     const long long n = (long long)a.B * a.H * a.nseg;
     if (n >= (1LL << 31)) return cudaErrorInvalidValue;
-    hd_gate_grad_kernel<<<(unsigned)n, 256, 0, s>>>(a);
-    if (a.dg_head) hd_head_grad_kernel<<<(unsigned)a.H, 32, 0, s>>>(a);
-    return cudaGetLastError();
+    const cudaError_t e = launch_kernel(hd_gate_grad_kernel, dim3((unsigned)n), 256, 0, s, false, a);
+    if (e != cudaSuccess || !a.dg_head) return e;
+    return launch_kernel(hd_head_grad_kernel, dim3((unsigned)a.H), 32, 0, s, true, a);
 }
 
 cudaError_t launch_group_sum(const GroupSum& a, cudaStream_t s) {
@@ -227,9 +234,7 @@ cudaError_t launch_group_sum(const GroupSum& a, cudaStream_t s) {
     const long long most = (long long)sm_count() * 8;
     const long long blocks = (n + 255) / 256;
     const unsigned g = (unsigned)(blocks < most ? blocks : most);
-    if (a.bf16) hd_group_sum_kernel<true><<<g, 256, 0, s>>>(a);
-    else hd_group_sum_kernel<false><<<g, 256, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_kernel(a.bf16 ? hd_group_sum_kernel<true> : hd_group_sum_kernel<false>, dim3(g), 256, 0, s, true, a);
 }
 
 }  // namespace hd

@@ -34,8 +34,8 @@
 // every one is stored from registers.
 //
 // A pass for states only (the segments' own contributions) walks the chunks from the far end, so that the weights
-// e^{(gates behind the token)} need no rescaling of R: its accumulator is touched by MMAs alone, and all groups form
-// Y~.
+// e^{(gates behind the token)} need no rescaling of R: its accumulator is touched by MMAs alone. Sixteen warps
+// form Y~, and four bring finished states to memory while the next unit goes on in another accumulator.
 //
 // Bound: by the bytes of x, y, z and o (1 KB a token and head at 128 x 128): a chunk is 128 KB, 5.6 K cycles of its
 // share of HBM bandwidth on 152 SMs, against 2.6 K cycles of products and about 2.5 K of each group's work.
@@ -63,7 +63,7 @@ struct alignas(128) Args {
     CUtensorMap map[3][4];    // [pass][x, y, z, o]
     Launch l;
     int total;                // units of work: segments times passes
-    int* counter;             // null: units u = blockIdx.x, + gridDim.x, ..; else all but a CTA's first come from here (0 at first)
+    int* counter;             // (outputs of a ragged batch) a CTA's first unit is blockIdx.x, all others come from here (0 at first)
 };
 
 // What the gate warp says of a chunk, double-buffered; A_i: cumulative gates at the start of block i of 32 tokens (log2
@@ -310,8 +310,9 @@ __device__ __forceinline__ void store_state(float* state, bool turned, int r0, u
     }
 }
 
-// One unit of work: a segment in a pass. The gate warp finds a CTA's units and names them to the copy warp; a CTA's chunks
-// are numbered through, so that copies, gates and products of a unit run into those of the one before.
+// One unit of work: a segment in a pass. A CTA takes u = blockIdx.x, + gridDim.x, ..; of a ragged batch the gate warp finds
+// its units and names them to the copy warp. A CTA's chunks are numbered through, so that copies, gates and products of a
+// unit run into those of the one before.
 struct Work {
     const Pass* p;
     const CUtensorMap* maps;
@@ -323,11 +324,12 @@ struct Work {
 };
 
 // False: nothing to do.
-template <bool STATES>
+template <bool STATES, bool RAGGED>
 __device__ __forceinline__ bool find_work(const Args& a, int u, Work& w) {
     const int pi = u % a.l.npass;      // the passes of a segment side by side: they read the same rows
     w.p = &a.l.pass[pi];
     w.maps = a.map[pi];
+    __builtin_assume(RAGGED == (a.l.geo.blocks != nullptr));
     if (!locate(a.l.geo, u / a.l.npass, w.sg)) return false;
     w.rev = w.p->reverse;
     if (w.p->states_only == 1 && (w.rev ? w.sg.first : w.sg.last)) return false;
@@ -345,7 +347,9 @@ __device__ __forceinline__ const float* start_state(const Work& w) {
     return p.ext_in && !w.sg.fresh ? p.ext_in + w.sg.ext * (long long)(DX * DZ) : nullptr;
 }
 
-template <int DX, int DZ, bool SPLIT, bool STATES>
+// RAGGED: of a ragged batch, whose units are found in tables and shared out as the CTAs get done. A batch of equal lengths
+// has its own variant: with the table's branches in the unit loop its passes took 3 % longer (B4 H16 T4096, gradients 349 -> 335 us).
+template <int DX, int DZ, bool SPLIT, bool STATES, bool RAGGED>
 __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Args a) {
     using Ly = Layout<DX, DZ, SPLIT, STATES>;
     extern __shared__ __align__(1024) unsigned char smem[];
@@ -375,6 +379,9 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
     uint64_t* y_rest = bars + 20;    // B2: of the others
     uint64_t* p_ready = bars + 21;   // C: P
     uint64_t* o_free = bars + 22;    // O: Oi and Op read
+    // a states pass has no half R, P or outputs: R of even and odd chunks, and stored states of even and odd units
+    uint64_t* const r_states[2] = {r_done, r_half};
+    uint64_t* const state_out[2] = {o_free, p_ready};
     uint64_t* u_full = bars + 23;    // gates: the next unit's number (-1: none)
     uint64_t* u_free = bars + 24;    // copies: taken
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 25);
@@ -394,11 +401,12 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
             if (i == 15 || i == 16) n = kWorkers + 1;
             else if (i == 17 || (i >= 20 && i <= 22)) n = 4;
             else if (i == 18) n = 8;
-            else if (i == 19) n = STATES ? kWorkers : 4;
+            else if (i == 19) n = STATES ? kWorkers - 4 : 4;
             mbar_init(bars + i, n);
         }
         mbar_fence_init();
     }
+    let_next_kernel_begin();
     if (warp == 0) tmem_alloc(tmem_holder, kTmemCols);
     fence_before_sync();
     __syncthreads();
@@ -429,21 +437,24 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
         // =================== copies ===================
         if (lane == 0) {
             uint32_t it = 0, nx = 0, ny = 0, nz = 0;    // chunks; copies started
-            // the first unit is the CTA's own number's, if there is something to do; the gate warp names the others
+            constexpr bool by_name = RAGGED;       // all but the CTA's own number's, if that has work
             int u = blockIdx.x;
-            for (uint32_t named = 0; !failed; u = -1) {
+            for (uint32_t named = 0; !failed; u = by_name ? -1 : u + (int)gridDim.x) {
                 Work w;
-                if (u < 0 || !find_work<STATES>(a, u, w)) {
+                if (!by_name) {
+                    if (u >= a.total) break;
+                    if (!find_work<STATES, RAGGED>(a, u, w)) continue;
+                } else if (u < 0 || !find_work<STATES, RAGGED>(a, u, w)) {
                     if (!mbar_wait(u_full, named & 1, wl)) { failed = true; break; }
                     u = *next_unit;
                     if (u < 0) break;
                     mbar_arrive(u_free);       // (behind the branch: the load has returned)
                     ++named;
-                    find_work<STATES>(a, u, w);
+                    find_work<STATES, RAGGED>(a, u, w);
                 }
                 const CUtensorMap* maps = w.maps;
                 const int hx = w.sg.h / w.p->x.div, hy = w.sg.h / w.p->y.div, hz = w.sg.h / w.p->z.div, bb = w.sg.b;
-                if (const float* src = STATES ? nullptr : start_state<DX, DZ>(w))
+                if (const float* src = !STATES && it > 0 ? start_state<DX, DZ>(w) : nullptr)    // (the first: A is about to load it)
                     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" :: "l"(src), "r"(DX * DZ * 4) : "memory");
                 for (int j = 0; j < w.nchunk; ++j, ++it) {
                     const int t = w.sg.t0 + w.chunk(j) * C;
@@ -514,10 +525,11 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                 }
                 mma_commit(oi_done);
             };
+            uint32_t tm_r = tmem + TM_R;      // a states pass has two, in turn
             auto mma_R = [&](uint32_t buf, uint32_t tz, int half, bool acc) {      // 64 tokens: four slices of 2048 bytes
 #pragma unroll 1
                 for (int s = 0; s < 2; ++s)
-                    mma_chain(tmem + TM_R, smem_desc_sw128(sb + (s ? Ly::T_YL : Ly::T_YH) + buf * Ly::XB + 8192 * half, kHalf, 1024), 2048,
+                    mma_chain(tm_r, smem_desc_sw128(sb + (s ? Ly::T_YL : Ly::T_YH) + buf * Ly::XB + 8192 * half, kHalf, 1024), 2048,
                               smem_desc_sw128(tz + 8192 * half, kHalf, 1024), 2048, idR, 64, acc || s > 0);
             };
             auto mma_Op = [&](uint32_t tz) {
@@ -529,6 +541,7 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                         mma_bf16_tmem_a(tmem + TM_OP, tmem + TM_D + 32 * (ks >> 1) + 8 * (ks & 1) + 16 * s,
                                         dadd(dz, 2048 * ks), idO, (s > 0 || ks > 0) ? 1u : 0u);
             };
+            [[maybe_unused]] uint32_t unit = 0;       // (states pass) units begun
             for (uint32_t it = 0;; ++it) {
                 const uint32_t par = it & 1, s = it % Ly::NZ, zpar = (it / Ly::NZ) & 1;
                 const uint32_t tz = sb + Ly::T_Z + s * Ly::ZB;
@@ -537,11 +550,16 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                 if (flags & kEnd) break;
                 mbar_arrive(&g_free[par]);       // (behind the branch: the load has returned)
                 if (STATES) {
+                    if (flags & kFirst) {      // the accumulator of the unit before the last: once it has been stored
+                        if (unit >= 2 && !wait1(state_out[unit & 1], ((unit >> 1) - 1) & 1)) { failed = true; break; }
+                        tm_r = tmem + TM_R + (unit & 1) * 128;
+                        ++unit;
+                    }
                     if (!wait1(y_ready, par) || !wait1(&full_z[s], zpar)) { failed = true; break; }
                     mma_R(s, tz, 0, !(flags & kFirst));
                     mma_R(s, tz, 1, true);
                     mma_commit(&free_z[s]);
-                    mma_commit(r_done);
+                    mma_commit(r_states[par]);
                     continue;
                 }
                 if (!wait1(full_x, par) || !wait1(full_y, par)) { failed = true; break; }
@@ -584,9 +602,10 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
         };
         // a ragged batch's blocks end before its table does
         int total = a.total;
-        if (a.l.geo.blocks) total = min(total, a.l.geo.block_starts[a.l.geo.R] * a.l.geo.H * a.l.npass);
+        if (RAGGED) total = min(total, a.l.geo.block_starts[a.l.geo.R] * a.l.geo.H * a.l.npass);
         uint32_t named = 0;
         auto name = [&](int u) {          // tells the copy warp of a unit
+            if (!RAGGED) return;
             if (named > 0 && !wait(u_free, (named - 1) & 1)) { failed = true; return; }
             if (lane == 0) *next_unit = u;
             arrive(u_full);
@@ -595,10 +614,10 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
         int unit = blockIdx.x, after = 0;
         for (bool begun = false; unit < total && !failed; unit = after, begun = true) {
             Work w;
-            if (STATES && a.l.geo.blocks) {      // most of a ragged batch's requests have one block and no boundary: 32 at a time
+            if (STATES && RAGGED) {      // most of a ragged batch's requests have one block and no boundary: 32 at a time
                 Work v;
                 const int mine = unit + lane * (int)gridDim.x;
-                const uint32_t some = __ballot_sync(0xffffffffu, mine < total && find_work<STATES>(a, mine, v));
+                const uint32_t some = __ballot_sync(0xffffffffu, mine < total && find_work<STATES, RAGGED>(a, mine, v));
                 if (some == 0) {
                     after = unit + 32 * (int)gridDim.x;
                     continue;
@@ -608,10 +627,10 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                 begun |= skip > 0;
             }
             after = unit + (int)gridDim.x;
-            if (!STATES && a.counter && lane == 0) after = (int)gridDim.x + atomicAdd(a.counter, 1);
+            if (!STATES && RAGGED && lane == 0) after = (int)gridDim.x + atomicAdd(a.counter, 1);
             // An outputs pass has no unit without work: the next one is named as soon as this one's first chunk is out. In a
             // states pass a unit is named when it has been found to have some.
-            const bool some = find_work<STATES>(a, unit, w);
+            const bool some = find_work<STATES, RAGGED>(a, unit, w);
             if (STATES && some && begun) name(unit);
             if (!some || failed) continue;
             const Pass& p = *w.p;
@@ -626,8 +645,19 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
             };
             float cur[4], nxt[4];
             raw(0, cur);
+            // what the others need to know of the unit
+            const float* src = STATES ? nullptr : start_state<DX, DZ>(w);
+            float* dst = nullptr;
+            if (STATES) dst = p.bound + (rev ? w.sg.entry : w.sg.entry + w.sg.step) * (long long)(DX * DZ);
+            else if (p.ext_out && (rev ? w.sg.first : w.sg.last)) dst = p.ext_out + w.sg.ext * (long long)(DX * DZ);
+            const long long ostep = p.ot, wstep = p.w.st;
+            char* o = static_cast<char*>(p.o) + (w.sg.b * p.ob + w.sg.h * p.oh) * (p.o_f32 ? 4 : 2);
+            const __nv_bfloat16* wv = SPLIT ? static_cast<const __nv_bfloat16*>(p.w.p) + w.sg.b * p.w.sb + (w.sg.h / p.w.div) * p.w.sh : nullptr;
+            float* dots = SPLIT ? p.dots + ((long long)w.sg.b * a.l.geo.H + w.sg.h) * a.l.geo.T : nullptr;
             float* gsum = STATES && p.gsum ? p.gsum + w.sg.entry : nullptr;
-            int kind = 0;
+            const int kind = (rev ? kRev : 0) | ((p.bound && !w.sg.alone ? p.bound_turned : p.ext_turned) ? kTurned : 0) |
+                             ((STATES ? p.bound_turned : p.ext_turned) ? kOutTurned : 0) | (p.o_f32 ? kOutF32 : 0) |
+                             (((reinterpret_cast<uintptr_t>(o) | reinterpret_cast<uintptr_t>(wv)) & 31) == 0 && ((ostep | wstep) & 15) == 0 ? kWide : 0);
             long long passed = 0;    // gates of the chunks before
             float lost = 0.f;        // NaN once a gate was: it then reaches everything behind
             for (int j = 0; j < w.nchunk; ++j, ++it) {
@@ -674,33 +704,20 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                     g.re[lane] = ex2(real(rev ? all - ej : sj));
                 }
                 if (lane == 0) {
-                    // what the others need to know: of the unit, in either buffer once (not kept in registers: they spilled)
-                    if (j < 2) {
-                        const long long ostep = p.ot, wstep = p.w.st;
-                        char* o = static_cast<char*>(p.o) + (w.sg.b * p.ob + w.sg.h * p.oh) * (p.o_f32 ? 4 : 2);
-                        const __nv_bfloat16* wv = SPLIT ? static_cast<const __nv_bfloat16*>(p.w.p) + w.sg.b * p.w.sb +
-                                                              (w.sg.h / p.w.div) * p.w.sh : nullptr;
-                        kind = (rev ? kRev : 0) | ((p.bound && !w.sg.alone ? p.bound_turned : p.ext_turned) ? kTurned : 0) |
-                               ((STATES ? p.bound_turned : p.ext_turned) ? kOutTurned : 0) | (p.o_f32 ? kOutF32 : 0) |
-                               (((reinterpret_cast<uintptr_t>(o) | reinterpret_cast<uintptr_t>(wv)) & 31) == 0 &&
-                                ((ostep | wstep) & 15) == 0 ? kWide : 0);
-                        g.h = w.sg.h;
-                        g.b = w.sg.b;
-                        g.pass = (int)(w.p - a.l.pass);
-                        g.src = STATES ? nullptr : start_state<DX, DZ>(w);
-                        g.dst = nullptr;
-                        if (STATES) g.dst = p.bound + (rev ? w.sg.entry : w.sg.entry + w.sg.step) * (long long)(DX * DZ);
-                        else if (p.ext_out && (rev ? w.sg.first : w.sg.last)) g.dst = p.ext_out + w.sg.ext * (long long)(DX * DZ);
-                        g.o = o;
-                        g.w = wv;
-                        g.dots = SPLIT ? p.dots + ((long long)w.sg.b * a.l.geo.H + w.sg.h) * a.l.geo.T : nullptr;
-                        g.ostep = ostep;
-                        g.wstep = wstep;
-                    }
                     g.en = ex2(real(all)) + lost;
                     g.n = w.rows(j);
                     g.flags = kind | (j == 0 ? kFirst : 0) | (j == w.nchunk - 1 ? kLast : 0);
                     g.t0 = w.sg.t0 + w.chunk(j) * C;
+                    g.h = w.sg.h;
+                    g.b = w.sg.b;
+                    g.pass = (int)(w.p - a.l.pass);
+                    g.src = src;
+                    g.dst = dst;
+                    g.o = o;
+                    g.w = wv;
+                    g.dots = dots;
+                    g.ostep = ostep;
+                    g.wstep = wstep;
                 }
                 passed += all;
                 arrive(&g_full[it & 1]);
@@ -727,8 +744,9 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
         const int grp = warp >> 2;
         const uint32_t tr = sb + Ly::T_R, turn = tr + 4096 * rw;     // rows 32 rw .. of the R tile's first half: A's warp's own
         bool storing = false;      // (O, lane 0) a store may still read the warp's rows of the o tile
-        auto work = [&](auto role_) {      // one loop for each role: 0 A, 1 B1 and B2, 3 C, 4 O (a states pass: all the same)
+        auto work = [&](auto role_) {      // one loop for each role: 0 A, 1 B1 and B2, 3 C, 4 O (a states pass: 0 and 4)
         constexpr int role = decltype(role_)::value;
+        [[maybe_unused]] uint32_t unit = 0;       // (states pass) units done
         for (uint32_t it = 0;; ++it) {
             const uint32_t b = it & 1, s = it % Ly::NZ, zpar = (it / Ly::NZ) & 1;
             const GateBuf& g = gates[b];
@@ -780,23 +798,36 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
             if (flags & kEnd) break;
             [[maybe_unused]] const bool rev = flags & kRev;
             if constexpr (STATES) {
-                // ---- every worker: Y~; behind the last chunk A: the state
-                // (lo's buffer too is free once y has landed in its own: the copy waited for the product that read both)
-                if (!wait(&full_y[s], zpar) || (n < C && !wait(&full_z[s], zpar))) { failed = true; break; }
-                scale_rows<DX>(sb + Ly::T_Y + s * Ly::XB, sb + Ly::T_YH + s * Ly::XB, sb + Ly::T_YL + s * Ly::XB, g, n, tid, 32 * kWorkers);
-                if (n < C) clear_rows<DZ>(sb + Ly::T_Z + s * Ly::ZB, n, C, tid, 32 * kWorkers);
-                float* dst = g.dst;
-                fence_async_smem();
-                fence_before_sync();      // (the state of the unit before has been read)
-                arrive(y_ready);
-                give_back(&g_free[b], (uint32_t)(uintptr_t)dst);
-                if ((flags & kLast) && grp == 0 && (DX == 128 || warp < 2)) {
-                    if (!wait(r_done, b)) { failed = true; break; }
-                    store_state<DX, DZ>(dst, flags & kOutTurned, 32 * warp, turn, tmem + TM_R + lane_off);
+                if constexpr (role == 0) {
+                    // ---- sixteen warps: Y~
+                    // (lo's buffer too is free once y has landed in its own: the copy waited for the product that read both)
+                    if (!wait(&full_y[s], zpar) || (n < C && !wait(&full_z[s], zpar))) { failed = true; break; }
+                    scale_rows<DX>(sb + Ly::T_Y + s * Ly::XB, sb + Ly::T_YH + s * Ly::XB, sb + Ly::T_YL + s * Ly::XB, g, n, tid,
+                                   32 * (kWorkers - 4));
+                    if (n < C) clear_rows<DZ>(sb + Ly::T_Z + s * Ly::ZB, n, C, tid, 32 * (kWorkers - 4));
+                    fence_async_smem();
+                    arrive(y_ready);
+                    give_back(&g_free[b], 0);       // (what was loaded has gone into the rows)
+                } else {
+                    // ---- four warps: the state, behind a unit's last chunk
+                    if (flags & kLast) {
+                        // (given back after the wait: at most one later product can then have completed the other barrier)
+                        if (!wait(r_states[b], (it >> 1) & 1)) { failed = true; break; }
+                        float* dst = g.dst;
+                        give_back(&g_free[b], (uint32_t)(uintptr_t)dst);
+                        if (DX == 128 || rw < 2)
+                            store_state<DX, DZ>(dst, flags & kOutTurned, 32 * rw, turn, tmem + TM_R + (unit & 1) * 128 + lane_off);
+                        fence_before_sync();
+                        arrive(state_out[unit & 1]);
+                        ++unit;
+                    } else {
+                        give_back(&g_free[b], (uint32_t)flags);
+                    }
                 }
             } else if constexpr (role == 0) {
                 // ---- A: the state (thread = row of R; with DX = 64 two warps only keep step)
                 const bool mine = DX == 128 || warp < 2;
+                if (it == 0) wait_for_kernel_before();      // the states that it starts from; the other roles read inputs
                 if (it > 0 && (!wait(oi_done, b ^ 1) || !wait(r_done, b ^ 1))) { failed = true; break; }
                 const float en = g.en;
                 const float* src = g.src;
@@ -1052,7 +1083,8 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
         }
         };
         if constexpr (STATES) {
-            work(std::integral_constant<int, 0>{});
+            if (grp < 4) work(std::integral_constant<int, 0>{});
+            else work(std::integral_constant<int, 4>{});
         } else if (grp == 0) {
             work(std::integral_constant<int, 0>{});
         } else if (grp <= 2) {
@@ -1067,6 +1099,8 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
         }
         if (storing) bulk_wait_all();
         if (failed && lane == 0) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
+    } else {
+        wait_for_kernel_before();      // a CTA that finds nothing to do does not end before it either
     }
     fence_before_sync();
     __syncthreads();
@@ -1078,22 +1112,22 @@ bool map_rows(CUtensorMap* m, const View& v, int D, long long T, int heads, int 
     return tensor_map_rows(m, v.p, D, T, heads, B, v.st, v.sh, v.sb, rows);
 }
 
-template <int DX, int DZ, bool SPLIT, bool STATES>
+template <int DX, int DZ, bool SPLIT, bool STATES, bool RAGGED>
 cudaError_t run(const Args& a, cudaStream_t s) {
     static std::atomic<uint64_t> set{0};
     constexpr int bytes = Layout<DX, DZ, SPLIT, STATES>::TOTAL;
-    auto f = hd_tc_kernel<DX, DZ, SPLIT, STATES>;
+    auto f = hd_tc_kernel<DX, DZ, SPLIT, STATES, RAGGED>;
     const cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(f), bytes, set);
     if (e != cudaSuccess) return e;
     const int sms = sm_count();
-    f<<<(unsigned)(a.total < sms ? a.total : sms), NT, bytes, s>>>(a);
-    return cudaGetLastError();
+    return launch_kernel(f, dim3((unsigned)(a.total < sms ? a.total : sms)), NT, bytes, s, a.l.follows != 0, a);
 }
 
 template <int DX, int DZ>
 cudaError_t run_kind(const Args& a, bool split, bool states, cudaStream_t s) {
-    if (states) return run<DX, DZ, false, true>(a, s);
-    return split ? run<DX, DZ, true, false>(a, s) : run<DX, DZ, false, false>(a, s);
+    if (a.l.geo.blocks) return states ? run<DX, DZ, false, true, true>(a, s) : run<DX, DZ, false, false, true>(a, s);
+    if (states) return run<DX, DZ, false, true, false>(a, s);
+    return split ? run<DX, DZ, true, false, false>(a, s) : run<DX, DZ, false, false, false>(a, s);
 }
 
 }  // namespace
@@ -1133,11 +1167,8 @@ cudaError_t launch_tc(const Launch& l, cudaStream_t s) {
         a.total = (int)n * a.l.npass;
         // Lengths of a ragged batch differ: CTAs take their units as they get done with others. Which one takes a unit does
         // not touch its result.
-        if (l.geo.blocks && !q.states_only) {
-            a.counter = l.status + 16;
-            const cudaError_t e = cudaMemsetAsync(a.counter, 0, sizeof(int), s);
-            if (e != cudaSuccess) return e;
-        }
+        if (l.geo.blocks && !q.states_only) a.counter = l.status + 16;
+        if (i > 0) a.l.follows = 1;
         const bool split = q.dots != nullptr, states = q.states_only != 0;
         cudaError_t e;
         if (q.DX == 128 && q.DZ == 128) e = run_kind<128, 128>(a, split, states, s);
