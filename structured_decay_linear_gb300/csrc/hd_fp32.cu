@@ -41,6 +41,34 @@ template <> struct Vec<__nv_bfloat16> {
 
 __device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
+// Two fp32 numbers in a register pair: one instruction multiplies and adds both. The products below are bound by the
+// instructions that a scheduler can issue, of which this takes off a third.
+struct F4 { uint64_t a, b; };
+__device__ __forceinline__ F4 ld4x2(const float* p) {
+    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(p);
+    return F4{v.x, v.y};
+}
+__device__ __forceinline__ uint64_t both(float x) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float2 two(uint64_t a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+    return r;
+}
+
 // C rows of a row sequence (D features) on their way through registers: 16 bytes a piece, pieces spread over the threads.
 // take() starts the loads of the rows t .. t + n - 1 (the others are zero), put() writes them as fp32 to shared memory.
 template <class IT, int D, int LD>
@@ -99,25 +127,6 @@ __device__ __forceinline__ void segment_pass(const Pass& p, const Geometry& geo,
     const bool rev = p.reverse;
     const bool so = p.states_only;
 
-    // ---- the starting state
-    {
-        const float* src = nullptr;
-        bool turned = false;
-        if (!so) {
-            if (p.bound && !sg.alone) {
-                src = p.bound + (rev ? sg.entry + sg.step : sg.entry) * (long long)DX * p.DZ;
-                turned = p.bound_turned;
-            } else if (p.ext_in && !sg.fresh) {
-                src = p.ext_in + sg.ext * (long long)DX * p.DZ;
-                turned = p.ext_turned;
-            }
-        }
-        for (int i = tid; i < DX * NZ; i += TH) {
-            // walk the state along its contiguous axis
-            const int r = turned ? i % DX : i / NZ, c = turned ? i / DX : i % NZ;
-            S[r * LDZ + c] = src ? src[turned ? (z0 + c) * DX + r : r * p.DZ + z0 + c] : 0.f;
-        }
-    }
     float gsum = 0.f;
     const float* gp = p.g + sg.b * p.gb + sg.h * p.gh;
     const int nchunk = (sg.n + C - 1) / C;
@@ -138,6 +147,30 @@ __device__ __forceinline__ void segment_pass(const Pass& p, const Geometry& geo,
         gr = tid < n ? gp[(t + tid) * gs] : 0.f;      // (n <= 32)
     };
     take(0);
+    wait_for_kernel_before();
+    // ---- the starting state, along its contiguous axis
+    {
+        const float* src = nullptr;
+        bool turned = false;
+        if (!so) {
+            if (p.bound && !sg.alone) {
+                src = p.bound + (rev ? sg.entry + sg.step : sg.entry) * (long long)DX * p.DZ;
+                turned = p.bound_turned;
+            } else if (p.ext_in && !sg.fresh) {
+                src = p.ext_in + sg.ext * (long long)DX * p.DZ;
+                turned = p.ext_turned;
+            }
+        }
+        if (src && turned) {
+#pragma unroll 8
+            for (int i = tid; i < DX * NZ; i += TH) S[(i % DX) * LDZ + i / DX] = src[(z0 + i / DX) * DX + i % DX];
+        } else {
+#pragma unroll 4
+            for (int i = tid; i < DX * CG; i += TH)
+                *reinterpret_cast<float4*>(S + i / CG * LDZ + 4 * (i % CG)) =
+                    src ? ld4(src + i / CG * p.DZ + z0 + 4 * (i % CG)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    }
     for (int jj = 0; jj < nchunk; ++jj) {
         const int j = rev ? nchunk - 1 - jj : jj;
         const long long t0 = (long long)sg.t0 + j * C;
@@ -149,19 +182,26 @@ __device__ __forceinline__ void segment_pass(const Pass& p, const Geometry& geo,
         const float graw = gr;
         if (jj + 1 < nchunk) take(jj + 1);
         if (tid < 32) {
-            const float g0 = graw < kMinGate ? kMinGate : graw;
-            double g = g0;      // sums in 64 bits: after a gate of -100 those between later tokens still count
+            // Sums in fixed point (32 fractional bits, 64 in all): after a gate of -100 those between later tokens still
+            // count. 64-bit floating point is slow here: with it a chunk waited 4 us for this warp (T2001 66 -> 40 us).
+            const bool bad = !(graw <= 1e4f);      // NaN (gates are not positive; one that large is no gate either)
+            const uint32_t nan = __ballot_sync(0xffffffffu, bad);
+            long long g = __float2ll_rn((bad ? 0.f : graw < kMinGate ? kMinGate : graw) * 4294967296.f);
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
-                const double y = __shfl_up_sync(0xffffffffu, g, off);
+                const long long y = __shfl_up_sync(0xffffffffu, g, off);
                 if (tid >= off) g += y;
             }
-            const double gn = __shfl_sync(0xffffffffu, g, 31);
-            const float all = (float)gn, rest = (float)(gn - g);
-            G[tid] = (float)g;
-            GL[tid] = (float)(g - (double)(float)g);
-            W[tid] = __expf(rev ? (float)g : rest);
-            CX[tid] = __expf(rev ? rest : (float)g);
+            const long long gn = __shfl_sync(0xffffffffu, g, 31);
+            const float lost = __int_as_float(0x7fc00000), scale = 2.3283064365386963e-10f;     // 2^-32
+            const float any = nan ? lost : 0.f, upto = nan & (0xffffffffu >> (31 - tid)) ? lost : 0.f;
+            const float all = __ll2float_rn(gn) * scale + any, rest = __ll2float_rn(gn - g) * scale + any;
+            const float hi = __ll2float_rn(g);
+            const float up = hi * scale + upto;
+            G[tid] = up;
+            GL[tid] = __ll2float_rn(g - __float2ll_rn(hi)) * scale;
+            W[tid] = __expf(rev ? up : rest);
+            CX[tid] = __expf(rev ? rest : up);
             if (tid == 0) tot[0] = all;
         }
         __syncthreads();
@@ -170,15 +210,15 @@ __device__ __forceinline__ void segment_pass(const Pass& p, const Geometry& geo,
         if (!so) {
             // ---- P: rows r, r + 16 x columns c, c + 16
             const int r = tid >> 4, c = tid & 15;
-            float a[2][2] = {};
+            uint64_t a[2][2] = {};      // even and odd features
 #pragma unroll 8
             for (int i = 0; i < DX; i += 4) {
-                const float4 x0 = ld4(X + r * LDX + i), x1 = ld4(X + (r + 16) * LDX + i);
-                const float4 y0 = ld4(Y + c * LDX + i), y1 = ld4(Y + (c + 16) * LDX + i);
-                a[0][0] = fmaf(x0.x, y0.x, fmaf(x0.y, y0.y, fmaf(x0.z, y0.z, fmaf(x0.w, y0.w, a[0][0]))));
-                a[0][1] = fmaf(x0.x, y1.x, fmaf(x0.y, y1.y, fmaf(x0.z, y1.z, fmaf(x0.w, y1.w, a[0][1]))));
-                a[1][0] = fmaf(x1.x, y0.x, fmaf(x1.y, y0.y, fmaf(x1.z, y0.z, fmaf(x1.w, y0.w, a[1][0]))));
-                a[1][1] = fmaf(x1.x, y1.x, fmaf(x1.y, y1.y, fmaf(x1.z, y1.z, fmaf(x1.w, y1.w, a[1][1]))));
+                const F4 x0 = ld4x2(X + r * LDX + i), x1 = ld4x2(X + (r + 16) * LDX + i);
+                const F4 y0 = ld4x2(Y + c * LDX + i), y1 = ld4x2(Y + (c + 16) * LDX + i);
+                a[0][0] = fma2(x0.a, y0.a, fma2(x0.b, y0.b, a[0][0]));
+                a[0][1] = fma2(x0.a, y1.a, fma2(x0.b, y1.b, a[0][1]));
+                a[1][0] = fma2(x1.a, y0.a, fma2(x1.b, y0.b, a[1][0]));
+                a[1][1] = fma2(x1.a, y1.a, fma2(x1.b, y1.b, a[1][1]));
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e)
@@ -187,34 +227,34 @@ __device__ __forceinline__ void segment_pass(const Pass& p, const Geometry& geo,
                     const int rr = r + 16 * e, cc = c + 16 * f;
                     const bool in = rev ? cc >= rr : cc <= rr;
                     const float d = (G[rr] - G[cc]) + (GL[rr] - GL[cc]);
-                    P[rr * LDP + cc] = in ? a[e][f] * __expf(rev ? -d : d) : 0.f;
+                    const float2 v = two(a[e][f]);
+                    P[rr * LDP + cc] = in ? (v.x + v.y) * __expf(rev ? -d : d) : 0.f;
                 }
             __syncthreads();
             // ---- o: rows OR rg .. of 4 columns
-            float o[OR][4] = {};
+            F4 oo[OR] = {};
 #pragma unroll 4
             for (int i = 0; i < DX; i += 4) {
-                float4 s[4];
+                F4 s[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[e] = ld4(S + (i + e) * LDZ + c0);
+                for (int e = 0; e < 4; ++e) s[e] = ld4x2(S + (i + e) * LDZ + c0);
 #pragma unroll
                 for (int q = 0; q < OR; ++q) {
                     const float4 x = ld4(X + (OR * rg + q) * LDX + i);
                     const float xv[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        o[q][0] = fmaf(xv[e], s[e].x, o[q][0]);
-                        o[q][1] = fmaf(xv[e], s[e].y, o[q][1]);
-                        o[q][2] = fmaf(xv[e], s[e].z, o[q][2]);
-                        o[q][3] = fmaf(xv[e], s[e].w, o[q][3]);
+                        const uint64_t xx = both(xv[e]);
+                        oo[q].a = fma2(xx, s[e].a, oo[q].a);
+                        oo[q].b = fma2(xx, s[e].b, oo[q].b);
                     }
                 }
             }
 #pragma unroll
             for (int q = 0; q < OR; ++q) {
-                const float cx = CX[OR * rg + q];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[q][e] *= cx;
+                const uint64_t cx = both(CX[OR * rg + q]);
+                oo[q].a = mul2(cx, oo[q].a);
+                oo[q].b = mul2(cx, oo[q].b);
             }
             // tokens that a row does not see may hold anything: they are left out, not multiplied by zero. First those that
             // all of the thread's rows see, then the few between its rows.
@@ -223,28 +263,24 @@ __device__ __forceinline__ void segment_pass(const Pass& p, const Geometry& geo,
                 const float* Pr = P + OR * rg * LDP;
 #pragma unroll 4
                 for (int u = lo; u < hi; ++u) {
-                    const float4 z = ld4(Z + u * LDZ + c0);
+                    const F4 z = ld4x2(Z + u * LDZ + c0);
 #pragma unroll
                     for (int q = 0; q < OR; ++q) {
-                        const float w = Pr[q * LDP + u];
-                        o[q][0] = fmaf(w, z.x, o[q][0]);
-                        o[q][1] = fmaf(w, z.y, o[q][1]);
-                        o[q][2] = fmaf(w, z.z, o[q][2]);
-                        o[q][3] = fmaf(w, z.w, o[q][3]);
+                        const uint64_t w = both(Pr[q * LDP + u]);
+                        oo[q].a = fma2(w, z.a, oo[q].a);
+                        oo[q].b = fma2(w, z.b, oo[q].b);
                     }
                 }
 #pragma unroll
                 for (int k = 1; k < OR; ++k) {        // forward: token OR rg + k, seen by rows k ..; backward: token
                     const int u = rev ? OR * rg + OR - 1 - k : OR * rg + k;      // OR rg + OR - 1 - k, by rows 0 .. OR - 1 - k
-                    const float4 z = ld4(Z + u * LDZ + c0);
+                    const F4 z = ld4x2(Z + u * LDZ + c0);
 #pragma unroll
                     for (int q = 0; q < OR; ++q) {
                         const bool in = rev ? q <= OR - 1 - k : q >= k;
-                        const float w = Pr[q * LDP + u];
-                        o[q][0] = in ? fmaf(w, z.x, o[q][0]) : o[q][0];
-                        o[q][1] = in ? fmaf(w, z.y, o[q][1]) : o[q][1];
-                        o[q][2] = in ? fmaf(w, z.z, o[q][2]) : o[q][2];
-                        o[q][3] = in ? fmaf(w, z.w, o[q][3]) : o[q][3];
+                        const uint64_t w = both(Pr[q * LDP + u]);
+                        oo[q].a = in ? fma2(w, z.a, oo[q].a) : oo[q].a;
+                        oo[q].b = in ? fma2(w, z.b, oo[q].b) : oo[q].b;
                     }
                 }
             }
@@ -252,13 +288,15 @@ __device__ __forceinline__ void segment_pass(const Pass& p, const Geometry& geo,
             for (int q = 0; q < OR; ++q) {
                 const int rr = OR * rg + q;
                 const long long t = t0 + rr;
-                if (rr < n) store4<IT>(p.o, sg.b * p.ob + sg.h * p.oh + t * p.ot + z0 + c0, o[q], p.o_f32);
+                const float2 oa = two(oo[q].a), ob = two(oo[q].b);
+                const float o[4] = {oa.x, oa.y, ob.x, ob.y};
+                if (rr < n) store4<IT>(p.o, sg.b * p.ob + sg.h * p.oh + t * p.ot + z0 + c0, o, p.o_f32);
                 if (p.dots) {
                     float d = 0.f;
                     if (rr < n) {
                         const IT* w = static_cast<const IT*>(p.w.p) + sg.b * p.w.sb + (sg.h / p.w.div) * p.w.sh + t * p.w.st + z0 + c0;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) d = fmaf(o[q][e], static_cast<float>(w[e]), d);
+                        for (int e = 0; e < 4; ++e) d = fmaf(o[e], static_cast<float>(w[e]), d);
                     }
 #pragma unroll
                     for (int off = CG / 2; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
@@ -270,18 +308,20 @@ __device__ __forceinline__ void segment_pass(const Pass& p, const Geometry& geo,
         }
         // ---- the state: rows SR rg .. of 4 columns
         {
-            float a[SR][4];
-            const float e = __expf(all);
+            F4 a[SR];
+            const uint64_t e = both(__expf(all));
 #pragma unroll
             for (int q = 0; q < SR; ++q) {
-                const float4 s = ld4(S + (SR * rg + q) * LDZ + c0);
-                a[q][0] = e * s.x; a[q][1] = e * s.y; a[q][2] = e * s.z; a[q][3] = e * s.w;
+                const F4 s = ld4x2(S + (SR * rg + q) * LDZ + c0);
+                a[q].a = mul2(e, s.a);
+                a[q].b = mul2(e, s.b);
             }
 #pragma unroll 4
             for (int u = 0; u < C; ++u) {      // (rows behind the last token are zero)
-                const float w = W[u];
-                float4 z = ld4(Z + u * LDZ + c0);
-                z.x *= w; z.y *= w; z.z *= w; z.w *= w;
+                const uint64_t w = both(W[u]);
+                F4 z = ld4x2(Z + u * LDZ + c0);
+                z.a = mul2(w, z.a);
+                z.b = mul2(w, z.b);
                 float y[SR];
                 if constexpr (SR % 4 == 0) {
 #pragma unroll
@@ -295,15 +335,14 @@ __device__ __forceinline__ void segment_pass(const Pass& p, const Geometry& geo,
                 }
 #pragma unroll
                 for (int q = 0; q < SR; ++q) {
-                    a[q][0] = fmaf(y[q], z.x, a[q][0]);
-                    a[q][1] = fmaf(y[q], z.y, a[q][1]);
-                    a[q][2] = fmaf(y[q], z.z, a[q][2]);
-                    a[q][3] = fmaf(y[q], z.w, a[q][3]);
+                    const uint64_t yy = both(y[q]);
+                    a[q].a = fma2(yy, z.a, a[q].a);
+                    a[q].b = fma2(yy, z.b, a[q].b);
                 }
             }
 #pragma unroll
             for (int q = 0; q < SR; ++q)
-                *reinterpret_cast<float4*>(S + (SR * rg + q) * LDZ + c0) = make_float4(a[q][0], a[q][1], a[q][2], a[q][3]);
+                *reinterpret_cast<ulonglong2*>(S + (SR * rg + q) * LDZ + c0) = make_ulonglong2(a[q].a, a[q].b);
         }
     }
     __syncthreads();
@@ -331,13 +370,14 @@ template <class IT>
 __global__ void __launch_bounds__(TH) hd_fp32_kernel(const __grid_constant__ Launch a, int zmax, long long bh) {
     extern __shared__ __align__(16) float sm[];
     let_next_kernel_begin();
-    wait_for_kernel_before();
     const Pass& p = a.pass[blockIdx.y];
     const int zb = blockIdx.x % zmax;
-    if (zb * (p.DZ == 32 ? 32 : 64) >= p.DZ) return;
     Segment sg;
-    if (!locate(a.geo, blockIdx.x / zmax, sg)) return;
-    if (p.states_only == 1 && (p.reverse ? sg.first : sg.last)) return;
+    if (zb * (p.DZ == 32 ? 32 : 64) >= p.DZ || !locate(a.geo, blockIdx.x / zmax, sg) ||
+        (p.states_only == 1 && (p.reverse ? sg.first : sg.last))) {
+        wait_for_kernel_before();      // a kernel of which no CTA waited would end before the one before it
+        return;
+    }
     switch (p.DX) {
         case 32: pass_nz<IT, 32>(p, a.geo, sg, zb, bh, sm); break;
         case 64: pass_nz<IT, 64>(p, a.geo, sg, zb, bh, sm); break;

@@ -11,7 +11,9 @@ namespace {
 
 constexpr int TH = 512;
 constexpr int kMaxRequests = 8192, kMaxSlots = 1 << 20;
-constexpr int kRows = 2 * TH;     // rows of the batch that a CTA fills in one turn
+constexpr int E = 4;              // requests that a thread scans in one turn
+constexpr int V = 4;              // rows that a thread fills
+constexpr int kRows = V * TH;     // rows of the batch that a CTA fills in one turn
 
 struct PlanArgs {
     int R, cap, block, nslots, nblocks;
@@ -64,24 +66,39 @@ __global__ void __launch_bounds__(TH) hd_plan_kernel(PlanArgs a) {
     __syncthreads();
     bool bad = false;
     long long rows = 0, blocks = 0;
-    for (int r0 = 0; r0 < a.R; r0 += TH) {
-        const int r = r0 + tid;
-        int n = 0;
-        if (r < a.R) {
-            n = a.lengths[r];
-            const int c = a.context[r];
-            if (n < 0 || n > a.cap || c < 0 || (long long)c + n > 2147483647LL) { bad = true; n = 0; }
-            if (n > 0) {
-                const int s = a.slots[r];
-                if (s < 0 || s >= a.nslots) bad = true;
-                else if (atomicOr(&seen[s >> 5], 1u << (s & 31)) & (1u << (s & 31))) bad = true;
+    for (int r0 = 0; r0 < a.R; r0 += E * TH) {     // E requests a thread: one turn up to 2048
+        const int r = r0 + E * tid;
+        int n[E], c[E], s[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            n[i] = r + i < a.R ? a.lengths[r + i] : 0;
+            c[i] = r + i < a.R ? a.context[r + i] : 0;
+            s[i] = r + i < a.R ? a.slots[r + i] : 0;
+        }
+        long long sn = 0, sb = 0;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            if (n[i] < 0 || n[i] > a.cap || c[i] < 0 || (long long)c[i] + n[i] > 2147483647LL) { bad = true; n[i] = 0; }
+            if (n[i] > 0) {
+                if (s[i] < 0 || s[i] >= a.nslots) bad = true;
+                else if (atomicOr(&seen[s[i] >> 5], 1u << (s[i] & 31)) & (1u << (s[i] & 31))) bad = true;
             }
+            c[i] = (n[i] + a.block - 1) / a.block;
+            sn += n[i];
+            sb += c[i];
         }
         long long en, eb, tn, tb;
-        scan2(n, (n + a.block - 1) / a.block, sh, en, eb, tn, tb);
-        if (r < a.R) {
-            st[r] = (int)min(rows + en, (long long)a.cap);
-            bs[r] = (int)min(blocks + eb, (long long)a.nblocks);
+        scan2(sn, sb, sh, en, eb, tn, tb);
+        en += rows;
+        eb += blocks;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            if (r + i < a.R) {
+                st[r + i] = (int)min(en, (long long)a.cap);
+                bs[r + i] = (int)min(eb, (long long)a.nblocks);
+            }
+            en += n[i];
+            eb += c[i];
         }
         rows += tn;
         blocks += tb;
@@ -107,15 +124,35 @@ __global__ void __launch_bounds__(TH) hd_plan_kernel(PlanArgs a) {
         }
         a.blocks[i] = e;
     }
-    for (int t = blockIdx.x * TH + tid; t < a.cap; t += stride) {
-        int slot = -1, pos = -1;
-        if (t < rows) {
-            const int r = find(st, a.R, t);
-            slot = a.slots[r];
-            pos = a.context[r] + (t - st[r]);
+    // V rows next to one another to a thread: one bisection, then on from request to request
+    const bool wide = ((reinterpret_cast<uintptr_t>(a.token_slot) | reinterpret_cast<uintptr_t>(a.token_pos)) & 15) == 0;
+    for (int t0 = V * (blockIdx.x * TH + tid); t0 < a.cap; t0 += V * stride) {
+        int slot[V], pos[V];
+        int r = t0 < rows ? find(st, a.R, t0) : 0;
+        int s = -1, c = 0, begin = 0, end = 0;      // of request r, once read
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int t = t0 + i;
+            slot[i] = pos[i] = -1;
+            if (t >= rows) continue;
+            if (t >= end) {
+                while (st[r + 1] <= t) ++r;          // (t < rows = st[R])
+                begin = st[r];
+                end = st[r + 1];
+                s = a.slots[r];
+                c = a.context[r];
+            }
+            slot[i] = s;
+            pos[i] = c + (t - begin);
         }
-        a.token_slot[t] = slot;
-        a.token_pos[t] = pos;
+        if (wide && t0 + V <= a.cap) {
+            *reinterpret_cast<int4*>(a.token_slot + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+            *reinterpret_cast<int4*>(a.token_pos + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (t0 + i < a.cap) { a.token_slot[t0 + i] = slot[i]; a.token_pos[t0 + i] = pos[i]; }
+        }
     }
 }
 
