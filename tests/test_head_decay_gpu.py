@@ -585,3 +585,175 @@ def test_bindings_refuse(sdl):
     z = torch.zeros(8, 1, 32, device="cuda")
     with pytest.raises(ValueError):        # no tables yet
         p(z, z, z, torch.zeros(8, 1, device="cuda"), torch.zeros(2, 1, 32, 32, device="cuda"))
+
+
+# ---- calls at the edges
+
+@pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 128), ("bf16", 64)])
+@pytest.mark.parametrize("T", [100, 700, 1500])
+def test_state_in_place(sdl, dtype, d, T):
+    """A prepared forward fed with its own S_T: one segment and several give the bits of a call that keeps S0."""
+    import torch
+    x = make(dtype, 1, 2, 1, T, d, d, seed=40)
+    f = sdl.HeadDecay(x["q"].dtype, 1, 2, T, d, d, q_heads=1)
+    o, S_T = (t.clone() for t in f(**x))
+    for _ in range(3):
+        f.S_T.copy_(x["S0"])
+        y = dict(x, S0=f.S_T)
+        o2, S2 = f(**y)
+        assert torch.equal(o, o2) and torch.equal(S_T, S2)
+
+
+@pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 128), ("bf16", 64)])
+def test_rows_on_sixteen_byte_steps(sdl, dtype, d):
+    """Rows whose strides are odd multiples of 16 bytes give the bits of contiguous ones, gradients included."""
+    import torch
+    x = make(dtype, 2, 2, 1, 260, d, d, seed=41)
+    dt, pad = x["q"].dtype, 8 if dtype == "bf16" else 4
+    dO = torch.randn(2, 2, 260, d, device="cuda").to(dt)
+    dST = torch.randn(2, 2, d, d, device="cuda")
+    apart = lambda t: torch.full((*t.shape[:-1], d + pad), 7.0, device="cuda", dtype=dt)[..., :d].copy_(t)  # noqa: E731
+    y = {n: apart(t) if n in "qkv" else t for n, t in x.items()}
+    f = sdl.HeadDecay(dt, 2, 2, 260, d, d, q_heads=1)
+    b = sdl.HeadDecayBackward(dt, 2, 2, 260, d, d, q_heads=1)
+    first = [t.clone() for t in f(**x)]
+    assert all(torch.equal(p, q) for p, q in zip(first, f(**y)))
+    grads = {n: t.clone() for n, t in b(dO, dST, **x).items()}
+    again = b(apart(dO), dST, **y)
+    assert all(torch.equal(grads[n], again[n]) for n in grads)
+
+
+@pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 128)])
+def test_a_gate_that_is_no_number(sdl, dtype, d):
+    """A NaN among a head's gates reaches everything behind it and no other head; chunks before it stay as they were."""
+    import torch
+    x = make(dtype, 1, 3, 3, 700, d, d, seed=42)
+    f = sdl.HeadDecay(x["q"].dtype, 1, 3, 700, d, d)
+    o, S = (t.clone() for t in f(**x))
+    x["decay"][0, 1, 400] = float("nan")
+    o2, S2 = f(**x)
+    assert torch.equal(o[:, ::2], o2[:, ::2]) and torch.equal(S[:, ::2], S2[:, ::2])
+    assert torch.equal(o[0, 1, :384], o2[0, 1, :384])
+    assert torch.isnan(o2[0, 1, 400:]).all() and torch.isnan(S2[0, 1]).all()
+
+
+@pytest.mark.parametrize("B,H,Hq,T,dk,dv", [(3, 2, 1, 129, 128, 128), (1, 6, 2, 700, 64, 128), (2, 2, 2, 513, 128, 64),
+                                            (1, 40, 40, 1100, 64, 64)])
+def test_gradients_give_the_same_bits_every_time(sdl, B, H, Hq, T, dk, dv):
+    """Fresh and used workspaces, with the memory between filled with NaN: nothing depends on timing or on what was there."""
+    import torch
+    x = make("bf16", B, H, Hq, T, dk, dv, seed=43)
+    dO = torch.randn(B, H, T, dv, device="cuda").bfloat16()
+    dST = torch.randn(B, H, dk, dv, device="cuda")
+    first = None
+    for _ in range(4):
+        junk = [torch.full((1 << 24,), float("nan"), device="cuda") for _ in range(3)]
+        del junk
+        b = sdl.HeadDecayBackward(torch.bfloat16, B, H, T, dk, dv, q_heads=Hq)
+        for _ in range(6):
+            got = b(dO, dST, **x)
+            first = first or {n: t.clone() for n, t in got.items()}
+            assert all(torch.equal(first[n], got[n]) for n in first)
+
+
+def test_offsets_past_32_bits(sdl):
+    """Sequences, and a pool of states, of over 2^31 elements. With gates of -0.5 or less what lies 400 tokens back has
+    faded to e^-200, so the last tokens are those of a short sequence."""
+    import torch
+    H, T, d, tail = 16, 1 << 20, 128, 512
+    g = torch.Generator(device="cuda").manual_seed(44)
+    rows = lambda: torch.randn(1, T + 300, H, d, device="cuda", generator=g, dtype=torch.bfloat16).transpose(1, 2)  # noqa: E731
+    x = dict(q=rows() * d ** -0.5, k=rows() * d ** -0.5, v=rows())
+    x["decay"] = -0.5 - torch.rand(1, H, T + 300, device="cuda", generator=g)
+    assert x["q"].numel() > 2 ** 31
+    f = sdl.HeadDecay(torch.bfloat16, 1, H, T + 300, d, d, token_major=True)
+    o, S_T = f(**x)
+    heads = slice(14, 16)
+    y = {n: t[:, heads, -1024:] for n, t in x.items()}
+    o_ref, S_ref, size, A = want(y)
+    check_forward("bf16", o[:, heads, -tail:], S_T[:, heads], (o_ref[:, :, -tail:], S_ref, size[:, :, -tail:], A))
+    del f, o, S_T, x, y
+    slots = 8200
+    pool = torch.zeros(slots, H, d, d, device="cuda")
+    assert pool.numel() > 2 ** 31
+    z = make("bf16", 3, H, H, 1, d, d, seed=45)
+    at = torch.tensor([slots - 1, 0, 8191], device="cuda", dtype=torch.int32)
+    pool[at.long()] = z["S0"]
+    dec = sdl.HeadDecayDecode(torch.bfloat16, 3, H, d, d, slots)
+    od = dec(z["q"][:, :, 0], z["k"][:, :, 0], z["v"][:, :, 0], z["decay"][:, :, 0], pool, at)
+    check_forward("bf16", od[:, :, None], pool[at.long()], want(z))
+    # a request of two segments and one of a single token on the pool's last states
+    lengths, n = [600, 1], 601
+    w, cap = ragged("bf16", lengths, H, H, d, d, 0, False, seed=46)
+    p = sdl.HeadDecayPacked(torch.bfloat16, 2, cap, slots, H, d, d, plan=sdl.RequestPlan(2, cap, slots, 256))
+    i32 = lambda *v: torch.tensor(v, device="cuda", dtype=torch.int32)  # noqa: E731
+    before = pool[[slots - 1, 8191]].clone()
+    p.plan(i32(*lengths), i32(slots - 1, 8191), i32(5, 5))
+    op = p(w["q"], w["k"], w["v"], w["decay"], pool)
+    for r, (a, b, s) in enumerate(((0, 600, slots - 1), (600, n, 8191))):
+        u = {name: t[a:b].transpose(0, 1)[None] for name, t in w.items()}
+        u["S0"] = before[r][None]
+        check_forward("bf16", op[a:b].transpose(0, 1)[None], pool[s][None], want(u))
+
+
+def test_many_requests(sdl):
+    """As many requests as the tables take, most of one token, each on a state of its own, twice with other lengths."""
+    import torch
+    R, H, d = 8192, 1, 64
+    gen = torch.Generator().manual_seed(47)
+    p = sdl.HeadDecayPacked(torch.bfloat16, R, 3 * R, R, H, d, d)
+    x, cap = ragged("bf16", [3 * R], H, H, d, d, 0, False, seed=48)
+    slot = torch.randperm(R, generator=gen).int()
+    zero = torch.zeros(R, dtype=torch.int32, device="cuda")
+    for _ in range(2):
+        n = torch.randint(0, 4, (R,), generator=gen)
+        n[17] = 300
+        n = torch.minimum(n, (cap - n.cumsum(0) + n).clamp(min=0))
+        pool = torch.zeros(R, H, d, d, device="cuda")
+        p.plan(n.int().cuda(), slot.cuda(), zero)
+        o = p(x["q"], x["k"], x["v"], x["decay"], pool)
+        assert p.plan.device_status() == 0 and p.device_status() == 0
+        starts = n.cumsum(0) - n
+        for r in (0, 16, 17, 18, 4095, 8190, 8191):
+            a, b = int(starts[r]), int(starts[r] + n[r])
+            if a == b:
+                assert not pool[int(slot[r])].any()
+                continue
+            u = {name: t[a:b].transpose(0, 1)[None] for name, t in x.items()}
+            check_forward("bf16", o[a:b].transpose(0, 1)[None], pool[int(slot[r])][None], want(u))
+
+
+@pytest.mark.parametrize("what", ["forward", "backward", "packed"])
+def test_waits_that_give_up_are_reported(sdl, what):
+    """Waits limited to 1000 cycles: the first product of a chunk takes longer, so some wait gives up. The kernels end and
+    report it, and with the usual limit the same object is right again."""
+    import torch
+    T, d = 700, 128
+    x = make("bf16", 1, 2, 2, T, d, d, state=False, seed=49)
+    if what == "forward":
+        f = sdl.HeadDecay(torch.bfloat16, 1, 2, T, d, d)
+        call = lambda: dict(zip("oS", f(**x)))  # noqa: E731
+    elif what == "backward":
+        f = sdl.HeadDecayBackward(torch.bfloat16, 1, 2, T, d, d)
+        dO = torch.randn(1, 2, T, d, device="cuda").bfloat16()
+        call = lambda: f(dO, None, **x)  # noqa: E731
+    else:
+        f = sdl.HeadDecayPacked(torch.bfloat16, 2, T, 2, 2, d, d, plan=sdl.RequestPlan(2, T, 2, 256))
+        i32 = lambda *v: torch.tensor(v, device="cuda", dtype=torch.int32)  # noqa: E731
+        f.plan(i32(600, 100), i32(1, 0), i32(0, 0))
+        y = {n: t[0].transpose(0, 1).contiguous() for n, t in x.items()}
+
+        def call():
+            pool = torch.zeros(2, 2, d, d, device="cuda")
+            return {"o": f(y["q"], y["k"], y["v"], y["decay"], pool), "S": pool}
+    first = {n: t.clone() for n, t in call().items()}
+    assert f.device_status() == 0
+    sdl.dplr_la_set_wait_limit(1000)
+    try:
+        call()
+        torch.cuda.synchronize()
+        assert f.device_status(clear=True) == sdl.dplr.DPLR_ERR_TIMEOUT
+    finally:
+        sdl.dplr_la_set_wait_limit(0)
+    got = call()
+    assert f.device_status() == 0 and all(torch.equal(first[n], got[n]) for n in first)
