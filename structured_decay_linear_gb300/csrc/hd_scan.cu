@@ -11,7 +11,7 @@ namespace {
 
 // ---- boundary states: one thread per four elements of one (sequence, head)'s state, walking its segments. The loads
 // of the contributions do not depend on the chain, so four are in flight at a time.
-constexpr int kAhead = 4;
+constexpr int kAhead = 4;      // (eight: 4 us off a scan of 16 segments, 3 us on one of four, whose kernel then starts later)
 
 __device__ __forceinline__ void scan_row(const Scan& a, int row, int at, bool back) {
     const long long size = (long long)a.dk * a.dv;

@@ -375,11 +375,14 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
     uint64_t* g_free = bars + 15;    // [2] every worker warp and the issuer
     uint64_t* r_ready = bars + 17;   // A: R scaled, its bf16 copy written
     uint64_t* y_read = bars + 18;    // B1, B2: the y tile is in their registers
-    uint64_t* y_ready = bars + 19;   // B1: Y~ of the first 64 tokens (a states pass: of all, every worker)
+    uint64_t* y_ready = bars + 19;   // B1: Y~ of the first 64 tokens
     uint64_t* y_rest = bars + 20;    // B2: of the others
     uint64_t* p_ready = bars + 21;   // C: P
     uint64_t* o_free = bars + 22;    // O: Oi and Op read
-    // a states pass has no half R, P or outputs: R of even and odd chunks, and stored states of even and odd units
+    // A states pass has no halves, P or outputs: Y~ and R of even and odd chunks, stored states of even and odd units. (Two
+    // barriers each: while the issuer waits for a state to be stored, Y~ of the next chunk may be handed on as well, and a
+    // wait for a phase takes the one after the next for it.)
+    uint64_t* const y_states[2] = {y_ready, y_rest};
     uint64_t* const r_states[2] = {r_done, r_half};
     uint64_t* const state_out[2] = {o_free, p_ready};
     uint64_t* u_full = bars + 23;    // gates: the next unit's number (-1: none)
@@ -399,9 +402,9 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
         for (int i = 0; i < 25; ++i) {
             uint32_t n = 1;
             if (i == 15 || i == 16) n = kWorkers + 1;
-            else if (i == 17 || (i >= 20 && i <= 22)) n = 4;
+            else if (STATES && (i == 19 || i == 20)) n = kWorkers - 4;
+            else if (i == 17 || (i >= 19 && i <= 22)) n = 4;
             else if (i == 18) n = 8;
-            else if (i == 19) n = STATES ? kWorkers - 4 : 4;
             mbar_init(bars + i, n);
         }
         mbar_fence_init();
@@ -555,7 +558,7 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                         tm_r = tmem + TM_R + (unit & 1) * 128;
                         ++unit;
                     }
-                    if (!wait1(y_ready, par) || !wait1(&full_z[s], zpar)) { failed = true; break; }
+                    if (!wait1(y_states[par], (it >> 1) & 1) || !wait1(&full_z[s], zpar)) { failed = true; break; }
                     mma_R(s, tz, 0, !(flags & kFirst));
                     mma_R(s, tz, 1, true);
                     mma_commit(&free_z[s]);
@@ -806,22 +809,21 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                                    32 * (kWorkers - 4));
                     if (n < C) clear_rows<DZ>(sb + Ly::T_Z + s * Ly::ZB, n, C, tid, 32 * (kWorkers - 4));
                     fence_async_smem();
-                    arrive(y_ready);
+                    arrive(y_states[b]);
                     give_back(&g_free[b], 0);       // (what was loaded has gone into the rows)
                 } else {
                     // ---- four warps: the state, behind a unit's last chunk
+                    // (Every product is waited for, and the gates given back behind that: the barrier is then neither a
+                    // product behind nor one ahead of the one that is asked for.)
+                    if (!wait(r_states[b], (it >> 1) & 1)) { failed = true; break; }
+                    float* dst = g.dst;
+                    give_back(&g_free[b], (uint32_t)(uintptr_t)dst);
                     if (flags & kLast) {
-                        // (given back after the wait: at most one later product can then have completed the other barrier)
-                        if (!wait(r_states[b], (it >> 1) & 1)) { failed = true; break; }
-                        float* dst = g.dst;
-                        give_back(&g_free[b], (uint32_t)(uintptr_t)dst);
                         if (DX == 128 || rw < 2)
                             store_state<DX, DZ>(dst, flags & kOutTurned, 32 * rw, turn, tmem + TM_R + (unit & 1) * 128 + lane_off);
                         fence_before_sync();
                         arrive(state_out[unit & 1]);
                         ++unit;
-                    } else {
-                        give_back(&g_free[b], (uint32_t)flags);
                     }
                 }
             } else if constexpr (role == 0) {

@@ -638,7 +638,7 @@ def test_a_gate_that_is_no_number(sdl, dtype, d):
 
 
 @pytest.mark.parametrize("B,H,Hq,T,dk,dv", [(3, 2, 1, 129, 128, 128), (1, 6, 2, 700, 64, 128), (2, 2, 2, 513, 128, 64),
-                                            (1, 40, 40, 1100, 64, 64)])
+                                            (1, 40, 40, 1100, 64, 64), (4, 16, 16, 2048, 128, 128), (2, 32, 16, 2500, 64, 128)])
 def test_gradients_give_the_same_bits_every_time(sdl, B, H, Hq, T, dk, dv):
     """Fresh and used workspaces, with the memory between filled with NaN: nothing depends on timing or on what was there."""
     import torch
@@ -654,6 +654,24 @@ def test_gradients_give_the_same_bits_every_time(sdl, B, H, Hq, T, dk, dv):
             got = b(dO, dST, **x)
             first = first or {n: t.clone() for n, t in got.items()}
             assert all(torch.equal(first[n], got[n]) for n in first)
+        for _ in range(50):
+            b(dO, dST, **x)
+        assert all(torch.equal(first[n], b.grads[n]) for n in first) and b.device_status() == 0
+
+
+@pytest.mark.parametrize("B,H,T,dk,dv", [(1, 16, 16384, 128, 128), (1, 3, 70000, 64, 64), (4, 16, 4096, 128, 64)])
+def test_long_forwards_give_the_same_bits_every_time(sdl, B, H, T, dk, dv):
+    """Many segments to a CTA, back to back, so that hand-offs between its warps meet in every order: same bits, no wait
+    that gives up."""
+    import torch
+    x = make("bf16", B, H, H, T, dk, dv, seed=50)
+    f = sdl.HeadDecay(torch.bfloat16, B, H, T, dk, dv)
+    first = [t.clone() for t in f(**x)]
+    differ = torch.zeros((), device="cuda", dtype=torch.int64)
+    for _ in range(100):
+        for a, b in zip(first, f(**x)):
+            differ += (a != b).sum()
+    assert int(differ) == 0 and f.device_status() == 0
 
 
 def test_offsets_past_32_bits(sdl):
