@@ -768,13 +768,16 @@ class _HeadDecayBase:
         """Address and strides of a row tensor (features last), checked."""
         if t is None or t.dtype is not self.in_dtype or t.shape != shape or t.device != self.device:
             _refuse(t, name, self.device, self.in_dtype, shape)
-        p, st, u = t.data_ptr(), t.stride(), self._unit
-        if t.numel() and (st[-1] != 1 or p & 15):
-            _refuse(t, name, self.device, self.in_dtype, shape)
-        for n, s in zip(shape, st[:-1]):
-            if n > 1 and (s <= 0 or s % u) and t.numel():
+        p = t.data_ptr()
+        if p & 15 or not t.is_contiguous():
+            st, u = t.stride(), self._unit
+            if t.numel() and (st[-1] != 1 or p & 15):
                 _refuse(t, name, self.device, self.in_dtype, shape)
-        return p, st
+            for n, s in zip(shape, st[:-1]):
+                if n > 1 and (s <= 0 or s % u) and t.numel():
+                    _refuse(t, name, self.device, self.in_dtype, shape)
+            return p, st
+        return p, t.stride()
 
     def _gates(self, t, shape):
         """Address and strides of the log-gates, checked (all strides 0 with per_head)."""
@@ -801,7 +804,7 @@ class _HeadDecayBase:
         """The C call on this object's device and a stream, as its last argument."""
         i = self.device.index
         s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(i)
-        if torch.cuda.current_device() == i:
+        if torch._C._cuda_getDevice() == i:
             st = fn(self._desc_ref, *args, s)
         else:
             with torch.cuda.device(i):
@@ -919,7 +922,7 @@ class RequestPlan:
         args = (self.R, self.capacity, self.block, self.n_slots, lengths.data_ptr(), slots.data_ptr(), context.data_ptr(),
                 self.starts.data_ptr(), self.blocks.data_ptr(), self.block_starts.data_ptr(), self.token_slot.data_ptr(),
                 self.token_pos.data_ptr(), self.status.data_ptr(), s)
-        if torch.cuda.current_device() == i:
+        if torch._C._cuda_getDevice() == i:
             st = self._fn(*args)
         else:
             with torch.cuda.device(i):
