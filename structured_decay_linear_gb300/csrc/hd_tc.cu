@@ -105,9 +105,12 @@ struct Layout {
     static constexpr int T_R = T_Z + NZ * ZB;
     static constexpr int T_O = T_R + RB * (SPLIT ? 2 : 1);    // o on its way out
     static constexpr bool STAGED = !SPLIT && !STATES;
+    // With 64 columns tensor memory has room for two Oi and two Op: the products of a chunk then do not wait for the outputs
+    // of the one before.
+    static constexpr bool TWO = DZ == 64 && !STATES;
     static constexpr int GATES = T_O + (STAGED ? ZB : 0);
     static constexpr int BARS = GATES + 2 * (int)sizeof(GateBuf);
-    static constexpr int TOTAL = BARS + 256;   // 25 barriers, the address of the tensor memory, a unit's number
+    static constexpr int TOTAL = BARS + 256;   // 27 barriers, the address of the tensor memory, a unit's number
     static_assert(TOTAL <= 227 * 1024, "shared memory budget");
 };
 
@@ -382,13 +385,17 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
     // A states pass has no halves, P or outputs: Y~ and R of even and odd chunks, stored states of even and odd units. (Two
     // barriers each: while the issuer waits for a state to be stored, Y~ of the next chunk may be handed on as well, and a
     // wait for a phase takes the one after the next for it.)
-    uint64_t* const y_states[2] = {y_ready, y_rest};
-    uint64_t* const r_states[2] = {r_done, r_half};
-    uint64_t* const state_out[2] = {o_free, p_ready};
+    // (chosen by arithmetic: an array of them goes to local memory, and its loads to L2)
+    auto y_states = [=](uint32_t par) { return y_ready + par; };
+    auto r_states = [=](uint32_t par) { return r_half + par; };
+    auto state_out = [=](uint32_t par) { return p_ready + par; };
     uint64_t* u_full = bars + 23;    // gates: the next unit's number (-1: none)
     uint64_t* u_free = bars + 24;    // copies: taken
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 25);
-    volatile int* next_unit = reinterpret_cast<volatile int*>(bars + 25) + 1;
+    // of even and odd chunks, where these have accumulators of their own
+    auto o_frees = [=](uint32_t par) { return o_free + (Ly::TWO ? 3 * par : 0); };
+    auto op_dones = [=](uint32_t par) { return op_done + (Ly::TWO ? 15 * par : 0); };
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 27);
+    volatile int* next_unit = reinterpret_cast<volatile int*>(bars + 27) + 1;
     GateBuf* gates = reinterpret_cast<GateBuf*>(smem + Ly::GATES);
 
     // (what is the same for a warp goes through a shuffle, which tells the compiler so: branches on it then cost no
@@ -399,11 +406,11 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
     const long long wl = a.l.wait_cycles;
 
     if (tid == 0) {
-        for (int i = 0; i < 25; ++i) {
+        for (int i = 0; i < 27; ++i) {
             uint32_t n = 1;
             if (i == 15 || i == 16) n = kWorkers + 1;
             else if (STATES && (i == 19 || i == 20)) n = kWorkers - 4;
-            else if (i == 17 || (i >= 19 && i <= 22)) n = 4;
+            else if (i == 17 || (i >= 19 && i <= 22) || i == 25) n = 4;
             else if (i == 18) n = 8;
             mbar_init(bars + i, n);
         }
@@ -519,11 +526,11 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                               smem_desc_sw128(sb + Ly::T_Y + h * kHalf, 16, 1024), 32, idD, 64, h > 0);
                 mma_commit(d_done);
             };
-            auto mma_Oi = [&]() {
+            auto mma_Oi = [&](uint32_t acc) {
 #pragma unroll 1
                 for (int i = 0; i < (SPLIT ? 2 : 1) * (DX / 64); ++i) {
                     const int h = i % (DX / 64), s = i / (DX / 64);
-                    mma_chain(tmem + TM_OI, smem_desc_sw128(sb + Ly::T_X + h * kHalf, 16, 1024), 32,
+                    mma_chain(acc + TM_OI, smem_desc_sw128(sb + Ly::T_X + h * kHalf, 16, 1024), 32,
                               smem_desc_sw128(sb + Ly::T_R + s * Ly::RB + h * 64 * 128, DX * 128, 1024), 2048, idO, 64, i > 0);
                 }
                 mma_commit(oi_done);
@@ -535,13 +542,13 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                     mma_chain(tm_r, smem_desc_sw128(sb + (s ? Ly::T_YL : Ly::T_YH) + buf * Ly::XB + 8192 * half, kHalf, 1024), 2048,
                               smem_desc_sw128(tz + 8192 * half, kHalf, 1024), 2048, idR, 64, acc || s > 0);
             };
-            auto mma_Op = [&](uint32_t tz) {
+            auto mma_Op = [&](uint32_t acc, uint32_t tz) {
                 const uint64_t dz = smem_desc_sw128(tz, kHalf, 1024);
 #pragma unroll 1
                 for (int s = 0; s < (SPLIT ? 2 : 1); ++s)
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)     // 16 tokens: 8 columns of P
-                        mma_bf16_tmem_a(tmem + TM_OP, tmem + TM_D + 32 * (ks >> 1) + 8 * (ks & 1) + 16 * s,
+                        mma_bf16_tmem_a(acc + TM_OP, tmem + TM_D + 32 * (ks >> 1) + 8 * (ks & 1) + 16 * s,
                                         dadd(dz, 2048 * ks), idO, (s > 0 || ks > 0) ? 1u : 0u);
             };
             [[maybe_unused]] uint32_t unit = 0;       // (states pass) units begun
@@ -554,26 +561,29 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                 mbar_arrive(&g_free[par]);       // (behind the branch: the load has returned)
                 if (STATES) {
                     if (flags & kFirst) {      // the accumulator of the unit before the last: once it has been stored
-                        if (unit >= 2 && !wait1(state_out[unit & 1], ((unit >> 1) - 1) & 1)) { failed = true; break; }
+                        if (unit >= 2 && !wait1(state_out(unit & 1), ((unit >> 1) - 1) & 1)) { failed = true; break; }
                         tm_r = tmem + TM_R + (unit & 1) * 128;
                         ++unit;
                     }
-                    if (!wait1(y_states[par], (it >> 1) & 1) || !wait1(&full_z[s], zpar)) { failed = true; break; }
+                    if (!wait1(y_states(par), (it >> 1) & 1) || !wait1(&full_z[s], zpar)) { failed = true; break; }
                     mma_R(s, tz, 0, !(flags & kFirst));
                     mma_R(s, tz, 1, true);
                     mma_commit(&free_z[s]);
-                    mma_commit(r_states[par]);
+                    mma_commit(r_states(par));
                     continue;
                 }
                 if (!wait1(full_x, par) || !wait1(full_y, par)) { failed = true; break; }
                 mma_D();
-                if (!wait1(r_ready, par) || (it > 0 && !wait1(o_free, par ^ 1))) { failed = true; break; }
-                mma_Oi();
+                // its accumulators, once the outputs of the chunk that used them have been read
+                const uint32_t acc = tmem + (Ly::TWO ? 64 * par : 0);
+                const bool free = Ly::TWO ? it < 2 || wait1(o_frees(par), ((it - 2) >> 1) & 1) : it < 1 || wait1(o_free, par ^ 1);
+                if (!free || !wait1(r_ready, par)) { failed = true; break; }
+                mma_Oi(acc);
                 if (!wait1(y_ready, par) || !wait1(&full_z[s], zpar)) { failed = true; break; }
                 if (SPLIT) {      // O takes longest here: Op before R (z has been cleared once both halves of Y~ are there)
                     if (!wait1(y_rest, par) || !wait1(p_ready, par)) { failed = true; break; }
-                    mma_Op(tz);
-                    mma_commit(op_done);
+                    mma_Op(acc, tz);
+                    mma_commit(op_dones(par));
                 }
                 mma_R(0, tz, 0, true);
                 mma_commit(r_half);
@@ -582,10 +592,10 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                 mma_commit(r_done);
                 if (!SPLIT) {
                     if (!wait1(p_ready, par)) { failed = true; break; }
-                    mma_Op(tz);
+                    mma_Op(acc, tz);
                 }
                 mma_commit(&free_z[s]);
-                if (!SPLIT) mma_commit(op_done);
+                if (!SPLIT) mma_commit(op_dones(par));
             }
             if (failed) atomicExch(a.l.status, (int)DPLR_ERR_TIMEOUT);
             mma_commit(drain);       // every MMA this thread issued: none may run on freed tensor memory
@@ -809,20 +819,20 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                                    32 * (kWorkers - 4));
                     if (n < C) clear_rows<DZ>(sb + Ly::T_Z + s * Ly::ZB, n, C, tid, 32 * (kWorkers - 4));
                     fence_async_smem();
-                    arrive(y_states[b]);
+                    arrive(y_states(b));
                     give_back(&g_free[b], 0);       // (what was loaded has gone into the rows)
                 } else {
                     // ---- four warps: the state, behind a unit's last chunk
                     // (Every product is waited for, and the gates given back behind that: the barrier is then neither a
                     // product behind nor one ahead of the one that is asked for.)
-                    if (!wait(r_states[b], (it >> 1) & 1)) { failed = true; break; }
+                    if (!wait(r_states(b), (it >> 1) & 1)) { failed = true; break; }
                     float* dst = g.dst;
                     give_back(&g_free[b], (uint32_t)(uintptr_t)dst);
                     if (flags & kLast) {
                         if (DX == 128 || rw < 2)
                             store_state<DX, DZ>(dst, flags & kOutTurned, 32 * rw, turn, tmem + TM_R + (unit & 1) * 128 + lane_off);
                         fence_before_sync();
-                        arrive(state_out[unit & 1]);
+                        arrive(state_out(unit & 1));
                         ++unit;
                     }
                 }
@@ -1011,11 +1021,12 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
 #pragma unroll
                     for (int i = 0; i < kWAhead; ++i) dot_rows(i, wq[2 * i], wq[2 * i + 1]);
                 }
-                if (!wait(oi_done, b) || !wait(op_done, b)) { failed = true; break; }
+                if (Ly::TWO ? !wait(op_dones(b), (it >> 1) & 1) : !wait(oi_done, b) || !wait(op_done, b)) { failed = true; break; }    // (Oi goes before Op)
+                const uint32_t acc = tmem + (Ly::TWO ? 64 * b : 0);
                 auto values = [&](int c, float (&v)[16]) {       // columns c .. c + 15 of o
                     float u[16];
                     __syncwarp();        // (dead rows come from another way: these loads are the whole warp's)
-                    tmem_ld16_pair(tmem + TM_OI + lane_off + c, tmem + TM_OP + lane_off + c, u, v);
+                    tmem_ld16_pair(acc + TM_OI + lane_off + c, acc + TM_OP + lane_off + c, u, v);
 #pragma unroll
                     for (int i = 0; i < 16; i += 2) {
                         const float2 x = __ffma2_rn(make_float2(u[i], u[i + 1]), make_float2(cx, cx), make_float2(v[i], v[i + 1]));
@@ -1071,7 +1082,7 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                 fence_before_sync();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(o_free);
+                    mbar_arrive(o_frees(b));
                     if (staged) {     // the warp's 32 rows
 #pragma unroll
                         for (int x = 0; x < DZ / 64; ++x)
