@@ -367,6 +367,12 @@ dplr_status dplr_hd_backward(const dplr_hd_desc* desc, const dplr_hd_tensor* q, 
     return DPLR_OK;
 }
 
+// Whether a ragged batch's blocks are put in order of their lengths: not where every CTA has one at most, and not where each
+// has so many that the last one's length does not matter and one CTA would take long to sort them.
+static bool ordered(const dplr_hd_desc* desc, long long max_blocks) {
+    return on_tensor_cores(desc) && max_blocks * desc->H > kSMs && max_blocks <= 16384;
+}
+
 size_t dplr_hd_packed_workspace_size(const dplr_hd_desc* desc, int32_t R, int32_t block) {
     if (check_desc(desc) != DPLR_OK || desc->B != 1 || R < 1 || block < 32 || block % 32 != 0) return 0;
     size_t off = kAlign;
@@ -375,6 +381,7 @@ size_t dplr_hd_packed_workspace_size(const dplr_hd_desc* desc, int32_t R, int32_
         off = up(off + n * state_bytes(desc));
         off = up(off + n * sizeof(float));
     }
+    if (ordered(desc, (long long)desc->T / block + R)) off = up(off + ((size_t)desc->T / block + R) * sizeof(int));
     return off;
 }
 
@@ -408,7 +415,14 @@ dplr_status dplr_hd_forward_packed(const dplr_hd_desc* desc, int32_t R, int32_t 
     a.B = 1; a.bf16 = desc->in_dtype == DPLR_BF16; a.max_blocks = (int)max_blocks; a.npass = 1;
     a.status = static_cast<int*>(workspace);
     a.wait_cycles = wait_limit();
-    if (on_tensor_cores(desc)) HD_CUDA(cudaMemsetAsync(a.status + 16, 0, sizeof(int), s));     // the unit counter
+    int* order = nullptr;
+    if (ordered(desc, max_blocks)) {
+        order = reinterpret_cast<int*>(ws + dplr_hd_packed_workspace_size(desc, R, block) - up((size_t)max_blocks * sizeof(int)));
+        HD_CUDA(launch_order(a.geo, (int)max_blocks, order, a.status + 16, s));
+        a.follows = 1;
+    } else if (on_tensor_cores(desc)) {
+        HD_CUDA(cudaMemsetAsync(a.status + 16, 0, sizeof(int), s));     // the unit counter
+    }
     Pass& p = a.pass[0];
     p = base_pass(g, desc->dk, desc->dv, false, false);
     p.x = vq; p.y = vk; p.z = vv;
@@ -425,6 +439,7 @@ dplr_status dplr_hd_forward_packed(const dplr_hd_desc* desc, int32_t R, int32_t 
         p.states_only = 0;
         a.follows = 1;
     }
+    a.order = order;
     p.ext_in = S; p.ext_out = S;
     output(p, vo);
     HD_CUDA(launch(a, on_tensor_cores(desc), s));

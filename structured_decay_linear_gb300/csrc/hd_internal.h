@@ -136,6 +136,7 @@ struct Launch {
     int* status;             // the workspace's status word; the word 16 behind it counts a ragged batch's units
     long long wait_cycles;
     int follows;             // another kernel of the call goes before
+    const int* order;        // packed, outputs on the tensor cores: the blocks, longest first; null: as they come
 };
 
 cudaError_t launch_decode(const View& q, const View& k, const View& v, const float* g, long long gb, long long gh,
@@ -149,6 +150,9 @@ cudaError_t launch_fp32(const Launch& a, cudaStream_t s);
 // Tensor-core kernels: bf16, head sizes 64 and 128; one CTA per segment of one (batch, head).
 bool tc_supported(bool bf16, int dk, int dv);
 cudaError_t launch_tc(const Launch& a, cudaStream_t s);
+
+// A ragged batch's blocks in falling order of their chunks, and its unit counter set to zero.
+cudaError_t launch_order(const Geometry& g, int max_blocks, int* order, int* counter, cudaStream_t s);
 
 // Turns segments' own contributions into boundary states, in place. Forward: the contribution of segment i lies at
 // boundary i + 1, and boundary 0 is ext (or zero); backward: that of segment i at boundary i, boundary nseg is ext.

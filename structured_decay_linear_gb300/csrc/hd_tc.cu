@@ -333,7 +333,12 @@ __device__ __forceinline__ bool find_work(const Args& a, int u, Work& w) {
     w.p = &a.l.pass[pi];
     w.maps = a.map[pi];
     __builtin_assume(RAGGED == (a.l.geo.blocks != nullptr));
-    if (!locate(a.l.geo, u / a.l.npass, w.sg)) return false;
+    int at = u / a.l.npass;
+    if (RAGGED && !STATES && a.l.order) {
+        if (at / a.l.geo.H >= a.l.geo.block_starts[a.l.geo.R]) return false;      // (the order ends with the batch's blocks)
+        at = a.l.order[at / a.l.geo.H] * a.l.geo.H + at % a.l.geo.H;
+    }
+    if (!locate(a.l.geo, at, w.sg)) return false;
     w.rev = w.p->reverse;
     if (w.p->states_only == 1 && (w.rev ? w.sg.first : w.sg.last)) return false;
     w.nchunk = (w.sg.n + C - 1) / C;
@@ -447,6 +452,7 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
         // =================== copies ===================
         if (lane == 0) {
             uint32_t it = 0, nx = 0, ny = 0, nz = 0;    // chunks; copies started
+            if (RAGGED && !STATES) wait_for_kernel_before();      // the order of the blocks
             constexpr bool by_name = RAGGED;       // all but the CTA's own number's, if that has work
             int u = blockIdx.x;
             for (uint32_t named = 0; !failed; u = by_name ? -1 : u + (int)gridDim.x) {
@@ -613,6 +619,7 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
             if (it >= 2 && !wait(&g_free[b], ((it - 2) >> 1) & 1)) { failed = true; return nullptr; }
             return gates + b;
         };
+        if (RAGGED && !STATES) wait_for_kernel_before();
         // a ragged batch's blocks end before its table does
         int total = a.total;
         if (RAGGED) total = min(total, a.l.geo.block_starts[a.l.geo.R] * a.l.geo.H * a.l.npass);

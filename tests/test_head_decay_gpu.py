@@ -775,3 +775,39 @@ def test_waits_that_give_up_are_reported(sdl, what):
         sdl.dplr_la_set_wait_limit(0)
     got = call()
     assert f.device_status() == 0 and all(torch.equal(first[n], got[n]) for n in first)
+
+
+@pytest.mark.parametrize("lengths,H,block", [
+    ([0] * 60, 8, 128),                                   # more CTAs than blocks: none at all
+    ([0] * 30 + [1] + [0] * 30, 4, 2048),
+    ([1] * 40 + [900] + [130] * 20 + [0, 0, 2000, 5], 8, 2048),
+    ([1] * 40 + [900] + [130] * 20 + [0, 0, 2000, 5], 8, 256),
+])
+def test_blocks_of_all_lengths(sdl, lengths, H, block):
+    """Ragged batches of more blocks than CTAs take at once, which are computed longest first: all requests, and the bits of
+    a batch that has each request alone."""
+    import torch
+    d, R = 64, len(lengths)
+    x, cap = ragged("bf16", lengths, H, H, d, d, 40, False, seed=51)
+    i32 = lambda v: torch.tensor(v, device="cuda", dtype=torch.int32)  # noqa: E731
+    p = sdl.HeadDecayPacked(torch.bfloat16, R, cap, R, H, d, d, plan=sdl.RequestPlan(R, cap, R, block))
+    pool = torch.zeros(R, H, d, d, device="cuda")
+    p.plan(i32(lengths), i32(list(range(R))), i32([0] * R))
+    p.o.fill_(7.0)
+    o = p(x["q"], x["k"], x["v"], x["decay"], pool)
+    assert p.plan.device_status() == 0 and p.device_status() == 0
+    at, seen = 0, set()
+    for r, n in enumerate(lengths):
+        if n == 0:
+            assert not pool[r].any()
+        elif n not in seen or n > 100:
+            seen.add(n)
+            one = sdl.HeadDecayPacked(torch.bfloat16, 1, n, 1, H, d, d, plan=sdl.RequestPlan(1, n, 1, block))
+            alone = torch.zeros(1, H, d, d, device="cuda")
+            one.plan(i32([n]), i32([0]), i32([0]))
+            y = one(*(x[name][at:at + n] for name in ("q", "k", "v", "decay")), alone)
+            assert torch.equal(o[at:at + n], y) and torch.equal(pool[r], alone[0])
+            u = {name: t[at:at + n].transpose(0, 1)[None] for name, t in x.items()}
+            check_forward("bf16", y.transpose(0, 1)[None], alone, want(u))
+        at += n
+    assert bool((o[at:] == 7.0).all())
