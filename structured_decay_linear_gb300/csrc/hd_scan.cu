@@ -250,9 +250,9 @@ cudaError_t launch_scan(const Scan& a, cudaStream_t s) {
     const long long rows = a.geo.blocks ? (long long)a.R * a.geo.H : (long long)a.B * a.geo.H;
     if (rows == 0) return cudaSuccess;
     const unsigned gy = (unsigned)((a.dk * a.dv / 4 + 255) / 256), gz = a.fwd && a.bwd ? 2 : 1;
-    // a ragged batch's rows are mostly of one block, with nothing to do: few CTAs walk them (1600 rows of which none had
-    // anything to do took 16 us as CTAs of their own)
-    const long long most = a.geo.blocks ? 256 : rows;
+    // a ragged batch's rows are mostly of one block, with nothing to do: as many CTAs as are resident at once walk them (1600
+    // rows of which none had anything to do took 16 us as CTAs of their own, 6 us as 256)
+    const long long most = a.geo.blocks ? 8 * sm_count() / gy : rows;
     return launch_kernel(hd_scan_kernel, dim3((unsigned)(rows < most ? rows : most), gy, gz), 256, 0, s, true, a, (int)rows);
 }
 
