@@ -7,6 +7,10 @@ as hand-written CUDA for GB300 (sm_103a) behind the C ABI of libdplr (include/dp
 with the transfers overlapped with the kernels; the C-ABI mirrors (``dplr_la_forward``,
 ``dplr_la_chunk_maps``, ...) take raw pointers. There is no CPU fallback: without
 libdplr.so the calls raise.
+
+Linear attention with one decay per head (no low-rank term): ``HeadDecay`` and ``HeadDecayBackward`` for prompts and
+training, ``HeadDecayDecode`` for single tokens on a pool of states, ``HeadDecayPacked`` with ``RequestPlan`` for the
+prompts of a ragged batch on that pool.
 """
 
 from .dplr import (  # noqa: F401

@@ -8,6 +8,11 @@
 //   backward   P_rc = (x_r . y_c) e^{G_c - G_r}, c >= r;  o_r = P z + e^{G_n - G_r} R^T x_r;  R <- e^{G_n} R + sum e^{G_c} y_c z_c^T
 // Columns of the state evolve independently, so the column blocks share nothing but the product x y^T, which each
 // forms again. Exponents are differences of cumulative gates and never positive: nothing overflows for any gate.
+//
+// Bound: by the instructions that two CTAs of eight warps an SM issue (0.4 a cycle and scheduler) and the shared-memory loads
+// among them. Chunks of 32 keep P small beside the state's products; 64 columns and 64 features give a thread 4 x 4
+// numbers of the state for three loads a token. Measured (fp32, B2 H8 T2001, 64 x 64, 16 segments a head): states 19 us,
+// outputs 44 us, 8 TFLOP/s of the recurrence; with scalar products 23 and 50.
 #include <cuda_bf16.h>
 
 #include "hd_internal.h"
@@ -183,7 +188,7 @@ __device__ __forceinline__ void segment_pass(const Pass& p, const Geometry& geo,
         if (jj + 1 < nchunk) take(jj + 1);
         if (tid < 32) {
             // Sums in fixed point (32 fractional bits, 64 in all): after a gate of -100 those between later tokens still
-            // count. 64-bit floating point is slow here: with it a chunk waited 4 us for this warp (T2001 66 -> 40 us).
+            // count. (64-bit floating point has few units here.)
             const bool bad = !(graw <= 1e4f);      // NaN (gates are not positive; one that large is no gate either)
             const uint32_t nan = __ballot_sync(0xffffffffu, bad);
             long long g = __float2ll_rn((bad ? 0.f : graw < kMinGate ? kMinGate : graw) * 4294967296.f);

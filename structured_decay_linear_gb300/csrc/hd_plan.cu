@@ -3,6 +3,8 @@
 // One launch without waits between CTAs: every CTA scans the lengths itself (R x 12 bytes, from L2 after the first) and
 // then fills its share of the tables, finding a row's request by bisection of the starts in shared memory. The floor
 // is a launch and the scan's latency for few requests, and for many the bytes of the tables (8 a row of the batch).
+// Four requests and four rows a thread: one turn of the scan, one bisection and 16-byte stores for the four. Measured: 12
+// requests 5 us, 1500 with 200 K rows 7 us (10 us with one request and one row a thread at a time).
 #include "dplr_internal.h"
 
 namespace dplr {

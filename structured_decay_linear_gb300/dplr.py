@@ -913,7 +913,8 @@ class RequestPlan:
         self._fn = library().dplr_hd_plan
 
     def __call__(self, lengths, slots, context, stream: Optional[torch.cuda.Stream] = None) -> dict:
-        """lengths, slots, context: int32 [R] on the device. Returns the tables (see device_status for refused input)."""
+        """lengths, slots, context: int32 [R] on the device. Returns the tables (see device_status for refused input). A packed
+        forward of this plan reads `slots` and `context` again: leave them as they are until it has run."""
         dev, i = self.device, self.device.index
         for t, name in ((lengths, "lengths"), (slots, "slots"), (context, "context")):
             if t is None or t.dtype is not torch.int32 or t.shape != (self.R,) or t.device != dev or not t.is_contiguous():
