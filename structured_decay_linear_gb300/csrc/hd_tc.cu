@@ -67,6 +67,10 @@ struct alignas(128) Args {
     CUtensorMap map[3][4];    // [pass][x, y, z, o]
     Launch l;
     int total;                // units of work: segments times passes
+    // A call's passes that differ in kind are launches that need the same states and nothing of each other. The first lets the
+    // next begin once these are there (late), and that one waits for nothing (independent): its CTAs start on SMs as these get
+    // done with the first, so that the two leave one ragged end, not two.
+    int late, independent;
     int* counter;             // (outputs of a ragged batch) a CTA's first unit is blockIdx.x, all others come from here (0 at first)
 };
 
@@ -425,7 +429,7 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
         }
         mbar_fence_init();
     }
-    let_next_kernel_begin();
+    if (!a.late) let_next_kernel_begin();
     if (warp == 0) tmem_alloc(tmem_holder, kTmemCols);
     fence_before_sync();
     __syncthreads();
@@ -850,7 +854,10 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
             } else if constexpr (role == 0) {
                 // ---- A: the state (thread = row of R; with DX = 64 two warps only keep step)
                 const bool mine = DX == 128 || warp < 2;
-                if (it == 0) wait_for_kernel_before();      // the states that it starts from; the other roles read inputs
+                if (it == 0) {
+                    if (!a.independent) wait_for_kernel_before();      // the states that it starts from; the other roles read inputs
+                    if (a.late) let_next_kernel_begin();
+                }
                 if (it > 0 && (!wait(oi_done, b ^ 1) || !wait(r_done, b ^ 1))) { failed = true; break; }
                 const float en = g.en;
                 const float* src = g.src;
@@ -1192,6 +1199,8 @@ cudaError_t launch_tc(const Launch& l, cudaStream_t s) {
         // Lengths of a ragged batch differ: CTAs take their units as they get done with others. Which one takes a unit does
         // not touch its result.
         if (l.geo.blocks && !q.states_only) a.counter = l.status + 16;
+        for (int j = i; j < l.npass; ++j) a.late |= !q.states_only && !done[j];
+        a.independent = i > 0 && !q.states_only;
         if (i > 0) a.l.follows = 1;
         const bool split = q.dots != nullptr, states = q.states_only != 0;
         cudaError_t e;
