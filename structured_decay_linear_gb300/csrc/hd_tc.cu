@@ -255,9 +255,6 @@ __device__ __forceinline__ uint32_t turn_at(int row, int piece) { return (uint32
 __device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void copy_async4(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(dst), "l"(src) : "memory");
-}
 __device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Starts columns c .. c + 31 of the warp's 32 rows (first row r0) of a state [DX][DZ], or `turned` of one [DZ][DX], on
@@ -269,14 +266,19 @@ __device__ __forceinline__ void start_block(const float* state, bool turned, int
         const float* src = state + (r0 + (lane >> 3)) * DZ + c + 4 * (lane & 7);
 #pragma unroll
         for (int k = 0; k < 8; ++k) copy_async16(turn + turn_at(4 * k + (lane >> 3), lane & 7), src + 4 * k * DZ);
-    } else {        // a column's 32 rows lie together
-        const float* src = state + r0 + lane + c * DX;
-#pragma unroll 8
-        for (int i = 0; i < 32; ++i) copy_async4(turn + turn_at(lane, i >> 2) + 4 * (i & 3), src + i * DX);
+    } else {        // a column's 32 rows lie together: they stay so, and block_row() reads across
+        const float* src = state + (c + (lane >> 3)) * DX + r0 + 4 * (lane & 7);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) copy_async16(turn + (4 * k + (lane >> 3)) * 128 + 16 * (lane & 7), src + 4 * k * DX);
     }
 }
-__device__ __forceinline__ void block_row(uint32_t turn, float (&v)[32]) {
+__device__ __forceinline__ void block_row(uint32_t turn, bool turned, float (&v)[32]) {
     const int lane = threadIdx.x & 31;
+    if (turned) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[i]) : "r"(turn + 128 * i + 4 * lane));
+        return;
+    }
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         uint32_t u[4];
@@ -880,7 +882,7 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                         for (int i = 0; i < AT; ++i) {
                             float v[32];
                             if (src) {
-                                block_row(place(i), v);
+                                block_row(place(i), turned, v);
                             } else {
 #pragma unroll
                                 for (int e = 0; e < 32; ++e) v[e] = 0.f;
