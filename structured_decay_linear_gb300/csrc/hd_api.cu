@@ -359,9 +359,8 @@ dplr_status dplr_hd_backward(const dplr_hd_desc* desc, const dplr_hd_tensor* q, 
     if (shared) {
         GroupSum gs{};
         gs.B = desc->B; gs.H = desc->H; gs.Hq = desc->Hq; gs.T = desc->T; gs.D = K; gs.bf16 = a.bf16;
-        gs.part = at(pl.part_q); gs.out = const_cast<void*>(vdq.p); gs.ob = vdq.sb; gs.oh = vdq.sh; gs.ot = vdq.st;
-        HD_CUDA(launch_group_sum(gs, s));
-        gs.part = at(pl.part_k); gs.out = const_cast<void*>(vdk.p); gs.ob = vdk.sb; gs.oh = vdk.sh; gs.ot = vdk.st;
+        gs.one[0] = {at(pl.part_q), const_cast<void*>(vdq.p), vdq.sb, vdq.sh, vdq.st};
+        gs.one[1] = {at(pl.part_k), const_cast<void*>(vdk.p), vdk.sb, vdk.sh, vdk.st};
         HD_CUDA(launch_group_sum(gs, s));
     }
     return DPLR_OK;

@@ -186,8 +186,10 @@ cudaError_t launch_gate_grad(const GateGrad& a, cudaStream_t s);
 // Gradients of shared query/key heads: out[b, hq, t] = sum over hq's value heads of part [B,H,T,D] (fp32), in head order.
 struct GroupSum {
     int B, H, Hq, T, D, bf16;
-    const float* part;
-    void* out; long long ob, oh, ot;
+    struct One {
+        const float* part;
+        void* out; long long ob, oh, ot;
+    } one[2];                // dq and dk
 };
 cudaError_t launch_group_sum(const GroupSum& a, cudaStream_t s);
 

@@ -14,9 +14,9 @@ namespace hd {
 namespace {
 
 // ---- boundary states: one thread per four elements of one (sequence, head)'s state, walking its segments. The loads
-// of the contributions do not depend on the chain, so four are in flight at a time.
-constexpr int kAhead = 4;      // (eight: 4 us off a scan of 16 segments, 3 us on one of four, whose kernel then starts later)
-
+// of the contributions do not depend on the chain, so kAhead are in flight at a time. (Eight took 4 us off a scan of 16
+// segments and put 3 us on one of four, whose larger CTAs started later: chosen by the number of segments.)
+template <int kAhead>
 __device__ __forceinline__ void scan_row(const Scan& a, int row, int at, bool back) {
     const long long size = (long long)a.dk * a.dv;
     float* W = back ? a.bwd : a.fwd;
@@ -77,6 +77,7 @@ __device__ __forceinline__ void scan_row(const Scan& a, int row, int at, bool ba
     }
 }
 
+template <int kAhead>
 __global__ void __launch_bounds__(256) hd_scan_kernel(const __grid_constant__ Scan a, int rows) {
     const int at = (blockIdx.y * 256 + threadIdx.x) * 4;
     let_next_kernel_begin();
@@ -87,7 +88,7 @@ __global__ void __launch_bounds__(256) hd_scan_kernel(const __grid_constant__ Sc
         if (!__syncthreads_or(any)) return;
     }
     if (at >= a.dk * a.dv) return;
-    for (int row = blockIdx.x; row < rows; row += gridDim.x) scan_row(a, row, at, a.fwd == nullptr || blockIdx.z == 1);
+    for (int row = blockIdx.x; row < rows; row += gridDim.x) scan_row<kAhead>(a, row, at, a.fwd == nullptr || blockIdx.z == 1);
 }
 
 // ---- the order in which CTAs take a ragged batch's blocks: the longest first, so that none starts late. (32 requests of up
@@ -223,27 +224,28 @@ __global__ void __launch_bounds__(32) hd_head_grad_kernel(const __grid_constant_
 
 template <bool BF>
 __global__ void __launch_bounds__(256) hd_group_sum_kernel(const __grid_constant__ GroupSum a) {
-    const int per = a.D / 4, group = a.H / a.Hq;
+    const int per = a.D / 4, lg = 31 - __clz(per), group = a.H / a.Hq;      // (per: 8, 16 or 32)
+    const GroupSum::One& w = a.one[blockIdx.y];
     let_next_kernel_begin();
     wait_for_kernel_before();
     const long long n = (long long)a.B * a.Hq * a.T * per;
     for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
-        const int c = (int)(i % per) * 4;
-        const long long row = i / per;
-        const long long t = row % a.T, hq = (row / a.T) % a.Hq, b = row / a.T / a.Hq;
-        const float* src = a.part + ((b * a.H + hq * group) * a.T + t) * a.D + c;
+        const int c = (int)(i & (per - 1)) * 4;
+        const uint32_t row = (uint32_t)(i >> lg), bh = row / a.T;      // rows: below 2^31
+        const long long t = row % a.T, hq = bh % a.Hq, b = bh / a.Hq;
+        const float* src = w.part + ((b * a.H + hq * group) * a.T + t) * a.D + c;
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int j = 0; j < group; ++j) {
             const float4 v = *reinterpret_cast<const float4*>(src + (long long)j * a.T * a.D);
             s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
         }
-        const long long at = b * a.ob + hq * a.oh + t * a.ot + c;
+        const long long at = b * w.ob + hq * w.oh + t * w.ot + c;
         if (BF) {
             __nv_bfloat162 x = __floats2bfloat162_rn(s.x, s.y), y = __floats2bfloat162_rn(s.z, s.w);
-            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) =
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(w.out) + at) =
                 make_uint2(*reinterpret_cast<uint32_t*>(&x), *reinterpret_cast<uint32_t*>(&y));
         } else {
-            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = s;
+            *reinterpret_cast<float4*>(static_cast<float*>(w.out) + at) = s;
         }
     }
 }
@@ -257,7 +259,8 @@ cudaError_t launch_scan(const Scan& a, cudaStream_t s) {
     // a ragged batch's rows are mostly of one block, with nothing to do: as many CTAs as are resident at once walk them (1600
     // rows of which none had anything to do took 16 us as CTAs of their own, 6 us as 256)
     const long long most = a.geo.blocks ? 8 * sm_count() / gy : rows;
-    return launch_kernel(hd_scan_kernel, dim3((unsigned)(rows < most ? rows : most), gy, gz), 256, 0, s, true, a, (int)rows);
+    const bool deep = !a.geo.blocks && a.geo.nseg > 8;
+    return launch_kernel(deep ? hd_scan_kernel<8> : hd_scan_kernel<4>, dim3((unsigned)(rows < most ? rows : most), gy, gz), 256, 0, s, true, a, (int)rows);
 }
 
 cudaError_t launch_order(const Geometry& g, int max_blocks, int* order, int* counter, cudaStream_t s) {
@@ -274,10 +277,10 @@ cudaError_t launch_gate_grad(const GateGrad& a, cudaStream_t s) {
 
 cudaError_t launch_group_sum(const GroupSum& a, cudaStream_t s) {
     const long long n = (long long)a.B * a.Hq * a.T * (a.D / 4);
-    const long long most = (long long)sm_count() * 8;
+    const long long most = (long long)sm_count() * 4;      // (of each of the two)
     const long long blocks = (n + 255) / 256;
     const unsigned g = (unsigned)(blocks < most ? blocks : most);
-    return launch_kernel(a.bf16 ? hd_group_sum_kernel<true> : hd_group_sum_kernel<false>, dim3(g), 256, 0, s, true, a);
+    return launch_kernel(a.bf16 ? hd_group_sum_kernel<true> : hd_group_sum_kernel<false>, dim3(g, 2), 256, 0, s, true, a);
 }
 
 }  // namespace hd
