@@ -366,7 +366,8 @@ __device__ __forceinline__ const float* start_state(const Work& w) {
 }
 
 // RAGGED: of a ragged batch, whose units are found in tables and shared out as the CTAs get done. A batch of equal lengths
-// has its own variant: with the table's branches in the unit loop its passes took 3 % longer (B4 H16 T4096, gradients 349 -> 335 us).
+// has its own variant: with the table's branches in the unit loop its passes took 3 % longer (B4 H16 T4096, gradients 349
+// instead of 335 us).
 template <int DX, int DZ, bool SPLIT, bool STATES, bool RAGGED>
 __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Args a) {
     using Ly = Layout<DX, DZ, SPLIT, STATES>;
