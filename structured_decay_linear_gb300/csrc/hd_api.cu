@@ -105,9 +105,10 @@ Cut forward_cut(const dplr_hd_desc* d) {
         const long long want = kSMs / ((long long)d->B * d->H);
         return cut(d->T, want < 1 ? 1 : (int)want, kChunk, 512, 0);
     }
-    const long long target = 2LL * kSMs;
-    const long long want = target / base_ctas(d, d->dv);
-    return cut(d->T, want < 1 ? 1 : (int)want, 32, 128, 0);
+    // Segments of 128 tokens, or of 64 where those would leave SMs without one (fp32 64 x 64, 16 heads: T777 48 -> 35 us; at
+    // T2001, with 256 of 128 tokens, 64 would take 64 us instead of 58: more states to scan).
+    const long long target = 2LL * kSMs, base = base_ctas(d, d->dv), want = target / base;
+    return cut(d->T, want < 1 ? 1 : (int)want, 32, base * ((d->T + 127) / 128) < kSMs ? 64 : 128, 0);
 }
 
 Cut backward_cut(const dplr_hd_desc* d) {
