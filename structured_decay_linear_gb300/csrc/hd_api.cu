@@ -103,7 +103,9 @@ bool on_tensor_cores(const dplr_hd_desc* d) { return tc_supported(d->in_dtype ==
 Cut forward_cut(const dplr_hd_desc* d) {
     if (on_tensor_cores(d)) {
         const long long want = kSMs / ((long long)d->B * d->H);
-        return cut(d->T, want < 1 ? 1 : (int)want, kChunk, 512, 0);
+        // Up to 512 tokens stay whole (B1 H16 T512: 19 us, in two segments 23 us: a scan and a pass more); longer sequences are
+        // cut into segments of 256 and more (T1024: 23 us, of 512 31 us; T2048: 27 and 31 us).
+        return cut(d->T, want < 1 ? 1 : (int)want, kChunk, d->T <= 512 ? 512 : 256, 0);
     }
     // Segments of 128 tokens, or of 64 where those would leave SMs without one (fp32 64 x 64, 16 heads: T777 48 -> 35 us; at
     // T2001, with 256 of 128 tokens, 64 would take 64 us instead of 58: more states to scan).
