@@ -170,3 +170,11 @@ def test_reference_gradients_against_differences():
         hi, lo = dict(x), dict(x)
         hi[n], lo[n] = x[n] + 1e-6 * u, x[n] - 1e-6 * u
         assert abs((loss(hi) - loss(lo)) / 2e-6 - (got[name] * u).sum()) <= 1e-6 * np.linalg.norm(got[name])
+
+
+def test_default_block_of_a_ragged_batch(sdl):
+    """A multiple of 32 that follows the tokens and heads that an SM gets: on the tensor cores the next power of two, at
+    least 512; on the CUDA cores the last one, at least 128."""
+    block = lambda dt, T, H: sdl.default_block(sdl.make_hd_desc(dt, 1, H, T, 128, 128))  # noqa: E731
+    assert [block("bf16", T, 16) for T in (0, 1, 3000, 16203, 55165)] == [512, 512, 512, 2048, 8192]
+    assert [block("f32", T, 16) for T in (0, 1, 3000, 10000, 55165)] == [128, 128, 256, 1024, 4096]
