@@ -178,3 +178,32 @@ def test_default_block_of_a_ragged_batch(sdl):
     block = lambda dt, T, H: sdl.default_block(sdl.make_hd_desc(dt, 1, H, T, 128, 128))  # noqa: E731
     assert [block("bf16", T, 16) for T in (0, 1, 3000, 16203, 55165)] == [512, 512, 512, 2048, 8192]
     assert [block("f32", T, 16) for T in (0, 1, 3000, 10000, 55165)] == [128, 128, 256, 1024, 4096]
+
+
+def test_outputs_on_top_of_inputs_are_refused(sdl):
+    """A result fed back into the object that holds it; S_T alone may be S0 (run on the GPU)."""
+    at = lambda i: FAKE + (i << 30)  # noqa: E731
+    d = sdl.make_hd_desc("bf16", 2, 4, 100, 128, 128)
+    t = [tensor(sdl, 2, 4, 100, 128, data=at(i)) for i in range(8)]
+    g = sdl.dplr_hd_tensor(at(9), 400, 100, 1)
+    for i in range(3):
+        assert forward(sdl, d, q=t[0], k=t[1], v=t[2], o=t[i], decay=g, S0=at(10), S_T=at(11), ws=at(12)) == 1
+    names = ["q", "k", "v", "decay", "S0", "dO", "dST", "dq", "dk", "dv", "ddecay", "dS0", "ws", "nbytes"]
+    base = [t[0], t[1], t[2], g, at(10), t[3], at(11), t[4], t[5], t[6], at(13), at(14), at(12),
+            sdl.dplr_hd_backward_workspace_size(d)]
+
+    def backward(**kw):
+        return sdl.dplr_hd_backward(d, *[kw.get(n, b) for n, b in zip(names, base)], None)
+
+    for n in ("dq", "dk", "dv"):
+        assert all(backward(**{n: t[i]}) == 1 for i in range(4)), n
+    assert backward(dk=t[4]) == 1 and backward(dv=t[5]) == 1 and backward(dv=t[4]) == 1
+    assert backward(dS0=at(10)) == 1 and backward(dS0=at(11)) == 1 and backward(ddecay=at(9)) == 1
+    d = sdl.make_hd_desc("bf16", 1, 4, 100, 128, 128)
+    t = [tensor(sdl, 1, 4, 100, 128, data=at(i)) for i in range(3)]
+    n = sdl.dplr_hd_packed_workspace_size(d, 3, 64)
+    one = sdl.make_hd_desc("bf16", 5, 4, 1, 128, 128)
+    u = [tensor(sdl, 5, 4, 1, 128, data=at(i)) for i in range(3)]
+    for i in range(3):
+        assert sdl.dplr_hd_forward_packed(d, 3, 64, 8, *[at(4)] * 4, *t, g, at(5), t[i], at(6), n, None) == 1
+        assert sdl.dplr_hd_decode_step(one, 8, at(4), *u, sdl.dplr_hd_tensor(at(9), 4, 1, 0), at(5), u[i], None, None) == 1
