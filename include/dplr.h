@@ -324,7 +324,8 @@ DPLR_API dplr_status dplr_hd_plan(int32_t R, int32_t capacity, int32_t block, in
  * starts from its slot's state, one with context 0 from zero; requests without tokens leave theirs as it was. desc: B = 1
  * and T = the capacity; q, k, v, o, decay have one row per token (the batch stride is not looked at). The tables are
  * those of dplr_hd_plan with the same R, T and `block`; context and slots the arrays given to it. Rows of o behind the
- * last token are left as they were. */
+ * last token are left as they were. So are the rows and the state of a request whose slot has been changed since to one
+ * out of range; the workspace's status word is then DPLR_ERR_INVALID_ARG. */
 DPLR_API size_t dplr_hd_packed_workspace_size(const dplr_hd_desc* desc, int32_t R, int32_t block);
 DPLR_API dplr_status dplr_hd_forward_packed(const dplr_hd_desc* desc, int32_t R, int32_t block, int32_t n_slots,
                                             const int32_t* blocks, const int32_t* block_starts, const int32_t* slots,

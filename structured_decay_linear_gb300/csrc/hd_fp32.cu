@@ -378,8 +378,10 @@ __global__ void __launch_bounds__(TH) hd_fp32_kernel(const __grid_constant__ Lau
     const Pass& p = a.pass[blockIdx.y];
     const int zb = blockIdx.x % zmax;
     Segment sg;
-    if (zb * (p.DZ == 32 ? 32 : 64) >= p.DZ || !locate(a.geo, blockIdx.x / zmax, sg) ||
-        (p.states_only == 1 && (p.reverse ? sg.first : sg.last))) {
+    sg.n = 0;
+    const bool found = locate(a.geo, blockIdx.x / zmax, sg);
+    if (zb * (p.DZ == 32 ? 32 : 64) >= p.DZ || !found || (p.states_only == 1 && (p.reverse ? sg.first : sg.last))) {
+        if (!found && sg.n > 0 && threadIdx.x == 0) atomicExch(a.status, (int)DPLR_ERR_INVALID_ARG);   // its request's slot is bad
         wait_for_kernel_before();      // a kernel of which no CTA waited would end before the one before it
         return;
     }

@@ -78,7 +78,9 @@ __host__ __device__ inline long long units(const Geometry& g, int B, int max_blo
     return g.blocks ? (long long)max_blocks * g.H : (long long)B * g.H * g.nseg;
 }
 
-// False: nothing to do (a block behind the last).
+// False: nothing to do: a block behind the last (s is as it was), or one of a request whose slot has been changed to one out of
+// range since the tables were made (s.n is its tokens). KEEP: that one stays, without tokens and without a state to leave.
+template <bool KEEP = false>
 __device__ __forceinline__ bool locate(const Geometry& g, int unit, Segment& s) {
     if (g.blocks) {
         const int blk = unit / g.H;
@@ -90,11 +92,15 @@ __device__ __forceinline__ bool locate(const Geometry& g, int unit, Segment& s) 
         s.alone = nb == 1; s.first = e.w == 0; s.last = e.w == nb - 1;
         s.fresh = g.context[e.x] == 0;
         const int slot = g.slots[e.x];
-        if (slot < 0 || slot >= g.n_slots) return false;
-        s.ext = (long long)slot * g.H + s.h;
+        const bool in = slot >= 0 && slot < g.n_slots;
+        if (KEEP) {
+            s.n = in ? e.z : 0;
+            s.last = in && e.w == nb - 1;
+        }
+        s.ext = (long long)(in ? slot : 0) * g.H + s.h;
         s.entry = (long long)blk * g.H + s.h;
         s.step = g.H;
-        return true;
+        return KEEP || in;
     }
     const int bh = unit / g.nseg, seg = unit % g.nseg;
     s.b = bh / g.H; s.h = bh % g.H;

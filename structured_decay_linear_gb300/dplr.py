@@ -813,8 +813,8 @@ class _HeadDecayBase:
             raise DplrError(st, name)
 
     def device_status(self, clear: bool = False) -> int:
-        """The workspace's device status word (0, or DPLR_ERR_TIMEOUT after a bounded wait gave up), read
-        synchronously through dplr_la_read_status."""
+        """The workspace's device status word (0, DPLR_ERR_TIMEOUT after a bounded wait gave up, or DPLR_ERR_INVALID_ARG
+        after a ragged forward found a slot out of range), read synchronously through dplr_la_read_status."""
         with torch.cuda.device(self.device):
             s = torch.cuda.current_stream(self.device)
             st, word = dplr_la_read_status(_ptr(self.workspace), self.workspace.numel(), clear, s.cuda_stream)

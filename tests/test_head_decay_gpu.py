@@ -811,3 +811,43 @@ def test_blocks_of_all_lengths(sdl, lengths, H, block):
             check_forward("bf16", y.transpose(0, 1)[None], alone, want(u))
         at += n
     assert bool((o[at:] == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype,d,H,block", [("bf16", 128, 2, 2048), ("bf16", 64, 8, 256), ("bf16", 64, 8, 128), ("f32", 64, 2, 128),
+                                             ("bf16", 32, 2, 64)])
+@pytest.mark.parametrize("bad", ["first", "last", "many", "all"])
+def test_slots_that_went_bad_after_planning(sdl, dtype, d, H, block, bad):
+    """Slots out of range by the time of the forward: these requests are left out, rows and states as they were, with a
+    status; the others' results keep their bits."""
+    import torch
+    lengths = [300, 5, 0, 700, 128, 1, 33] + [40, 130, 1] * 12 + [513, 2]
+    R = len(lengths)
+    x, cap = ragged(dtype, lengths, H, H, d, d, 20, False, seed=62)
+    i32 = lambda v: torch.tensor(v, device="cuda", dtype=torch.int32)  # noqa: E731
+    at = torch.randperm(R, generator=torch.Generator().manual_seed(5)).tolist()
+    lost = {"first": [0], "last": [R - 1], "many": [0, 1, 3] + list(range(6, R, 2)), "all": list(range(R))}[bad]
+    f = sdl.HeadDecayPacked(x["q"].dtype, R, cap, R, H, d, d, plan=sdl.RequestPlan(R, cap, R, block))
+    start = torch.randn(R, H, d, d, device="cuda")
+    slot, out = i32(at), []
+    f.plan(i32(lengths), slot, i32([r % 2 for r in range(R)]))
+    for turn in range(3):
+        if turn == 1:
+            slot[i32(lost).long()] = i32([(-1, R, 2 ** 31 - 1, -2 ** 31)[i % 4] for i in range(len(lost))])
+        elif turn == 2:
+            slot.copy_(i32(at))
+        pool = start.clone()
+        f.o.fill_(7.0)
+        f(x["q"], x["k"], x["v"], x["decay"], pool)
+        out.append((f.o.clone(), pool))
+        assert f.device_status(clear=True) == (sdl.dplr.DPLR_ERR_INVALID_ARG if turn == 1 else 0)
+    (o, S), (o2, S2), (o3, S3) = out
+    assert torch.equal(o, o3) and torch.equal(S, S3)
+    at_row = 0
+    for r, n in enumerate(lengths):
+        rows = slice(at_row, at_row + n)
+        at_row += n
+        if r in lost:
+            assert (o2[rows] == 7.0).all() and torch.equal(S2[at[r]], start[at[r]])
+        else:
+            assert torch.equal(o2[rows], o[rows]) and torch.equal(S2[at[r]], S[at[r]])
+    assert (o2[at_row:] == 7.0).all()
