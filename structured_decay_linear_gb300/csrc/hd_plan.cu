@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(TH) hd_plan_kernel(PlanArgs a) {
                 if (s[i] < 0 || s[i] >= a.nslots) bad = true;
                 else if (atomicOr(&seen[s[i] >> 5], 1u << (s[i] & 31)) & (1u << (s[i] & 31))) bad = true;
             }
-            c[i] = (n[i] + a.block - 1) / a.block;
+            c[i] = (int)(((unsigned)n[i] + (unsigned)a.block - 1) / (unsigned)a.block);   // (the sum may pass 2^31)
             sn += n[i];
             sb += c[i];
         }

@@ -851,3 +851,25 @@ def test_slots_that_went_bad_after_planning(sdl, dtype, d, H, block, bad):
         else:
             assert torch.equal(o2[rows], o[rows]) and torch.equal(S2[at[r]], S[at[r]])
     assert (o2[at_row:] == 7.0).all()
+
+
+@pytest.mark.parametrize("block", [1 << 30, (1 << 30) + 32, 2 ** 31 - 32])
+def test_blocks_longer_than_anything(sdl, block):
+    """A caller's "never split": a length and such a block add up to more than 31 bits. One block a request, and the bits of
+    any other block that splits none."""
+    import torch
+    lengths = [40, 100, 5, 0, 33, 65, 32, 300, 1, 31, 66, 7]
+    R, d = len(lengths), 64
+    x, cap = ragged("bf16", lengths, 2, 2, d, d, 9, False, seed=64)
+    i32 = lambda v: torch.tensor(v, device="cuda", dtype=torch.int32)  # noqa: E731
+    out = []
+    for b in (2048, block):
+        f = sdl.HeadDecayPacked(torch.bfloat16, R, cap, R, 2, d, d, plan=sdl.RequestPlan(R, cap, R, b))
+        t = f.plan(i32(lengths), i32(list(range(R))), i32([0] * R))
+        assert f.plan.device_status() == 0
+        for name, w in ref.plan(lengths, range(R), [0] * R, cap, b).items():
+            assert np.array_equal(t[name].cpu().numpy(), w), name
+        pool = torch.zeros(R, 2, d, d, device="cuda")
+        out.append((f(x["q"], x["k"], x["v"], x["decay"], pool), pool))
+        assert f.device_status() == 0
+    assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
