@@ -8,6 +8,7 @@ raise: there is no CPU or PyTorch fallback.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import struct
 import threading
@@ -650,7 +651,16 @@ def make_hd_desc(in_dtype, B: int, H: int, T: int, dk: int, dv: int, q_heads: Op
         dt = DPLR_F32
     else:
         raise ValueError(f"unsupported input dtype {in_dtype}")
-    return dplr_hd_desc(dt, B, H, H if q_heads is None else q_heads, T, dk, dv, int(bool(per_head)))
+    sizes = _int32(B=B, H=H, q_heads=H if q_heads is None else q_heads, T=T, dk=dk, dv=dv)
+    return dplr_hd_desc(dt, *sizes, int(bool(per_head)))
+
+
+def _int32(**sizes):
+    """The sizes as ints, refused beyond the C interface's 32 bits (ctypes would drop the bits above)."""
+    for name, n in sizes.items():
+        if not -2 ** 31 <= operator.index(n) < 2 ** 31:
+            raise ValueError(f"{name} is {n}, which does not fit 32 bits")
+    return [operator.index(n) for n in sizes.values()]
 
 
 def dplr_hd_check(desc: dplr_hd_desc) -> int:
@@ -897,7 +907,8 @@ class RequestPlan:
 
     def __init__(self, requests: int, capacity: int, slots: int, block: int = 128,
                  device: Optional[torch.device] = None):
-        self.R, self.capacity, self.n_slots, self.block = int(requests), int(capacity), int(slots), int(block)
+        self.R, self.capacity, self.n_slots, self.block = _int32(requests=int(requests), capacity=int(capacity),
+                                                                 slots=int(slots), block=int(block))
         self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
@@ -994,7 +1005,7 @@ class HeadDecayDecode(_HeadDecayBase):
     def __init__(self, in_dtype, rows: int, H: int, dk: int, dv: int, slots: int, q_heads: Optional[int] = None,
                  per_head: bool = False, device: Optional[torch.device] = None):
         self._setup(in_dtype, rows, H, 1, dk, dv, q_heads, per_head, device)
-        self.n_slots = int(slots)
+        self.n_slots, = _int32(slots=int(slots))
         self.o = torch.zeros((rows, H, dv), dtype=self.in_dtype, device=self.device)
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._fn, self._slots = library().dplr_hd_decode_step, _Slots(5)

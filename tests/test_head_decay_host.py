@@ -207,3 +207,23 @@ def test_outputs_on_top_of_inputs_are_refused(sdl):
     for i in range(3):
         assert sdl.dplr_hd_forward_packed(d, 3, 64, 8, *[at(4)] * 4, *t, g, at(5), t[i], at(6), n, None) == 1
         assert sdl.dplr_hd_decode_step(one, 8, at(4), *u, sdl.dplr_hd_tensor(at(9), 4, 1, 0), at(5), u[i], None, None) == 1
+
+
+def test_sizes_beyond_32_bits_are_refused(sdl):
+    """The C interface takes 32-bit sizes; one above would lose its upper bits on the way: a block of 2^32 + 128 would become
+    one of 128, for which the tables made for it have no room."""
+    torch = pytest.importorskip("torch")
+    device = torch.device("cuda", 0)
+    for kw in (dict(block=2 ** 32 + 128), dict(block=2 ** 31), dict(capacity=2 ** 32 + 5), dict(requests=2 ** 32 + 1),
+               dict(slots=2 ** 32 + 3)):
+        a = dict(requests=3, capacity=100, slots=4, block=128)
+        a.update(kw)
+        with pytest.raises(ValueError, match="32 bits"):
+            sdl.RequestPlan(**a, device=device)
+    for kw in (dict(T=2 ** 32 + 5), dict(B=2 ** 32 + 1), dict(q_heads=2 ** 33 + 4), dict(dk=2 ** 32 + 64)):
+        a = dict(B=1, H=4, T=10, dk=64, dv=64, q_heads=None)
+        a.update(kw)
+        with pytest.raises(ValueError, match="32 bits"):
+            sdl.make_hd_desc("bf16", a["B"], a["H"], a["T"], a["dk"], a["dv"], a["q_heads"])
+    with pytest.raises(ValueError, match="32 bits"):
+        sdl.HeadDecayDecode(torch.bfloat16, 3, 4, 64, 64, 2 ** 32 + 3, device=device)
