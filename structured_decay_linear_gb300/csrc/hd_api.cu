@@ -391,13 +391,14 @@ static bool ordered(const dplr_hd_desc* desc, long long max_blocks) {
 
 size_t dplr_hd_packed_workspace_size(const dplr_hd_desc* desc, int32_t R, int32_t block) {
     if (check_desc(desc) != DPLR_OK || desc->B != 1 || R < 1 || block < 32 || block % 32 != 0) return 0;
+    const long long most = (long long)desc->T / block + R;
     size_t off = kAlign;
     if (desc->T > block) {
-        const size_t n = (size_t)(desc->T / block + R) * desc->H;
+        const size_t n = (size_t)most * desc->H;
         off = up(off + n * state_bytes(desc));
         off = up(off + n * sizeof(float));
     }
-    if (ordered(desc, (long long)desc->T / block + R)) off = up(off + ((size_t)desc->T / block + R) * sizeof(int));
+    if (ordered(desc, most)) off = up(off + (size_t)most * sizeof(int));
     return off;
 }
 

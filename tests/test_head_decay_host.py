@@ -227,3 +227,12 @@ def test_sizes_beyond_32_bits_are_refused(sdl):
             sdl.make_hd_desc("bf16", a["B"], a["H"], a["T"], a["dk"], a["dv"], a["q_heads"])
     with pytest.raises(ValueError, match="32 bits"):
         sdl.HeadDecayDecode(torch.bfloat16, 3, 4, 64, 64, 2 ** 32 + 3, device=device)
+
+
+def test_workspace_of_a_ragged_batch_is_counted_without_overflow(sdl):
+    """R requests and T / block blocks more may pass 31 bits: states and gate sums of all of them, 256-byte aligned."""
+    d = sdl.make_hd_desc("f32", 1, 2, 1 << 20, 64, 32)
+    for R in (1, 8192, 2 ** 31 - 32768, 2 ** 31 - 1):
+        n = ((1 << 20) // 32 + R) * 2
+        up = lambda x: -(-x // 256) * 256  # noqa: E731
+        assert sdl.dplr_hd_packed_workspace_size(d, R, 32) == up(up(256 + n * 64 * 32 * 4) + n * 4)
