@@ -257,9 +257,10 @@ DPLR_API const char* dplr_gdp_path(const dplr_desc* desc);
  * Their data must be 16-byte aligned and their strides positive multiples of 16 bytes. Log-gates g <= 0 are fp32:
  * [B,H,T] with any non-negative strides, or with desc->per_head [H], contiguous (the strides are not looked at); -inf
  * forgets the state. States are fp32, contiguous [dk][dv] per (batch, head) or (slot, head), 16-byte aligned.
- * dk, dv in {32, 64, 128}; H a multiple of Hq; B*H < 2^24; T >= 0 with B*H*T < 2^31. Outputs must not overlap inputs
- * or one another (one that starts where another tensor does is refused); S_T may be S0. A non-finite value of a token reaches the outputs of the tokens after it and may reach those of the
- * up to 127 tokens before it (the chunk that is computed together), never another batch entry, head or request.
+ * dk, dv in {32, 64, 128}; H a multiple of Hq; B*H < 2^24; T >= 0 with B*H*T < 2^31. Outputs and the pool
+ * of states must not overlap inputs, the workspace or one another (one that starts where another of these does is
+ * refused); S_T may be S0. A non-finite value of a token reaches the outputs of the tokens after it and may reach those
+ * of the up to 127 tokens before it (the chunk that is computed together), never another batch entry, head or request.
  * Results do not depend on timing (fixed orders of summation, no atomics on values). Workspaces are 256-byte aligned
  * device memory of the caller, not shared by calls that overlap; the first 256 bytes hold a status word as described
  * for dplr_la_workspace_size (zero it once; read it with dplr_la_read_status). Nothing is allocated. */

@@ -1,7 +1,5 @@
 // Host side of the per-head-decay operator's C ABI: checks, segment and workspace plans, and the launches of the forward,
 // the backward, the ragged forward and the one-token step (hd_internal.h has the operator and its passes).
-#include <initializer_list>
-
 #include "hd_internal.h"
 
 namespace dplr {
@@ -81,14 +79,6 @@ bool state_ok(const void* p, bool needed) {
 dplr_status check_workspace(size_t need, const void* ws, size_t bytes) {
     if (!ws || bytes < need || (reinterpret_cast<uintptr_t>(ws) % kAlign) != 0) return DPLR_ERR_WORKSPACE;
     return DPLR_OK;
-}
-
-// Whether an output starts where an input or another output does: a result fed back into the object that holds it, which
-// the kernels would overwrite while others still read it.
-bool taken(const void* out, std::initializer_list<const void*> others) {
-    for (const void* p : others)
-        if (out && out == p) return true;
-    return false;
 }
 
 // ---- segments of a dense batch
@@ -236,7 +226,8 @@ dplr_status dplr_hd_forward(const dplr_hd_desc* desc, const dplr_hd_tensor* q, c
     if (!state_ok(S0, false) || !state_ok(S_T, false)) return DPLR_ERR_INVALID_ARG;
     const ForwardPlan pl = forward_plan(desc);
     HD_TRY(check_workspace(pl.total, workspace, ws_bytes));
-    if (taken(vo.p, {vq.p, vk.p, vv.p})) return DPLR_ERR_INVALID_ARG;
+    if (taken({vo.p, S_T}, {vq.p, vk.p, vv.p, g.p, S_T == S0 ? nullptr : S0, workspace}) || (vo.p && vo.p == S0))
+        return DPLR_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (desc->T == 0) {
         HD_CUDA(copy_state(S_T, S0, (size_t)desc->B * desc->H * state_bytes(desc), s));
@@ -293,8 +284,7 @@ dplr_status dplr_hd_backward(const dplr_hd_desc* desc, const dplr_hd_tensor* q, 
     if (ddecay && (reinterpret_cast<uintptr_t>(ddecay) & 3u)) return DPLR_ERR_INVALID_ARG;
     const BackwardPlan pl = backward_plan(desc);
     HD_TRY(check_workspace(pl.total, workspace, ws_bytes));
-    if (taken(vdq.p, {vq.p, vk.p, vv.p, vdo.p, vdk.p, vdv.p}) || taken(vdk.p, {vq.p, vk.p, vv.p, vdo.p, vdv.p}) ||
-        taken(vdv.p, {vq.p, vk.p, vv.p, vdo.p}) || taken(dS0, {S0, dST}) || taken(ddecay, {g.p}))
+    if (taken({vdq.p, vdk.p, vdv.p, ddecay, dS0}, {vq.p, vk.p, vv.p, g.p, S0, vdo.p, dST, workspace}))
         return DPLR_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const long long bh = (long long)desc->B * desc->H;
@@ -420,7 +410,7 @@ dplr_status dplr_hd_forward_packed(const dplr_hd_desc* desc, int32_t R, int32_t 
     HD_TRY(view_of(desc, o, desc->H, desc->dv, true, &vo));
     HD_TRY(gates_of(desc, decay, &g));
     HD_TRY(check_workspace(dplr_hd_packed_workspace_size(desc, R, block), workspace, ws_bytes));
-    if (taken(vo.p, {vq.p, vk.p, vv.p})) return DPLR_ERR_INVALID_ARG;
+    if (taken({vo.p, S}, {vq.p, vk.p, vv.p, g.p, blocks, block_starts, slots, context, workspace})) return DPLR_ERR_INVALID_ARG;
     if (desc->T == 0) return DPLR_OK;
     const long long max_blocks = (long long)desc->T / block + R;
     if (max_blocks * desc->H >= (1LL << 24) || (long long)R * desc->H >= (1LL << 24)) return DPLR_ERR_UNSUPPORTED;
@@ -479,7 +469,7 @@ dplr_status dplr_hd_decode_step(const dplr_hd_desc* desc, int32_t n_slots, const
     HD_TRY(gates_of(desc, decay, &g));
     if (!slots || (reinterpret_cast<uintptr_t>(slots) & 3u) || !state_ok(S, true)) return DPLR_ERR_INVALID_ARG;
     if (status && (reinterpret_cast<uintptr_t>(status) & 3u)) return DPLR_ERR_INVALID_ARG;
-    if (taken(vo.p, {vq.p, vk.p, vv.p})) return DPLR_ERR_INVALID_ARG;
+    if (taken({vo.p, S, status}, {vq.p, vk.p, vv.p, g.p, slots})) return DPLR_ERR_INVALID_ARG;
     HD_CUDA(launch_decode(vq, vk, vv, g.p, g.sb, g.sh, S, slots, n_slots, desc->B, desc->H, desc->dk, desc->dv,
                           desc->in_dtype == DPLR_BF16, const_cast<void*>(vo.p), vo.sb, vo.sh, status,
                           static_cast<cudaStream_t>(stream)));

@@ -14,6 +14,8 @@
 // into the boundary states, and "outputs" passes compute every segment from its boundary state.
 #pragma once
 
+#include <initializer_list>
+
 #include "dplr_internal.h"
 
 namespace dplr {
@@ -21,6 +23,19 @@ namespace hd {
 
 constexpr int kChunk = 128;           // tokens that the tensor-core kernels compute together
 constexpr float kMinGate = -128.f;    // log-gates below this act like it: e^-128 is zero in fp32
+
+// Whether an output starts where an input or another output does: a result fed back into the object that holds it, which
+// the kernels would overwrite while others still read it.
+inline bool taken(std::initializer_list<const void*> outputs, std::initializer_list<const void*> inputs) {
+    for (auto o = outputs.begin(); o != outputs.end(); ++o) {
+        if (!*o) continue;
+        for (const void* p : inputs)
+            if (p == *o) return true;
+        for (auto p = outputs.begin(); p != o; ++p)
+            if (*p == *o) return true;
+    }
+    return false;
+}
 
 // Kernels of one call are launched so that the next begins while the one before still runs (programmatic dependent launch):
 // it sets itself up and reads the caller's inputs, and calls wait_for_kernel_before() in front of the first access to

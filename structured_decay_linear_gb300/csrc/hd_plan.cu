@@ -5,7 +5,7 @@
 // is a launch and the scan's latency for few requests, and for many the bytes of the tables (8 a row of the batch).
 // Four requests and four rows a thread: one turn of the scan, one bisection and 16-byte stores for the four. Measured: 12
 // requests 5 us, 1500 with 200 K rows 7 us (10 us with one request and one row a thread at a time).
-#include "dplr_internal.h"
+#include "hd_internal.h"
 
 namespace dplr {
 namespace hd {
@@ -176,6 +176,9 @@ extern "C" dplr_status dplr_hd_plan(int32_t R, int32_t capacity, int32_t block, 
     auto ok = [](const void* p, unsigned al) { return p && (reinterpret_cast<uintptr_t>(p) & (al - 1)) == 0; };
     if (!ok(lengths, 4) || !ok(slots, 4) || !ok(context, 4) || !ok(starts, 4) || !ok(blocks, 16) || !ok(block_starts, 4) ||
         !ok(status, 4) || (capacity > 0 && (!ok(token_slot, 4) || !ok(token_pos, 4))))
+        return DPLR_ERR_INVALID_ARG;
+    if (taken({starts, blocks, block_starts, status, capacity > 0 ? token_slot : nullptr, capacity > 0 ? token_pos : nullptr},
+              {lengths, slots, context}))
         return DPLR_ERR_INVALID_ARG;
     PlanArgs a{R, capacity, block, n_slots, capacity / block + R, lengths, slots, context, starts,
                reinterpret_cast<int4*>(blocks), block_starts, token_slot, token_pos, status};

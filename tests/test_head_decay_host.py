@@ -236,3 +236,52 @@ def test_workspace_of_a_ragged_batch_is_counted_without_overflow(sdl):
         n = ((1 << 20) // 32 + R) * 2
         up = lambda x: -(-x // 256) * 256  # noqa: E731
         assert sdl.dplr_hd_packed_workspace_size(d, R, 32) == up(up(256 + n * 64 * 32 * 4) + n * 4)
+
+
+def test_every_output_on_top_of_another_tensor_is_refused(sdl):
+    """All pairs of an output and another tensor that start at the same address, for each call. (S_T may be S0.)"""
+    at = lambda i: FAKE + (i << 30)  # noqa: E731
+    d = sdl.make_hd_desc("bf16", 2, 4, 100, 128, 128)
+    one = sdl.make_hd_desc("bf16", 5, 4, 1, 128, 128)
+    ragged = sdl.make_hd_desc("bf16", 1, 4, 100, 128, 128)
+
+    def row(desc, p):
+        return tensor(sdl, desc.B, 4, desc.T, 128, data=p)
+
+    def gates(desc, p):
+        return sdl.dplr_hd_tensor(p, 4 * desc.T, desc.T, 1)
+
+    def forward_call(q, k, v, decay, S0, o, S_T, ws):
+        r = lambda p: row(d, p)  # noqa: E731
+        return sdl.dplr_hd_forward(d, r(q), r(k), r(v), gates(d, decay), S0, r(o), S_T, ws, sdl.dplr_hd_workspace_size(d),
+                                   None)
+
+    def backward_call(q, k, v, decay, S0, dO, dST, dq, dk, dv, ddecay, dS0, ws):
+        r = lambda p: row(d, p)  # noqa: E731
+        return sdl.dplr_hd_backward(d, r(q), r(k), r(v), gates(d, decay), S0, r(dO), dST, r(dq), r(dk), r(dv), ddecay, dS0,
+                                    ws, sdl.dplr_hd_backward_workspace_size(d), None)
+
+    def packed_call(blocks, block_starts, slots, context, q, k, v, decay, S, o, ws):
+        r = lambda p: row(ragged, p)  # noqa: E731
+        return sdl.dplr_hd_forward_packed(ragged, 3, 64, 8, blocks, block_starts, slots, context, r(q), r(k), r(v),
+                                          gates(ragged, decay), S, r(o), ws,
+                                          sdl.dplr_hd_packed_workspace_size(ragged, 3, 64), None)
+
+    def decode_call(slots, q, k, v, decay, S, o, status):
+        r = lambda p: row(one, p)  # noqa: E731
+        return sdl.dplr_hd_decode_step(one, 8, slots, r(q), r(k), r(v), gates(one, decay), S, r(o), status, None)
+
+    def plan_call(lengths, slots, context, starts, blocks, block_starts, token_slot, token_pos, status):
+        return sdl.dplr_hd_plan(4, 100, 128, 8, lengths, slots, context, starts, blocks, block_starts, token_slot, token_pos,
+                                status, None)
+
+    for call, outputs in ((forward_call, "o S_T"), (backward_call, "dq dk dv ddecay dS0"), (packed_call, "S o"),
+                          (decode_call, "S o status"),
+                          (plan_call, "starts blocks block_starts token_slot token_pos status")):
+        names = call.__code__.co_varnames[:call.__code__.co_argcount]
+        for out in outputs.split():
+            for other in names:
+                if other != out and {out, other} != {"S_T", "S0"}:
+                    p = {n: at(i) for i, n in enumerate(names)}
+                    p[out] = p[other]
+                    assert call(**p) == 1, (call.__name__, out, other)
