@@ -755,7 +755,8 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                     g.ostep = ostep;
                     g.wstep = wstep;
                 }
-                passed += all;
+                // (kept above e^-700000, which is zero: the sum over a block of millions of forgetting tokens passes 63 bits)
+                passed = max(passed + all, -(1LL << 52));
                 arrive(&g_full[it & 1]);
                 if (!STATES && j == 0) {
                     after = __shfl_sync(0xffffffffu, after, 0);

@@ -873,3 +873,25 @@ def test_blocks_longer_than_anything(sdl, block):
         out.append((f(x["q"], x["k"], x["v"], x["decay"], pool), pool))
         assert f.device_status() == 0
     assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
+
+
+def test_a_block_that_forgets_millions_of_times(sdl):
+    """A request of two blocks, the first of 12 million tokens of which each forgets all before it: the sum of the gates
+    is past every fixed-point range, and the request ends with its last token alone."""
+    import torch
+    block, n, d = 12_000_000, 12_000_200, 64
+    gen = torch.Generator(device="cuda").manual_seed(61)
+    x = torch.empty(n, 1, d, device="cuda", dtype=torch.bfloat16)
+    for i in range(0, n, 1_000_000):
+        x[i:i + 1_000_000] = torch.randn(min(1_000_000, n - i), 1, d, device="cuda", generator=gen).bfloat16()
+    i32 = lambda *v: torch.tensor(v, device="cuda", dtype=torch.int32)  # noqa: E731
+    f = sdl.HeadDecayPacked(torch.bfloat16, 1, n, 1, 1, d, d, per_head=True, plan=sdl.RequestPlan(1, n, 1, block))
+    pool = torch.randn(1, 1, d, d, device="cuda", generator=gen)
+    f.plan(i32(n), i32(0), i32(3))
+    o = f(x, x, x, torch.full((1,), float("-inf"), device="cuda"), pool)
+    assert f.device_status() == 0
+    last = host(x[-1, 0])
+    assert rel(host(pool[0, 0]), np.outer(last, last)) <= REL["f32"]
+    for a, b in ((0, 300), (block - 300, block + 200)):
+        y = host(x[a:b, 0])
+        assert rel(host(o[a:b, 0]), (y * y).sum(1, keepdims=True) * y) <= REL["bf16"]
