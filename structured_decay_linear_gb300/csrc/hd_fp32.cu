@@ -187,18 +187,18 @@ __device__ __forceinline__ void segment_pass(const Pass& p, const Geometry& geo,
         const float graw = gr;
         if (jj + 1 < nchunk) take(jj + 1);
         if (tid < 32) {
-            // Sums in fixed point (32 fractional bits, 64 in all): after a gate of -100 those between later tokens still
+            // Sums in fixed point (40 fractional bits, 64 in all): after a gate of -100 those between later tokens still
             // count. (64-bit floating point has few units here.)
             const bool bad = !(graw <= 1e4f);      // NaN (gates are not positive; one that large is no gate either)
             const uint32_t nan = __ballot_sync(0xffffffffu, bad);
-            long long g = __float2ll_rn((bad ? 0.f : graw < kMinGate ? kMinGate : graw) * 4294967296.f);
+            long long g = __float2ll_rn((bad ? 0.f : graw < kMinGate ? kMinGate : graw) * kGateUnits);
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
                 const long long y = __shfl_up_sync(0xffffffffu, g, off);
                 if (tid >= off) g += y;
             }
             const long long gn = __shfl_sync(0xffffffffu, g, 31);
-            const float lost = __int_as_float(0x7fc00000), scale = 2.3283064365386963e-10f;     // 2^-32
+            const float lost = __int_as_float(0x7fc00000), scale = kGateUnit;
             const float any = nan ? lost : 0.f, upto = nan & (0xffffffffu >> (31 - tid)) ? lost : 0.f;
             const float all = __ll2float_rn(gn) * scale + any, rest = __ll2float_rn(gn - g) * scale + any;
             const float hi = __ll2float_rn(g);

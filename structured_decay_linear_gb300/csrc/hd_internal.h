@@ -24,6 +24,12 @@ namespace hd {
 constexpr int kChunk = 128;           // tokens that the tensor-core kernels compute together
 constexpr float kMinGate = -128.f;    // log-gates below this act like it: e^-128 is zero in fp32
 
+// Sums of gates are formed in fixed point, 40 fractional bits of 64: with 32, gates of some 1e-10 became zero or twice what
+// they are, and a state that 2^21 such tokens had passed was off by 1.7e-4 (2^22: 3.3e-4). A chunk's sum stays below 2^15
+// (a token's below 185), and a sum over chunks is kept above -kForgotten, at which its exponential has long been zero.
+constexpr float kGateUnits = 1099511627776.f, kGateUnit = 9.094947017729282e-13f;     // 2^40 and 2^-40
+constexpr long long kForgotten = 1LL << 52;                                           // 4096
+
 // Whether an output starts where an input or another output does: a result fed back into the object that holds it, which
 // the kernels would overwrite while others still read it.
 inline bool taken(std::initializer_list<const void*> outputs, std::initializer_list<const void*> inputs) {

@@ -626,9 +626,9 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
         __syncwarp();
     } else if (warp == 22) {
         // =================== gates: lane holds tokens 4 lane .. 4 lane + 3 ===================
-        // Sums in fixed point (log2 units, 32 fractional bits, 64 in all): exact, and unlike 64-bit floating point (with
+        // Sums in fixed point (units of log2, 40 fractional bits, 64 in all): exact, and unlike 64-bit floating point (with
         // which this warp took 6.6 K cycles a chunk and held up all others) a few integer instructions each.
-        auto real = [](long long x) { return (float)x * 2.3283064365386963e-10f; };     // 2^-32
+        auto real = [](long long x) { return (float)x * kGateUnit; };
         uint32_t it = 0;
         auto take = [&]() -> GateBuf* {       // the next buffer, once its chunk before the last is done with
             const uint32_t b = it & 1;
@@ -704,7 +704,7 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                 for (int i = 0; i < 4; ++i) {
                     nan |= !(cur[i] <= 1e4f);        // (gates are not positive; one that large is no gate either)
                     const float g = cur[i] < kMinGate ? kMinGate : cur[i];
-                    x[i] = __float2ll_rn(g * (float)kLog2e * 4294967296.f) + (i > 0 ? x[i - 1] : 0);
+                    x[i] = __float2ll_rn(g * (float)kLog2e * kGateUnits) + (i > 0 ? x[i - 1] : 0);
                 }
                 if (__any_sync(0xffffffffu, nan)) lost = __int_as_float(0x7fc00000);
                 long long s = x[3];
@@ -755,8 +755,7 @@ __global__ void __launch_bounds__(NT, 1) hd_tc_kernel(const __grid_constant__ Ar
                     g.ostep = ostep;
                     g.wstep = wstep;
                 }
-                // (kept above e^-700000, which is zero: the sum over a block of millions of forgetting tokens passes 63 bits)
-                passed = max(passed + all, -(1LL << 52));
+                passed = max(passed + all, -kForgotten);      // (over a block of many forgetting tokens it would pass 63 bits)
                 arrive(&g_full[it & 1]);
                 if (!STATES && j == 0) {
                     after = __shfl_sync(0xffffffffu, after, 0);

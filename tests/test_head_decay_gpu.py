@@ -895,3 +895,35 @@ def test_a_block_that_forgets_millions_of_times(sdl):
     for a, b in ((0, 300), (block - 300, block + 200)):
         y = host(x[a:b, 0])
         assert rel(host(o[a:b, 0]), (y * y).sum(1, keepdims=True) * y) <= REL["bf16"]
+
+
+@pytest.mark.parametrize("dtype,d,T", [("bf16", 64, 1 << 21), ("f32", 32, 1 << 22)])
+def test_gates_close_to_zero_add_up(sdl, dtype, d, T):
+    """A gate of -2^-33.6 a token: nothing for one, 1.7e-4 and 3.3e-4 over a long sequence. Only the first token writes, so
+    S_T = e^{gT} S0 + e^{g(T-1)} k_0 v_0^T and o_t = S_t^T q_t without other terms.
+
+    Bound: each of the at most 152 (fp32: 304) segments multiplies a state by one exponential and the last one by one per
+    chunk of 128 (32) tokens more, each within 2^-22 of its value and rounded once (2^-24): 7.7e-5 (fp32: 2.2e-4). o adds
+    its own error (REL)."""
+    import torch
+    g = -0.34 * 2.0 ** -32
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    gen = torch.Generator(device="cuda").manual_seed(60)
+    x = torch.zeros(1, 1, T, d, device="cuda", dtype=dt)
+    x[0, 0, 0] = torch.randn(d, device="cuda", generator=gen).to(dt)
+    x[0, 0, 1:] = 0
+    q = torch.zeros_like(x)
+    q[0, 0, -64:] = torch.randn(64, d, device="cuda", generator=gen).to(dt)
+    S0 = torch.randn(1, 1, d, d, device="cuda", generator=gen)
+    decay = torch.full((1,), g, device="cuda")
+    f = sdl.HeadDecay(dt, 1, 1, T, d, d, per_head=True)
+    o, S_T = f(q, x, x, decay, S0=S0)
+    g = float(decay.double().item())
+    w = host(x[0, 0, 0])
+    S = np.exp(g * T) * host(S0[0, 0]) + np.exp(g * (T - 1)) * np.outer(w, w)
+    segments, chunk = (152, 128) if dtype == "bf16" else (304, 32)
+    bound = (segments + T / segments / chunk) * (2.0 ** -22 + 2.0 ** -24)
+    assert bound < -g * T                                     # the gates' own effect is larger
+    assert rel(host(S_T[0, 0]), S) <= bound
+    assert rel(host(o[0, 0, -64:]), host(q[0, 0, -64:]) @ S) <= bound + REL[dtype]
+    assert f.device_status() == 0
