@@ -927,3 +927,46 @@ def test_gates_close_to_zero_add_up(sdl, dtype, d, T):
     assert rel(host(S_T[0, 0]), S) <= bound
     assert rel(host(o[0, 0, -64:]), host(q[0, 0, -64:]) @ S) <= bound + REL[dtype]
     assert f.device_status() == 0
+
+
+@pytest.mark.parametrize("lengths,H,Hq,dk,dv,block,per_head", [
+    ([33, 31, 32, 65, 1, 0, 200], 3, 3, 128, 128, 32, False),
+    ([300, 1, 64, 63, 129], 2, 1, 64, 64, 64, True),
+    ([97, 96, 95, 500, 2], 4, 2, 128, 64, 96, False),
+    ([400, 161, 7], 2, 2, 64, 128, 160, True),
+    ([1, 40] * 30 + [700], 8, 8, 64, 64, 32, False),
+    ([130] * 24, 16, 4, 128, 128, 96, False),
+])
+def test_packed_in_blocks_shorter_than_a_chunk(sdl, lengths, H, Hq, dk, dv, block, per_head):
+    """Blocks that are no multiple of 128 tokens put short chunks inside a request on the tensor cores too; each request
+    against its own recurrence, twice with the same bits."""
+    import torch
+    R = len(lengths)
+    x, cap = ragged("bf16", lengths, H, Hq, dk, dv, 3, per_head, seed=63)
+    for name in ("q", "k", "v"):
+        x[name][sum(lengths):] = float("nan")
+    i32 = lambda v: torch.tensor(v, device="cuda", dtype=torch.int32)  # noqa: E731
+    f = sdl.HeadDecayPacked(torch.bfloat16, R, cap, R, H, dk, dv, q_heads=Hq, per_head=per_head,
+                            plan=sdl.RequestPlan(R, cap, R, block))
+    assert f.path == "hd_tcgen05"
+    start, out = torch.randn(R, H, dk, dv, device="cuda"), []
+    f.plan(i32(lengths), i32(list(range(R))), i32([r % 2 for r in range(R)]))
+    for _ in range(2):
+        pool = start.clone()
+        f.o.fill_(7.0)
+        f(x["q"], x["k"], x["v"], x["decay"], pool)
+        out.append((f.o.clone(), pool))
+        assert f.plan.device_status() == 0 and f.device_status() == 0
+    (o, pool), (o2, pool2) = out
+    assert torch.equal(o, o2) and torch.equal(pool, pool2)
+    at = 0
+    for r, n in enumerate(lengths):
+        if n == 0:
+            assert torch.equal(pool[r], start[r])
+            continue
+        y = {name: (t if t.dim() == 1 else t[at:at + n].transpose(0, 1)[None]) for name, t in x.items()}
+        if r % 2:
+            y["S0"] = start[r][None]
+        check_forward("bf16", o[at:at + n].transpose(0, 1)[None], pool[r][None], want(y))
+        at += n
+    assert (o[at:] == 7.0).all()
