@@ -719,13 +719,15 @@ def dplr_hd_decode_step(desc, n_slots, slots, q, k, v, decay, S, o, status, stre
 
 class _Slots:
     """The dplr_hd_tensor arguments of one prepared call, in one buffer that each call fills anew: a call's host time is
-    its launches', and building a ctypes structure per tensor and call took longer than those."""
+    its launches', and building a ctypes structure per tensor and call took longer than those. `turn` is held from filling
+    it to the end of the C call, which reads it: another thread may call the same object."""
 
     def __init__(self, n: int):
         self.buf = ctypes.create_string_buffer(32 * n)
         at = ctypes.addressof(self.buf)
         self.refs = [ctypes.cast(at + 32 * i, ctypes.POINTER(dplr_hd_tensor)) for i in range(n)]
         self.fill = struct.Struct(f"={4 * n}q").pack_into
+        self.turn = threading.Lock()
 
     def __call__(self, *values):
         self.fill(self.buf, 0, *values)
@@ -857,12 +859,13 @@ class HeadDecay(_HeadDecayBase):
         pg, sg = self._gates(decay, (B, H, T))
         o, so = self.o, self.o.stride()
         f = self._slots
-        f(pq, sq[0], sq[1], sq[2], pk, sk[0], sk[1], sk[2], pv, sv[0], sv[1], sv[2], pg, sg[0], sg[1], sg[2], o.data_ptr(),
-          so[0], so[1], so[2])
-        r = f.refs
-        self._call(self._fn, "dplr_hd_forward", stream, r[0], r[1], r[2], r[3],
-                   self._state(S0, "S0", (B, H, self.dk, self.dv)), r[4], self.S_T.data_ptr(), self.workspace.data_ptr(),
-                   self.ws_bytes)
+        with f.turn:
+            f(pq, sq[0], sq[1], sq[2], pk, sk[0], sk[1], sk[2], pv, sv[0], sv[1], sv[2], pg, sg[0], sg[1], sg[2],
+              o.data_ptr(), so[0], so[1], so[2])
+            r = f.refs
+            self._call(self._fn, "dplr_hd_forward", stream, r[0], r[1], r[2], r[3],
+                       self._state(S0, "S0", (B, H, self.dk, self.dv)), r[4], self.S_T.data_ptr(),
+                       self.workspace.data_ptr(), self.ws_bytes)
         return o, self.S_T
 
 
@@ -892,11 +895,12 @@ class HeadDecayBackward(_HeadDecayBase):
         G = self.grads
         at += [(G[n].data_ptr(), G[n].stride()) for n in ("q", "k", "v")]
         f = self._slots
-        f(*[x for p, st in at for x in (p, st[0], st[1], st[2])])
-        r = f.refs
-        self._call(self._fn, "dplr_hd_backward", stream, r[0], r[1], r[2], r[3], self._state(S0, "S0", state), r[4],
-                   self._state(dST, "dST", state), r[5], r[6], r[7], G["decay"].data_ptr() if decay_grad else None,
-                   G["S0"].data_ptr(), self.workspace.data_ptr(), self.ws_bytes)
+        with f.turn:
+            f(*[x for p, st in at for x in (p, st[0], st[1], st[2])])
+            r = f.refs
+            self._call(self._fn, "dplr_hd_backward", stream, r[0], r[1], r[2], r[3], self._state(S0, "S0", state), r[4],
+                       self._state(dST, "dST", state), r[5], r[6], r[7], G["decay"].data_ptr() if decay_grad else None,
+                       G["S0"].data_ptr(), self.workspace.data_ptr(), self.ws_bytes)
         return G if decay_grad else {n: t for n, t in G.items() if n != "decay"}
 
 
@@ -979,11 +983,13 @@ class HeadDecayPacked(_HeadDecayBase):
         if S is None:
             raise ValueError("S is required")
         f = self._slots
-        f(*[x for ptr, st in at for x in (ptr, 0, st[1], st[0])])
-        r = f.refs
-        self._call(self._fn, "dplr_hd_forward_packed", stream, p.R, p.block, self.n_slots, p.blocks.data_ptr(),
-                   p.block_starts.data_ptr(), p.slots.data_ptr(), p.context.data_ptr(), r[0], r[1], r[2], r[3],
-                   self._state(S, "S", (self.n_slots, H, self.dk, self.dv)), r[4], self.workspace.data_ptr(), self.ws_bytes)
+        with f.turn:
+            f(*[x for ptr, st in at for x in (ptr, 0, st[1], st[0])])
+            r = f.refs
+            self._call(self._fn, "dplr_hd_forward_packed", stream, p.R, p.block, self.n_slots, p.blocks.data_ptr(),
+                       p.block_starts.data_ptr(), p.slots.data_ptr(), p.context.data_ptr(), r[0], r[1], r[2], r[3],
+                       self._state(S, "S", (self.n_slots, H, self.dk, self.dv)), r[4], self.workspace.data_ptr(),
+                       self.ws_bytes)
         return o
 
 
@@ -1031,9 +1037,10 @@ class HeadDecayDecode(_HeadDecayBase):
                 not slots.is_contiguous():
             _need(slots, "slots", self.device, torch.int32, (n,))
         f = self._slots
-        f(pq, sq[0], sq[1], 0, pk, sk[0], sk[1], 0, pv, sv[0], sv[1], 0, pg, sg[0], sg[1], 0, o.data_ptr(), H * self.dv,
-          self.dv, 0)
-        r = f.refs
-        self._call(self._fn, "dplr_hd_decode_step", stream, self.n_slots, slots.data_ptr(), r[0], r[1], r[2], r[3],
-                   self._state(S, "S", (self.n_slots, H, self.dk, self.dv)), r[4], self.status.data_ptr())
+        with f.turn:
+            f(pq, sq[0], sq[1], 0, pk, sk[0], sk[1], 0, pv, sv[0], sv[1], 0, pg, sg[0], sg[1], 0, o.data_ptr(), H * self.dv,
+              self.dv, 0)
+            r = f.refs
+            self._call(self._fn, "dplr_hd_decode_step", stream, self.n_slots, slots.data_ptr(), r[0], r[1], r[2], r[3],
+                       self._state(S, "S", (self.n_slots, H, self.dk, self.dv)), r[4], self.status.data_ptr())
         return o

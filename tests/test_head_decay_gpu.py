@@ -970,3 +970,44 @@ def test_packed_in_blocks_shorter_than_a_chunk(sdl, lengths, H, Hq, dk, dv, bloc
         check_forward("bf16", o[at:at + n].transpose(0, 1)[None], pool[r][None], want(y))
         at += n
     assert (o[at:] == 7.0).all()
+
+
+def test_one_object_called_by_several_threads(sdl):
+    """A prepared step used by four threads on one stream, each with a pool and inputs of its own: every pool gets its own
+    thread's tokens, also if another thread comes between a call's arguments and the C call. (The output is the object's, so
+    threads that read it take turns by themselves.)"""
+    import threading
+    import time
+
+    import torch
+    N, H, d, steps, threads = 4, 2, 32, 50, 4
+    step = sdl.HeadDecayDecode(torch.float32, N, H, d, d, N)
+    launch = step._fn
+
+    def interrupted(*a):
+        time.sleep(1e-5)
+        return launch(*a)
+
+    slot = torch.arange(N, device="cuda", dtype=torch.int32)
+    x = [[make("f32", N, H, H, 1, d, d, state=False, seed=70 + 10 * i + j) for j in range(2)] for i in range(threads)]
+    rows = [[[y[n][:, :, 0] for n in ("q", "k", "v", "decay")] for y in xs] for xs in x]
+    start = torch.randn(N, H, d, d, device="cuda")
+
+    def run(i, pool):
+        for t in range(steps):
+            step(*rows[i][t % 2], pool, slot)
+
+    alone = [start.clone() for _ in range(threads)]
+    for i in range(threads):
+        run(i, alone[i])
+    step._fn = interrupted
+    for _ in range(3):
+        pools = [start.clone() for _ in range(threads)]
+        torch.cuda.synchronize()
+        team = [threading.Thread(target=run, args=(i, pools[i])) for i in range(threads)]
+        for t in team:
+            t.start()
+        for t in team:
+            t.join()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(alone, pools))
