@@ -1,10 +1,11 @@
 // The small steps between the passes of the per-head-decay operator: boundary states from segments' own contributions,
-// the gradient of the log-gates, and the sums over value heads that share a query/key head. All are bound by the
-// bytes that they move; none uses atomics on values, so their results do not depend on timing.
+// the gradient of the log-gates, and the sums over value heads that share a query/key head. None uses atomics on values,
+// so their results do not depend on timing.
 //
-// Measured: boundary states of B4 H16 T4096, 128 x 128, eight segments a head, both directions: 19 us for 137 MB read and
-// 151 MB written (mostly in L2); the gates' gradient of the same: 19.5 us, 137 MB at 7 TB/s; a ragged batch without a request
-// of two blocks: 3.5 us.
+// Measured: boundary states of B4 H16 T4096, 128 x 128, eight segments a head, both directions: 19 us for 63 MB read (15
+// contributions of 4.2 MB) and 71 MB written (17 boundaries, mostly into L2), 7 TB/s; the gates' gradient of the same: 20 us
+// for 61 MB, 3 TB/s: a CTA's chain (two states, their product, the sums over its tokens) takes that long, not the memory; a
+// ragged batch without a request of two blocks: 3.5 us.
 #include <cuda_bf16.h>
 
 #include "hd_internal.h"
