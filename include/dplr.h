@@ -260,7 +260,9 @@ DPLR_API const char* dplr_gdp_path(const dplr_desc* desc);
  * Accuracy: everything is summed in fp32. With bf16 inputs on the tensor cores the masked scores and the state that q
  * reads are rounded to bf16 once in front of their products, beside o's own rounding (o: 2.4e-3 of its 2-norm, 1.7e-3
  * from its own rounding alone); what enters a state has two bf16 parts (states and dS0: 3e-6 of their 2-norm, where fp32
- * inputs give 3e-7; ddecay: 6e-6, 3e-7).
+ * inputs give 3e-7; ddecay: 6e-6, 3e-7). ddecay is formed as sums of q_t . dq_t - k_t . dk_t, each off by some 1e-6 of
+ * its two terms however small the gradient itself is: for gates below about -5, which next to nothing depends on, few of
+ * its digits are right, and summed over tokens (per_head) 1e-3 of it.
  * dk, dv in {32, 64, 128}; H a multiple of Hq; B*H < 2^24; T >= 0 with B*H*T < 2^31. Outputs and the pool
  * of states must not overlap inputs, the workspace or one another (one that starts where another of these does is
  * refused); S_T may be S0. A non-finite value of a token reaches the outputs of the tokens after it and may reach those
