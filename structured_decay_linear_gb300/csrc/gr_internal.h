@@ -145,14 +145,15 @@ template <int GATE, int INPUT, bool WANT_M> __device__ __forceinline__ void deca
         const float2 t = mul2(g, both(kLog2e));
         a = make_float2(exp2_hw(t.x), exp2_hw(t.y));
         if (!WANT_M) return;
-        // 1 - e^g by its series up to g^6 above -1/4, where the next term is below 5e-8 of it; below, the difference loses two bits
+        // 1 - e^g by its series up to g^6 for |g| < 1/4, where the next term is below 5e-8 of it; beyond, gates above 0 among them,
+        // the difference loses two bits
         float2 p = fma2(g, both(-1.f / 720.f), both(-1.f / 120.f));
         p = fma2(g, p, both(-1.f / 24.f));
         p = fma2(g, p, both(-1.f / 6.f));
         p = fma2(g, p, both(-0.5f));
         p = fma2(g, p, both(-1.f));
         p = mul2(g, p);
-        m = make_float2(g.x > -0.25f ? p.x : 1.f - a.x, g.y > -0.25f ? p.y : 1.f - a.y);
+        m = make_float2(fabsf(g.x) < 0.25f ? p.x : 1.f - a.x, fabsf(g.y) < 0.25f ? p.y : 1.f - a.y);
         if (INPUT == kUnit) {
             const float2 s2 = mul2(m, add2(a, both(1.f)));
             m = make_float2(sqrt_hw(s2.x), sqrt_hw(s2.y));

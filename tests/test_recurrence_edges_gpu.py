@@ -1,0 +1,104 @@
+"""The elementwise gated recurrence where its arithmetic and its tables have edges: log-gates above 0."""
+
+import numpy as np
+import pytest
+
+from test_recurrence_gpu import DT, TYPES, dev, f32, near, ragged, sdl  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+# ---- log-gates above 0
+
+# Rounding errors of one token, relative: of a, from the hardware's power of two (2^-22) and from g log2(e) in 32 bits, its
+# product and its constant (|g| 2^-23.7); of 1 - a, from the series below |g| = 1/4 (its terms' roundings and what it leaves out,
+# 2^-22) or from the difference, which has a's error and a rounding. The scan adds six of 2^-24: its multiply-add and
+# product, a warp's and a tile's.
+def growing(input, x, g, h0=None, dy=None, dh=None):
+    """y, dx, dg, dh0 of log-gates of any sign, each with the bound of its error."""
+    B, T, D = x.shape
+    a, m = np.exp(g), -np.expm1(g)
+    ea = 2.0 ** -22 + np.abs(g) * 2.0 ** -23.7 + 6 * 2.0 ** -24
+    one = input == "plain"
+    s = np.ones_like(a) if one else m
+    es = np.zeros_like(a) if one else np.where(np.abs(g) < 0.25, 2.0 ** -22 * np.abs(m), a * ea) + 2.0 ** -24 * np.abs(m)
+    zero = np.zeros((B, D))
+    first = zero if h0 is None else h0.astype(np.float64)
+    h, M, e = first, np.abs(first), zero
+    y, mag, bound = np.empty((B, T, D)), np.empty((B, T, D)), np.empty((B, T, D))
+    for t in range(T):
+        b = s[:, t] * x[:, t]
+        e = a[:, t] * (e + ea[:, t] * M) + es[:, t] * np.abs(x[:, t]) + 2.0 ** -23 * np.abs(b)
+        h, M = a[:, t] * h + b, a[:, t] * M + np.abs(b)
+        y[:, t], mag[:, t], bound[:, t] = h, M, e
+    if dy is None:
+        return y, bound
+    E = zero if dh is None else dh.astype(np.float64)
+    N, eE = np.abs(E), zero
+    out = {n: (np.zeros((B, T, D)), np.zeros((B, T, D))) for n in ("x", "gate")}
+    for t in range(T - 1, -1, -1):
+        hp, Mp, ep = (y[:, t - 1], mag[:, t - 1], bound[:, t - 1]) if t else (first, np.abs(first), zero)
+        at, xt = a[:, t], x[:, t]
+        Dt, Dm = dy[:, t] + E, np.abs(dy[:, t]) + N
+        eD = eE + 2.0 ** -24 * Dm
+        out["x"][0][:, t] = s[:, t] * Dt
+        out["x"][1][:, t] = np.abs(s[:, t]) * (eD + 2.0 ** -24 * Dm) + es[:, t] * Dm
+        through, size = (hp, Mp) if one else (hp - xt, Mp + np.abs(xt))
+        out["gate"][0][:, t] = Dt * at * through
+        out["gate"][1][:, t] = at * (eD * size + Dm * (ep + (ea[:, t] + 3 * 2.0 ** -24) * size))
+        E, N, eE = at * Dt, at * Dm, at * (eD + ea[:, t] * Dm)
+    out["h0"] = (E, eE)
+    return y, bound, out
+
+
+def rising(shape, r):
+    """Log-gates of which a quarter lie between 0 and 4, at the series' ends among them, and the others forget what those grew."""
+    g = -r.uniform(0.5, 2.5, shape)
+    up = r.random(shape) < 0.25
+    g[up] = r.uniform(0, 4, up.sum())
+    g.reshape(-1)[:6] = [0.25, 0.2421875, 0.2578125, 1.0, 2.0, 4.0][:g.size]
+    return g
+
+
+@pytest.mark.parametrize("xt,gt", TYPES)
+@pytest.mark.parametrize("input", ["plain", "complement"])
+@pytest.mark.parametrize("B,T,D", [(1, 1, 8), (2, 40, 72), (1, 300, 24)])
+def test_gates_above_zero(sdl, input, xt, gt, B, T, D):  # noqa: F811
+    r = np.random.default_rng(31)
+    x, xv = dev(r.standard_normal((B, T, D)), xt)
+    g, gv = dev(rising((B, T, D), r), gt)
+    dy, dyv = dev(r.standard_normal((B, T, D)), xt)
+    h0 = r.standard_normal((B, D)).astype(np.float32)
+    f = sdl.GatedRecurrence(DT[xt], B, T, D, "log", input, DT[gt], keep_states=True)
+    y, hT = f(x, g, h0=f32(h0))
+    want, bound, grads = growing(input, xv, gv, h0, dyv)
+    near(y, want, bound, xt, "y")
+    near(hT, want[:, -1], bound[:, -1], "f32", "h_T")
+    d = sdl.GatedRecurrenceBackward(DT[xt], B, T, D, "log", input, DT[gt])(dy, None, x, g, h0=f32(h0), states=f.states)
+    near(d["x"], *grads["x"], xt, "dx")
+    near(d["gate"], *grads["gate"], gt, "dgate")
+    near(d["h0"], *grads["h0"], "f32", "dh0")
+
+
+@pytest.mark.parametrize("xt,gt", TYPES)
+def test_gates_above_zero_on_a_pool(sdl, xt, gt):  # noqa: F811
+    lengths, context, D = [1, 37, 0, 64], [0, 5, 0, 9], 72
+    r = np.random.default_rng(32)
+    p, x, xv, _, _, S0, slot = ragged(sdl, xt, gt, "log", "complement", lengths, context, D)
+    g, gv = dev(rising((sum(lengths), D), r), gt)
+    S, at = f32(S0), 0
+    y = p(x, g, S)
+    for n, s, c in zip(lengths, slot, context):
+        if n:
+            w, bound = growing("complement", xv[None, at:at + n], gv[None, at:at + n], S0[s:s + 1] if c else None)
+            near(y[at:at + n], w[0], bound[0], xt, "y")
+            near(S[s], w[0, -1], bound[0, -1], "f32", "state")
+        at += n
+    N = len(slot)
+    S, f = f32(S0), sdl.GatedRecurrenceDecode(DT[xt], N, D, S0.shape[0], "log", "complement", DT[gt])
+    y = f(x[:N], g[:N], S, torch.tensor(slot, dtype=torch.int32, device="cuda"))
+    for i, s in enumerate(slot):
+        w, bound = growing("complement", xv[None, i:i + 1], gv[None, i:i + 1], S0[s:s + 1])
+        near(y[i], w[0, 0], bound[0, 0], xt, "one token")
+        near(S[s], w[0, 0], bound[0, 0], "f32", "its state")
