@@ -34,10 +34,17 @@ __device__ __forceinline__ void store_record(Record* p, float A, float b, unsign
         :: "l"(p), "l"(lo), "l"(static_cast<uint64_t>(tag)) : "memory");
 }
 
-// The map h -> A h + b. RESET: tiles in which a request starts have A = 0, and what came before it does not reach it even if it
-// is not a number.
+// The map h -> A h + b. RESET: a request may start in its tokens. Such a map has A = -0, and what came before does not reach it
+// even if it is not a number. Products of decays are +0 and above: one that underflowed is not taken for a start, and a NaN or
+// an infinity goes on through it.
+constexpr float kReset = -0.f;
+__device__ __forceinline__ bool resets(float A) { return __float_as_uint(A) == 0x80000000u; }
 template <bool RESET> __device__ __forceinline__ float after(float A, float h, float b) {
-    return RESET && A == 0.f ? b : fmaf(A, h, b);
+    return RESET && resets(A) ? b : fmaf(A, h, b);
+}
+// The factor of a map behind one of factor `before`.
+template <bool RESET> __device__ __forceinline__ float joined(float A, float before) {
+    return RESET && resets(A) ? kReset : A * before;
 }
 
 // The walk of one channel, by one lane of the warp that looks after a tile's channels. `rec` is the channel in tile 0 of
@@ -128,7 +135,7 @@ __device__ __forceinline__ void join_runs(float2& A, float2& H, float2& Ax, floa
     Ax = last ? Ao : both(1.f);
     Hx = last ? Ho : both(0.f);
     H = make_float2(after<RESET>(A.x, Hx.x, H.x), after<RESET>(A.y, Hx.y, H.y));
-    A = make_float2(RESET && A.x == 0.f ? 0.f : A.x * Ax.x, RESET && A.y == 0.f ? 0.f : A.y * Ax.y);
+    A = make_float2(joined<RESET>(A.x, Ax.x), joined<RESET>(A.y, Ax.y));
 }
 
 // The launch's last CTA makes the counters ready for the next launch. By one thread, after its CTA's last access to the records.

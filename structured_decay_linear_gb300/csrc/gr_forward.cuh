@@ -190,7 +190,7 @@ gr_forward_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
                     if (start) av[i] = both(0.f);
                     A = mul2(A, av[i]);
                     H = fma2(av[i], H, bv[i]);
-                    if (start) { A = both(0.f); H = bv[i]; }    // whatever came before
+                    if (start) { A = both(kReset); H = bv[i]; }    // whatever came before
                 }
             } else {
 #pragma unroll
@@ -219,7 +219,7 @@ gr_forward_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
                 const float Av = aggA[v][cc];
                 preA[v][cc] = At;
                 preB[v][cc] = Ht;
-                At = PACKED && Av == 0.f ? 0.f : At * Av;
+                At = joined<PACKED>(Av, At);
                 Ht = after<PACKED>(Av, Ht, aggB[v][cc]);
             }
             Record* mine = rec + (long long)j * kCols;

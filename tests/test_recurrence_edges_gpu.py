@@ -1,4 +1,5 @@
-"""The elementwise gated recurrence where its arithmetic and its tables have edges: log-gates above 0."""
+"""The elementwise gated recurrence where its arithmetic and its tables have edges: log-gates above 0, values that are not finite in
+ragged batches."""
 
 import numpy as np
 import pytest
@@ -102,3 +103,44 @@ def test_gates_above_zero_on_a_pool(sdl, xt, gt):  # noqa: F811
         w, bound = growing("complement", xv[None, i:i + 1], gv[None, i:i + 1], S0[s:s + 1])
         near(y[i], w[0, 0], bound[0, 0], xt, "one token")
         near(S[s], w[0, 0], bound[0, 0], "f32", "its state")
+
+
+# ---- what is not finite, in ragged batches
+
+@pytest.mark.parametrize("xt,gt", TYPES)
+@pytest.mark.parametrize("gate,value", [("log", -1.0), ("log", -8.0), ("sigmoid", -1.0), ("log", -0.01), ("log", -np.inf)])
+def test_packed_not_finite_reaches_what_follows(sdl, gate, value, xt, gt):  # noqa: F811
+    """Over tokens and tiles whose product of decays is too small for a number, as the dense forward has it; the request in front, the
+    one behind and other channels never see it."""
+    lengths, D = [5, 1500, 700], 72
+    p, x, xv, g, gv, S0, slot = ragged(sdl, xt, gt, gate, "plain", lengths, [1, 1, 1], D)
+    g[...] = value
+    S = f32(S0)
+    clean, states = p(x, g, S).clone(), S.clone()
+    x[8, 3], x[5, 70], x[5 + 600, 40] = float("nan"), float("inf"), float("nan")
+    S = f32(S0)
+    y = p(x, g, S)
+    hit = torch.zeros_like(y, dtype=torch.bool)
+    hit[8:1505, 3] = hit[5:1505, 70] = hit[605:1505, 40] = True
+    assert torch.equal(y[~hit], clean[~hit]) and not torch.isfinite(y[hit]).any()
+    bad = torch.zeros_like(S, dtype=torch.bool)
+    bad[slot[1], [3, 40, 70]] = True
+    assert torch.equal(S[~bad], states[~bad]) and not torch.isfinite(S[bad]).any()
+    dense = sdl.GatedRecurrence(DT[xt], 1, 1500, D, gate, "plain", DT[gt])
+    h0 = f32(S0[slot[1]:slot[1] + 1])
+    yd, hd = dense(x[None, 5:1505], g[None, 5:1505], h0=h0)
+    assert torch.equal(torch.isfinite(yd[0]), torch.isfinite(y[5:1505]))
+    assert torch.equal(torch.isfinite(hd[0]), torch.isfinite(S[slot[1]]))
+
+
+@pytest.mark.parametrize("gate", ["log", "sigmoid"])
+def test_decays_are_not_below_zero(sdl, gate):  # noqa: F811
+    """A start in a ragged batch is told by a factor of -0, so no gate may give one: a state of 1 without an input becomes a."""
+    g = torch.cat([torch.linspace(-110, -80, 20000), torch.linspace(-1000, 0, 20001), torch.tensor([-float("inf"), -3e38, -88.0])])
+    D = g.numel()
+    f = sdl.GatedRecurrenceDecode(torch.float32, 1, D, 1, gate, "plain")
+    wide = torch.zeros(1, D + -D % 4, device="cuda")
+    wide[0, :D] = g.cuda()
+    S = torch.ones(1, D, device="cuda")
+    f(torch.zeros_like(wide)[:, :D], wide[:, :D], S, torch.zeros(1, dtype=torch.int32, device="cuda"))
+    assert not torch.signbit(S).any() and (S[0, -3:-1] == 0).all()
