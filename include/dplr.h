@@ -436,7 +436,8 @@ DPLR_API dplr_status dplr_gr_decode_step(const dplr_gr_desc* desc, int32_t n_slo
  * Frequencies are given as 64-bit fractions of a turn, turns[i] = f_i / (2 pi) * 2^64 on the device (dplr_nr_turns), so that
  * an angle is off by at most 2^-32 turns (and a position times 2^-65) at any position. Positions are int32 on the device, element (b, t) at
  * positions[b pos_sb + t pos_st] (strides >= 0, 0 repeats), or, where positions is null, first_position + t. A row with
- * a negative position holds no token: its outputs stay as they were, and it adds nothing to weight gradients.
+ * a negative position holds no token: the forward leaves its outputs as they were; the backward makes its dq and dk zero, and
+ * it adds nothing to weight gradients.
  * Tensors are dplr_hd_tensor with element strides along batch, head and token: q [B,Hq,T,d], k [B,Hk,T,d] (not looked at
  * with Hk = 0), outputs likewise with strides of their own, of in_dtype; data 16-byte aligned, strides positive multiples of
  * 16 bytes. fp32 arithmetic, one rounding; a head whose squares sum beyond 3e38 comes out as zeros, and one of zeros

@@ -82,11 +82,17 @@ __global__ void __launch_bounds__(kThreads, SUMS ? 6 : 8) nr_backward_kernel(con
     for (long long tok = (long long)cta * kWarps + w; tok < tokens; tok += (long long)ctas * kWarps) {
         const int b = (int)(tok / a.T), t = (int)(tok - (long long)b * a.T);
         const int pos = position(a, b, t);
-        if (pos < 0) continue;                                  // a row without a token
         const Rows &X = is_q ? a.q : a.k, &G = is_q ? a.gq : a.gk, &O = is_q ? a.oq : a.ok;
+        XT* op = static_cast<XT*>(const_cast<void*>(O.p)) + b * O.sb + t * O.st + mine * O.sh + f0;
+        if (pos < 0) {                                          // a row without a token: what is not used has no gradient
+            for (int h = mine; h < H; h += SIDE, op += SIDE * O.sh) {
+                *reinterpret_cast<uint4*>(op) = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4*>(op + to_f1) = make_uint4(0, 0, 0, 0);
+            }
+            continue;
+        }
         const XT* xp = static_cast<const XT*>(X.p) + b * X.sb + t * X.st + mine * X.sh + f0;
         const GT* gp = static_cast<const GT*>(G.p) + b * G.sb + t * G.st + mine * G.sh + f0;
-        XT* op = static_cast<XT*>(const_cast<void*>(O.p)) + b * O.sb + t * O.st + mine * O.sh + f0;
         for (int h = mine; h - mine < H; h += SIDE, xp += SIDE * X.sh, gp += SIDE * G.sh, op += SIDE * O.sh) {
             Grads<GT, E> g0, g1;
             uint4 r0 = make_uint4(0, 0, 0, 0), r1 = r0;

@@ -550,7 +550,8 @@ class RotaryBackward(_Rotary):
 
     def __call__(self, dq, dk, positions=None, first_position: int = 0,
                  stream: Optional[torch.cuda.Stream] = None) -> dict:
-        """Gradients of Rotary's inputs given those of its outputs, dq [B,Hq,T,d] and dk [B,Hk,T,d]."""
+        """Gradients of Rotary's inputs given those of its outputs, dq [B,Hq,T,d] and dk [B,Hk,T,d]; zero in rows without a
+        token."""
         return self._run(dq, dk, None, positions, first_position, None, None, None, None, stream)
 
     def _run(self, dq, dk, inputs, positions, first, wq, wk, dwq, dwk, stream):
@@ -585,7 +586,8 @@ class NormRotaryBackward(RotaryBackward):
 
     def __call__(self, dq, dk, q, k, positions=None, first_position: int = 0, q_weight=None, k_weight=None,
                  stream: Optional[torch.cuda.Stream] = None) -> dict:
-        """Gradients of NormRotary's inputs given those of its outputs, and its inputs."""
+        """Gradients of NormRotary's inputs given those of its outputs, and its inputs; zero in rows without a token, which add
+        nothing to those of the weights."""
         wq, wk = _weights(self, q_weight, k_weight)
         dw = [None if self.grads.get(n) is None else self.grads[n].data_ptr() for n in ("q_weight", "k_weight")]
         return self._run(dq, dk, (q, k), positions, first_position, wq, wk, *dw, stream)

@@ -1,0 +1,46 @@
+"""Head norms and rotary positions where they have edges: rows without a token in an object that is called again."""
+
+import numpy as np
+import pytest
+
+import layer_reference as ref
+from test_heads_gpu import BASE, make, values, weights
+from test_recurrence_gpu import DT, dev, near, sdl  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+# ---- rows without a token
+
+@pytest.mark.parametrize("t,gt", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("norm,weighted", [(None, False), ("rms", True), ("l2", False)])
+@pytest.mark.parametrize("B,T,Hq,Hk,d,rot", [(2, 7, 3, 1, 64, 16), (9, 1, 5, 0, 256, 256), (1, 40, 33, 7, 64, 0),
+                                             (2, 30, 4, 2, 128, 112)])
+def test_gradients_of_rows_without_a_token(sdl, t, gt, norm, weighted, B, T, Hq, Hk, d, rot):  # noqa: F811
+    """Zeros, whatever the buffers held: an input that is not used has no gradient. Other rows on every call."""
+    r = np.random.default_rng(41)
+    q, qv = values(Hq, B, T, d, t, r, True)
+    k, kv = values(Hk, B, T, d, t, r, False)
+    gq, gqv = values(Hq, B, T, d, gt, r, False)
+    gk, gkv = values(Hk, B, T, d, gt, r, True)
+    kw, wq, wk = weights(norm, weighted, Hk, d, r)
+    freq = BASE ** (-2 * np.arange(rot // 2) / max(rot, 1))
+    f = make(sdl, True, norm, weighted, t, B, T, Hq, Hk, d, rot, token_major=T % 2 == 0, grad_dtype=DT[gt])
+    for g in f.grads.values():
+        if g is not None:
+            g.fill_(7)
+    for part in range(3):                                        # the third call has no tokens at all
+        pos = np.arange(B * T).reshape(B, T) + 100
+        pos[(np.arange(B * T) % 2 == part).reshape(B, T) | (part == 2)] = -1 - part
+        p = torch.tensor(pos, dtype=torch.int32, device="cuda")
+        got = f(*((gq, gk, p) if norm is None else (gq, gk, q, k, p)), **kw)
+        live = (pos >= 0)[:, None, :, None]
+        for n, g, x, w in (("q", gqv, qv, wq), ("k", gkv, kv, wk)):
+            if g is None:
+                continue
+            dx, dw, edx, edw = ref.heads_grads(g, x, pos, freq, norm, 1e-6, w)
+            near(got[n], np.where(live, dx, 0.0), edx * live, t, n)
+            assert not got[n][torch.tensor(pos < 0, device="cuda")[:, None].expand(B, got[n].shape[1], T)].any()
+            if dw is not None:
+                near(got[n + "_weight"], dw, edw, "f32", n + "_weight")
