@@ -72,6 +72,7 @@ __global__ void __launch_bounds__(kThreads, SUMS ? 6 : 8) nr_backward_kernel(con
     int f0, f1;
     places<E>(j, a.rot, INTER, f0, f1);
     const int to_f1 = f1 - f0;
+    const bool turned = 2 * E * j < a.rot;                      // this lane's features are rotated
     if (NORM) {
         if (w == 0) fill_weights<E, L>(weight, is_q ? a.wq : a.wk, j, f0, f1);
         __syncthreads();
@@ -114,11 +115,16 @@ __global__ void __launch_bounds__(kThreads, SUMS ? 6 : 8) nr_backward_kernel(con
             float2 dy[E], z[E];
             g0.values(dy);
             g1.values(dy + E / 2);
-            Turn<E, L, INTER> by;
-            by.load(table[w], j, a.rot);
+            if (turned) {
+                Turn<E, L, INTER> by;
+                by.load(table[w], j);
+                by.template apply<true>(dy, z);
+            } else {
 #pragma unroll
-            for (int e = 0; e < E; ++e)                         // by minus the angles
-                z[e] = mul2(both(out_scale), fma2(dy[e], by.p(e), mul2(Turn<E, L, INTER>::other(dy, e), Turn<E, L, INTER>::minus(by.q(e)))));
+                for (int e = 0; e < E; ++e) z[e] = dy[e];
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) z[e] = mul2(both(out_scale), z[e]);
             if (NORM) {
                 float2 x[E];
                 unpack<XT>(r0, x);

@@ -32,6 +32,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<XT>::CTAS)) nr_forward_kernel
         __syncthreads();
     }
     const int to_f1 = f1 - f0;
+    const bool turned = 2 * E * j < a.rot;                      // this lane's features are rotated
     const long long items = (long long)a.B * a.T * split, step = (long long)gridDim.x * kWarps;
     for (long long it = (long long)blockIdx.x * kWarps + w; it < items; it += step) {
         const unsigned tok = split == 1 ? (unsigned)it : (unsigned)(it / split);
@@ -62,7 +63,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<XT>::CTAS)) nr_forward_kernel
 #pragma unroll 1
                 for (int i = lane; i < a.rot / 2; i += 32) angle<E, L>(a, pos, i, table[w]);
                 __syncwarp();
-                if (E == 4) by.load(table[w], j, a.rot);        // with larger pieces there are no registers to keep them
+                if (E == 4 && turned) by.load(table[w], j);     // with larger pieces there are no registers to keep them
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -78,10 +79,15 @@ __global__ void __launch_bounds__(kThreads, (Shape<XT>::CTAS)) nr_forward_kernel
 #pragma unroll
                     for (int e = 0; e < E; ++e) x[e] = mul2(x[e], weight_of<E, L>(wt, j, e));
                 }
-                if (E != 4) by.load(table[w], j, a.rot);
+                if (turned) {
+                    if (E != 4) by.load(table[w], j);
+                    by.template apply<false>(x, y);
+                } else {
 #pragma unroll
-                for (int e = 0; e < E; ++e)
-                    y[e] = mul2(both(scale), fma2(x[e], by.p(e), mul2(Turn<E, L, INTER>::other(x, e), by.q(e))));
+                    for (int e = 0; e < E; ++e) y[e] = x[e];
+                }
+#pragma unroll
+                for (int e = 0; e < E; ++e) y[e] = mul2(both(scale), y[e]);
                 if (h < end) {
                     XT* p = h < a.Hq ? oq + h * a.oq.sh : ok + (h - a.Hq) * a.ok.sh;
                     *reinterpret_cast<uint4*>(p) = pack<XT>(y);

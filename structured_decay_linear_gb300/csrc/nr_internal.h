@@ -99,16 +99,16 @@ template <int E, int L> __device__ __forceinline__ void angle(const Args& a, int
     row.s[place_of<E, L>(pair)] = s * a.rot_scale;
 }
 
-// What a lane's pairs are multiplied with: v[e] becomes v[e] p[e] + (the other members) q[e], the other members being v's other
-// piece, or with neighbours v[e]'s two numbers changed over. Lanes behind the rotated part have p = 1 and q = 0.
+// The rotation of a lane's pairs: v[e] becomes v[e] p[e] + (the other members) q[e], the other members being v's other piece, or
+// with neighbours v[e]'s two numbers changed over. Lanes behind the rotated part keep theirs: a factor of 0 would make NaN of a
+// partner that is not finite.
 template <int E, int L, bool INTER> struct Turn {
     float c[E], s[E];
-    __device__ __forceinline__ void load(const Angles& row, int j, int rot) {
-        const bool turned = 2 * E * j < rot;
+    __device__ __forceinline__ void load(const Angles& row, int j) {
 #pragma unroll
         for (int e = 0; e < E; e += 4) {
-            const float4 cs = turned ? *reinterpret_cast<const float4*>(row.c + (e * L + 4 * j)) : make_float4(1.f, 1.f, 1.f, 1.f);
-            const float4 sn = turned ? *reinterpret_cast<const float4*>(row.s + (e * L + 4 * j)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float4 cs = *reinterpret_cast<const float4*>(row.c + (e * L + 4 * j));
+            const float4 sn = *reinterpret_cast<const float4*>(row.s + (e * L + 4 * j));
             c[e] = cs.x; c[e + 1] = cs.y; c[e + 2] = cs.z; c[e + 3] = cs.w;
             s[e] = sn.x; s[e + 1] = sn.y; s[e + 2] = sn.z; s[e + 3] = sn.w;
         }
@@ -124,6 +124,11 @@ template <int E, int L, bool INTER> struct Turn {
         return e < E / 2 ? minus(v) : v;
     }
     static __device__ __forceinline__ float2 other(const float2 (&v)[E], int e) { return INTER ? over(v[e]) : v[(e + E / 2) % E]; }
+    // BACK: by minus the angles.
+    template <bool BACK> __device__ __forceinline__ void apply(const float2 (&v)[E], float2 (&to)[E]) const {
+#pragma unroll
+        for (int e = 0; e < E; ++e) to[e] = fma2(v[e], p(e), mul2(other(v, e), BACK ? minus(q(e)) : q(e)));
+    }
 };
 
 // Where feature f of a head stands in a row of weights, so that lanes side by side read side by side: pieces of four features,

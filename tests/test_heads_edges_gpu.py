@@ -1,4 +1,5 @@
-"""Head norms and rotary positions where they have edges: rows without a token in an object that is called again."""
+"""Head norms and rotary positions where they have edges: rows without a token in an object that is called again, values that are not
+finite beside the rotated part."""
 
 import numpy as np
 import pytest
@@ -44,3 +45,30 @@ def test_gradients_of_rows_without_a_token(sdl, t, gt, norm, weighted, B, T, Hq,
             assert not got[n][torch.tensor(pos < 0, device="cuda")[:, None].expand(B, got[n].shape[1], T)].any()
             if dw is not None:
                 near(got[n + "_weight"], dw, edw, "f32", n + "_weight")
+
+
+# ---- features that are not rotated
+
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("d,rot", [(64, 0), (64, 16), (64, 48), (128, 64), (256, 112), (32, 16)])
+def test_not_finite_beside_the_rotated_part(sdl, t, interleaved, d, rot):  # noqa: F811
+    """A feature behind the rotated part stays as it is and nobody else's, whatever its value, forwards and backwards."""
+    B, T, H = 1, 5, 3
+    r = np.random.default_rng(42)
+    kw = dict(interleaved=interleaved, q_scale=0.25, rot_scale=1.1)
+    f = make(sdl, False, None, False, t, B, T, H, 0, d, rot, **kw)
+    b = make(sdl, True, None, False, t, B, T, H, 0, d, rot, **kw)
+    x, _ = values(H, B, T, d, t, r, False)
+    clean, back = f(x, None, first_position=9)[0].clone(), b(x, None, first_position=9)["q"].clone()
+    assert torch.equal(clean[..., rot:], (0.25 * x[..., rot:].float()).to(x.dtype))      # one rounding of an exact product
+    for i in {rot, rot + 1, (rot + d) // 2, d - 9, d - 1}:
+        if i < rot:
+            continue
+        for value in (float("nan"), float("inf"), -float("inf")):
+            z = x.clone()
+            z[0, 1, 2, i] = value
+            for got, want in ((f(z, None, first_position=9)[0], clean), (b(z, None, first_position=9)["q"], back)):
+                want = want.clone()
+                want[0, 1, 2, i] = value
+                assert torch.equal(torch.nan_to_num(got, nan=12345.0), torch.nan_to_num(want, nan=12345.0)), (i, value)
