@@ -434,8 +434,8 @@ DPLR_API dplr_status dplr_gr_decode_step(const dplr_gr_desc* desc, int32_t n_slo
  * Pair i is (x_i, x_{i + rot/2}), or with `interleaved` the neighbours (x_{2i}, x_{2i+1}). The weights w are fp32 [d], one
  * for queries and one for keys, each nullable (ones); only with a norm.
  * Frequencies are given as 64-bit fractions of a turn, turns[i] = f_i / (2 pi) * 2^64 on the device (dplr_nr_turns), so that
- * an angle is off by at most 2^-32 turns (and a position times 2^-65) at any position. Positions are int32 on the device, element (b, t) at
- * positions[b pos_sb + t pos_st] (strides >= 0, 0 repeats), or, where positions is null, first_position + t. A row with
+ * an angle is off by less than 2^-27 turns (and a position times 2^-65) at any position. Positions are int32 on the device,
+ * element (b, t) at positions[b pos_sb + t pos_st] (strides >= 0, 0 repeats), or, where positions is null, first_position + t. A row with
  * a negative position holds no token: the forward leaves its outputs as they were; the backward makes its dq and dk zero, and
  * it adds nothing to weight gradients.
  * Tensors are dplr_hd_tensor with element strides along batch, head and token: q [B,Hq,T,d], k [B,Hk,T,d] (not looked at

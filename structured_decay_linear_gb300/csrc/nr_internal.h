@@ -11,7 +11,8 @@
 //   dx = r (o - x r^2 (o . x) / d)  (L2: without / d),   dw = sum over tokens and heads of z x r
 //
 // Angles: a frequency is a 64-bit fraction of a turn, so position times frequency in 64-bit integers is exact modulo whole
-// turns at every position; 32 bits of it go into sine and cosine.
+// turns at every position. It is rounded to 32 bits and its quarter turns are taken off in integers; the rest, up to an eighth of a
+// turn, is off by at most 2^-28 turns as a 32-bit float (the whole phase would be off by 2^-26).
 #pragma once
 
 #include "hd_internal.h"
@@ -93,10 +94,13 @@ template <int E, int L> __device__ __forceinline__ int place_of(int pair) {
 }
 template <int E, int L> __device__ __forceinline__ void angle(const Args& a, int pos, int pair, Angles& row) {
     const unsigned long long phase = (unsigned long long)(unsigned)pos * a.turns[pair];
+    const unsigned turn = (unsigned)((phase + 0x80000000u) >> 32);           // in units of 2^-32
+    const unsigned quarters = (turn + 0x20000000u) >> 30;                    // the nearest number of quarter turns, modulo 4
     float s, c;
-    sincospif((float)(int)(phase >> 32) * 0x1p-31f, &s, &c);
-    row.c[place_of<E, L>(pair)] = c * a.rot_scale;
-    row.s[place_of<E, L>(pair)] = s * a.rot_scale;
+    sincospif((float)(int)(turn - (quarters << 30)) * 0x1p-31f, &s, &c);     // what is left of it, up to an eighth of a turn
+    const float cosine = quarters & 1 ? s : c, sine = quarters & 1 ? c : s;
+    row.c[place_of<E, L>(pair)] = ((quarters + 1) & 2 ? -cosine : cosine) * a.rot_scale;
+    row.s[place_of<E, L>(pair)] = (quarters & 2 ? -sine : sine) * a.rot_scale;
 }
 
 // The rotation of a lane's pairs: v[e] becomes v[e] p[e] + (the other members) q[e], the other members being v's other piece, or

@@ -1,5 +1,5 @@
 """Head norms and rotary positions where they have edges: rows without a token in an object that is called again, values that are not
-finite beside the rotated part."""
+finite beside the rotated part, the angles' own precision."""
 
 import numpy as np
 import pytest
@@ -72,3 +72,28 @@ def test_not_finite_beside_the_rotated_part(sdl, t, interleaved, d, rot):  # noq
                 want = want.clone()
                 want[0, 1, 2, i] = value
                 assert torch.equal(torch.nan_to_num(got, nan=12345.0), torch.nan_to_num(want, nan=12345.0)), (i, value)
+
+
+# ---- angles
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_angles_alone(sdl, interleaved):  # noqa: F811
+    """Pairs (1, 0) come out as the cosine and the sine themselves: off by 2^-28 turns from the angle's conversion, 2^-33 from its
+    last bit and a position times 2^-65 from the frequency's, and by a unit in the last place of sine and cosine."""
+    from fractions import Fraction
+    pi = Fraction(314159265358979323846264338327950288419716939937510582097494, 10 ** 59)
+    T, d = 2000, 64
+    r = np.random.default_rng(43)
+    pos = np.concatenate([np.arange(500), r.integers(0, 2 ** 31, T - 502), [2 ** 31 - 1, 2 ** 30]])
+    freq = sdl.rotary_frequencies(d, BASE).numpy()
+    per = [Fraction(float(v)) / (2 * pi) for v in freq]
+    turn = np.array([[float(v * int(p) % 1) for v in per] for p in pos])
+    x = torch.zeros(1, 1, T, d, device="cuda")
+    u, v = (slice(0, d, 2), slice(1, d, 2)) if interleaved else (slice(0, d // 2), slice(d // 2, d))
+    x[..., u] = 1
+    f = sdl.Rotary(torch.float32, 1, T, 1, 0, d, freq, interleaved=interleaved)
+    y = f(x, None, torch.tensor(pos[None], dtype=torch.int32, device="cuda"))[0][0, 0].double().cpu().numpy()
+    angle = 2 * np.pi * (2.0 ** -28 + 2.0 ** -33 + pos[:, None] * 2.0 ** -65)
+    for got, want in ((y[:, u], np.cos(2 * np.pi * turn)), (y[:, v], np.sin(2 * np.pi * turn))):
+        off = np.abs(got - want) - 2.0 ** -23 * np.abs(want)
+        assert (off <= angle).all(), (off / angle).max()
