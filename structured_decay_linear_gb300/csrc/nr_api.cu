@@ -105,9 +105,12 @@ dplr_status dplr_nr_turns(const double* radians, int32_t n, uint64_t* turns) {
     // 1 / (2 pi) in two parts, so that a fraction of a turn keeps all of its 64 bits
     constexpr double kTurn = 0x1.45f306dc9c883p-3, kRest = -0x1.6b01ec5417056p-57;
     for (int32_t i = 0; i < n; ++i) {
-        const double t = radians[i] * kTurn, rest = std::fma(radians[i], kTurn, -t) + radians[i] * kRest;
-        const double part = t - std::floor(t);
-        turns[i] = static_cast<uint64_t>(std::ldexp(part, 64)) + static_cast<uint64_t>(std::llrint(std::ldexp(rest - std::floor(rest + 0.5), 64)));
+        // rounded here, whatever compilers for Arm make of a product and a difference
+        const double t = std::fma(radians[i], kTurn, 0.0), rest = std::fma(radians[i], kTurn, -t) + radians[i] * kRest;
+        // the fraction's bits below 2^-64 and the rest are rounded together
+        const double units = std::ldexp(t - std::floor(t), 64), whole = std::floor(units);
+        const double below = std::ldexp(rest - std::floor(rest + 0.5), 64) + (units - whole);
+        turns[i] = static_cast<uint64_t>(whole) + static_cast<uint64_t>(std::llrint(below));
     }
     return DPLR_OK;
 }
