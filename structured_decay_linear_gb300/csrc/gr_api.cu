@@ -225,7 +225,7 @@ dplr_status dplr_gr_forward_packed(const dplr_gr_desc* desc, int32_t R, int32_t 
     GR_MAP(map_of(desc, ry, desc->in_dtype, tile, &my));
     ForwardArgs a{};
     a.c = arg_of(desc, tile, workspace);
-    a.pool = h; a.total = starts + R; a.slot = token_slot; a.pos = token_pos; a.n_slots = n_slots;
+    a.pool = h; a.starts = starts; a.R = R; a.slot = token_slot; a.pos = token_pos; a.n_slots = n_slots;
     a.y = Out{ry.p, ry.sb, ry.st};
     GR_CUDA(launch_packed(types_of(desc), mx, mg, my, a, static_cast<cudaStream_t>(stream)));
     return DPLR_OK;

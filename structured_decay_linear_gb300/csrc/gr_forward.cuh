@@ -43,6 +43,16 @@ template <class XT, class GT> struct Shape {
 constexpr unsigned kStarts = 1u << 20, kHasState = 1u << 21, kEnds = 1u << 22;
 constexpr unsigned kSlotMask = kStarts - 1;
 
+// Whether a request's first row is `row`.
+__device__ __noinline__ bool is_first_row(const int* starts, int R, int row) {
+    int lo = 0, hi = R;                        // the first of starts that is not in front of the row lies in [lo, hi]
+    while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (starts[mid] < row) lo = mid + 1; else hi = mid;
+    }
+    return starts[lo] == row;
+}
+
 template <class XT, class GT, int GATE, int INPUT, bool PACKED>
 __global__ void __launch_bounds__(kThreads, kCtas)
 gr_forward_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mg,
@@ -65,7 +75,7 @@ gr_forward_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
     const int li = lane % 16, run = w * kRuns + lane / 16, t0 = run * L;    // two channels of a run of L tokens
     const Dims d = a.c.d;
     const int BG = d.B * d.G;
-    const int total = PACKED ? min(max(*a.total, 0), d.T) : d.T;
+    const int total = PACKED ? min(max(a.starts[a.R], 0), d.T) : d.T;
     const int NT = PACKED ? (total + TT - 1) / TT : d.NT;
     const unsigned tiles = (unsigned)NT * BG;
     const unsigned long long stamp = 4 * (__ldcg(&a.c.head->epoch) + 1);
@@ -98,7 +108,10 @@ gr_forward_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
             f = good ? (unsigned)me : 0u;
             if (me != before) f |= kStarts | (good && place > 0 ? kHasState : 0u);
             if (me != behind && good) f |= kEnds;
-            if (!good) a.c.head->status = DPLR_ERR_INVALID_ARG;
+            if (!good) {                       // neighbours may have the same slot
+                if (is_first_row(a.starts, a.R, row)) f |= kStarts;
+                a.c.head->status = DPLR_ERR_INVALID_ARG;
+            }
         }
         if (tid < TT) to[tid] = f;
     };

@@ -78,7 +78,8 @@ struct ForwardArgs {
     float* states;                 // [B][ceil(T / kStateStep)][D], nullable: the state in front of every kStateStep tokens
     // a ragged batch (B = 1, T rows): the pool of states and the plan's tables
     float* pool;                   // [n_slots][D]
-    const int* total;              // rows that hold tokens
+    const int* starts;             // [R + 1] requests' first rows; the last: rows that hold tokens
+    int R;
     const int* slot;               // [T]
     const int* pos;                // [T]
     int n_slots;

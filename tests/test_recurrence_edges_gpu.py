@@ -1,9 +1,10 @@
 """The elementwise gated recurrence where its arithmetic and its tables have edges: log-gates above 0, values that are not finite in
-ragged batches."""
+ragged batches, neighbouring requests without a state."""
 
 import numpy as np
 import pytest
 
+import layer_reference as ref
 from test_recurrence_gpu import DT, TYPES, dev, f32, near, ragged, sdl  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -144,3 +145,31 @@ def test_decays_are_not_below_zero(sdl, gate):  # noqa: F811
     S = torch.ones(1, D, device="cuda")
     f(torch.zeros_like(wide)[:, :D], wide[:, :D], S, torch.zeros(1, dtype=torch.int32, device="cuda"))
     assert not torch.signbit(S).any() and (S[0, -3:-1] == 0).all()
+
+
+# ---- requests without a state beside one another
+
+@pytest.mark.parametrize("xt,gt", TYPES)
+@pytest.mark.parametrize("bad", [-1, 1 << 19])
+@pytest.mark.parametrize("lengths", [[30, 40, 50], [300, 1, 2, 400, 0, 17]])
+def test_neighbours_without_a_state(sdl, xt, gt, bad, lengths):  # noqa: F811
+    """Rows whose slots have become the same number out of range: each of their requests starts from zero and leaves no state, also
+    where its positions go on where the request in front ends."""
+    D = 72
+    context = [7 if i == 0 else 7 + sum(lengths[:i]) for i in range(len(lengths))]
+    p, x, xv, g, gv, S0, slot = ragged(sdl, xt, gt, "log", "plain", lengths, context, D)
+    last = sum(lengths[:-1])
+    p.plan.token_slot[:last] = bad
+    S = f32(S0)
+    y = p(x, g, S)
+    assert p.device_status(clear=True) == sdl.dplr.DPLR_ERR_INVALID_ARG
+    at = 0
+    for i, n in enumerate(lengths):
+        if n:
+            h0 = S0[slot[i]:slot[i] + 1] if at >= last else None
+            w, bound, _ = ref.recurrence("log", "plain", xv[None, at:at + n], gv[None, at:at + n], h0)
+            near(y[at:at + n], w[0], bound[0], xt, f"request {i}")
+        at += n
+    near(S[slot[-1]], w[0, -1], bound[0, -1], "f32", "state")
+    others = [i for i in range(S0.shape[0]) if i != slot[-1]]
+    assert torch.equal(S[others], f32(S0)[others])
