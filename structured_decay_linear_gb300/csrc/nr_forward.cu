@@ -45,7 +45,6 @@ __global__ void __launch_bounds__(kThreads, (Shape<XT>::CTAS)) nr_forward_kernel
         XT* oq = static_cast<XT*>(const_cast<void*>(a.oq.p)) + b * a.oq.sb + t * a.oq.st + f0;
         XT* ok = static_cast<XT*>(const_cast<void*>(a.ok.p)) + b * a.ok.sb + t * a.ok.st + f0;
         const int first = part * per, end = min(H, first + per);
-        Turn<E, L, INTER> by;
         for (int h0 = first; h0 < end; h0 += U * SIDE) {
             uint4 r[U][2];
 #pragma unroll
@@ -63,7 +62,6 @@ __global__ void __launch_bounds__(kThreads, (Shape<XT>::CTAS)) nr_forward_kernel
 #pragma unroll 1
                 for (int i = lane; i < a.rot / 2; i += 32) angle<E, L>(a, pos, i, table[w]);
                 __syncwarp();
-                if (E == 4 && turned) by.load(table[w], j);     // with larger pieces there are no registers to keep them
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -80,7 +78,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<XT>::CTAS)) nr_forward_kernel
                     for (int e = 0; e < E; ++e) x[e] = mul2(x[e], weight_of<E, L>(wt, j, e));
                 }
                 if (turned) {
-                    if (E != 4) by.load(table[w], j);
+                    Turn<E, L, INTER> by;
+                    by.load(table[w], j);
                     by.template apply<false>(x, y);
                 } else {
 #pragma unroll
