@@ -126,9 +126,10 @@ cudaError_t launch_step(const Types& t, const StepArgs& a, cudaStream_t s);
 // One token's a, m = 1 - a and s, two channels at a time (Blackwell multiplies and adds pairs of fp32 numbers in one
 // instruction, and instructions issued are what a kernel of few bytes a channel runs out of first).
 //
-// Exponentials are 2^(g log2 e) of the hardware: off by 2 units of 2^-23 and by |g| 2^-25. In what enters a state, a h, that
-// is at most 2^-26 of h beyond the two units, whatever g. m is formed without a difference of nearly equal numbers: a gate
-// that forgets a thousandth a token would lose ten of its 24 bits.
+// Exponentials are 2^(g log2 e) of the hardware: off by 2 units of 2^-23 and by |g| 2^-23.7, from the product's rounding and the
+// constant's. In what enters a state, a h, that is at most 2^-25 of h beyond the two units for gates below 0 (|g| e^g is at most
+// 1 / e); gates above 0 have the factor |g|. m is formed without a difference of nearly equal numbers: a gate that forgets a
+// thousandth a token would lose ten of its 24 bits.
 // ---------------------------------------------------------------------------------------------------------------
 constexpr int kLog = DPLR_GR_LOG, kSigmoid = DPLR_GR_SIGMOID;
 constexpr int kPlain = DPLR_GR_PLAIN, kComplement = DPLR_GR_COMPLEMENT, kUnit = DPLR_GR_UNIT;

@@ -7,9 +7,9 @@
 // bits on every run. That many CTAs as an SM holds at once (6, for the sums' registers): more would each add sums.
 //
 // Measured (16 query and 4 key heads of 128, 16 bits, B4 T4096): 57 us with weights, 4.4 TB/s of q, k and the gradients;
-// with the forward in front 91 us, and without weights, where 8 CTAs an SM and many rounds of them are free, 80 us. Half the
-// issue slots are used and warps wait for memory most. The next heads' features asked for before these are done: 6 us more
-// (registers); 5 CTAs an SM: 3 us more.
+// with the forward in front 89 us, and without weights, where 8 CTAs an SM and many rounds of them are free, 75 us. With 32-bit
+// gradients coming in 62 us (5.4 TB/s), all in 32 bits 90 us (5.6). Less than half of the issue slots are used and warps wait for
+// memory most. The next heads' features asked for before these are done: 6 us more (registers); 5 CTAs an SM: 3 us more.
 #include "nr_internal.h"
 
 namespace dplr {

@@ -6,9 +6,11 @@
 // of them load, and then all compute (243 us where many rounds took 182, at B8 T8192, 32 heads of 128). A token's rows may
 // lie anywhere: heads before tokens on one side and after them on the other.
 //
-// Measured at that size (the copy rate is 6.79 TB/s): 176 us, 6.1 TB/s; without a norm 159 us, 6.8; heads of 64, 185 us; one
-// token for each of 64 rows 3.5 us, a launch's latency. A norm's instructions are what keeps it from the copy rate: 64% of
-// all issue slots. Rings of asynchronous copies, angles shared by a CTA's heads, larger CTAs: slower.
+// Measured at that size (the copy rate is 6.79 TB/s): 164 us, 6.5 TB/s; without a norm 157 us, 6.8; heads of 64, 166 us; in 32
+// bits with half the batch 172 us; one token for each of 64 rows 3.4 us, a launch's latency. A norm's instructions are what
+// keeps it from the copy rate: 63% of all issue slots. Rings of asynchronous copies, angles shared by a CTA's heads, larger CTAs:
+// slower. Lanes behind the rotated part go a way of their own (Turn); sines held in registers over a token's heads in 32 bits:
+// 192 instead of 179 us, with spills.
 #include "nr_internal.h"
 
 namespace dplr {
