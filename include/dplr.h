@@ -365,9 +365,9 @@ DPLR_API dplr_status dplr_hd_decode_step(const dplr_hd_desc* desc, int32_t n_slo
  * are not looked at). D is any number: rows whose channels do not fill 16 bytes are padded, and what is in the padding is
  * neither used nor kept. x, y, dy and dx are of in_dtype, g and dg of gate_dtype (in_dtype or DPLR_F32). States are fp32,
  * contiguous [B][D] or [n_slots][D]; everything is computed in fp32, 1 - a never as a difference of nearly equal numbers, and
- * y, dx and dg are rounded once. Log-gates above 0 grow the state as the formula says (a product of factors beyond 3e38 over some tokens makes
- * NaN), and DPLR_GR_UNIT has no value for them. Non-finite values stay in their channel and sequence, reach the tokens after
- * them, and may reach those before them in gradients. Results do not depend on timing.
+ * y, dx and dg are rounded once. Log-gates above 0 grow the state as the formula says (a product of factors beyond 3e38 over
+ * some tokens makes NaN), and DPLR_GR_UNIT has no value for them. Non-finite values stay in their channel and sequence, reach
+ * the tokens after them, and may reach those before them in gradients. Results do not depend on timing.
  * B*T < 2^31, T <= 2^30, D <= 2^25. Outputs must not overlap inputs or one another (one that starts where another tensor
  * does is refused), except that h_T may be h0. Workspaces are 256-byte aligned device memory of the caller: one for one descriptor,
  * zeroed once in front of its first use (again if it goes to another descriptor), not shared by calls that overlap; its
@@ -436,8 +436,8 @@ DPLR_API dplr_status dplr_gr_decode_step(const dplr_gr_desc* desc, int32_t n_slo
  * Frequencies are given as 64-bit fractions of a turn, turns[i] = f_i / (2 pi) * 2^64 on the device (dplr_nr_turns), so that
  * an angle is off by less than 2^-27 turns (and a position times 2^-65) at any position. Positions are int32 on the device,
  * element (b, t) at positions[b pos_sb + t pos_st] (strides >= 0, 0 repeats), or, where positions is null, first_position + t.
- * A row with a negative position holds no token: the forward leaves its outputs as they were; the backward makes its dq and dk zero, and
- * it adds nothing to weight gradients.
+ * A row with a negative position holds no token: the forward leaves its outputs as they were; the backward makes its dq and
+ * dk zero, and it adds nothing to weight gradients.
  * Tensors are dplr_hd_tensor with element strides along batch, head and token: q [B,Hq,T,d], k [B,Hk,T,d] (not looked at
  * with Hk = 0), outputs likewise with strides of their own, of in_dtype; data 16-byte aligned, strides positive multiples of
  * 16 bytes. fp32 arithmetic, one rounding; a head whose squares sum beyond 3e38 comes out as zeros, and one of zeros
